@@ -30,6 +30,12 @@
  *    call enqueues nothing and returns a non-zero gqa_status.
  *  - A context may be used from one stream at a time; calls on one context must not
  *    overlap on different streams (they share the context's workspace).
+ *  - Lengths that a call takes per sequence (prefix_len, kv_len, n_accept, path) are DEVICE
+ *    int32 arrays, so a captured graph can be replayed with other lengths.  They are checked
+ *    on the device: a sequence whose value is out of range is left out as the call says, the
+ *    others are computed, and the next attn_sync_status returns GQA_ERR_SHAPE.
+ *  - Memory that a call recorded into a CUDA graph uses stays allocated until attn_destroy,
+ *    also when a later call needs a larger workspace.
  *  - Kernels bound every wait on the device.  A wait that runs out records
  *    GQA_ERR_TIMEOUT in the context's device status word and the kernel returns; read
  *    it with attn_sync_status.
@@ -49,7 +55,7 @@ typedef struct gqa_ctx gqa_ctx; /* opaque */
 typedef enum {
     GQA_OK = 0,
     GQA_ERR_INVALID_ARG = 1, /* null pointer / null context / bad flag */
-    GQA_ERR_SHAPE = 2,       /* B, T, S_max, start_pos out of range */
+    GQA_ERR_SHAPE = 2,       /* B, T, S_max, start_pos (or a length read on the device) out of range */
     GQA_ERR_ALIGN = 3,       /* a device pointer is not 16-byte aligned */
     GQA_ERR_CUDA = 4,        /* a CUDA runtime call failed (see attn_last_cuda_error) */
     GQA_ERR_TIMEOUT = 5,     /* a bounded device-side wait ran out (device status word) */
@@ -202,9 +208,146 @@ gqa_status attn_decode_residual(gqa_ctx *ctx, const void *x, int B, int start_po
                                 gqa_stream_t stream);
 
 /*
+ * Drafted trees over a cache (speculative decoding).  A draft proposes T tokens per sequence
+ * that form a tree: each token continues the prefix or another drafted token.  One call
+ * verifies them all: the drafted tokens' keys and values lie behind the prefix, at positions
+ * prefix_len[b] .. prefix_len[b] + T - 1, and token t sees the prefix and the drafted tokens
+ * its mask row names (itself and its ancestors).
+ */
+#define GQA_MAX_TREE 256 /* drafted tokens per sequence */
+
+/*
+ * attn_tree_attention — the attention of T drafted tokens per sequence (head sharing, scores,
+ * scaling, mask, softmax, value product, merge): for token t and query head h of kv head g
+ *     h[b,t,h] = sum_s a_s v_s,  a = softmax over the visible s of q_r[b,t,h] . k_s / sqrt(128)
+ * where s runs over positions 0 .. prefix_len[b] - 1 and prefix_len[b] + j for the bits j set
+ * in row t of the mask.
+ *
+ * q_r     [B,T,512 n_kv] bf16: rotated queries (n_kv: the context's kv heads, 8 for the block).
+ * tree_mask [B,T,ceil(T/32)] 32-bit words: bit j & 31 of word j / 32 of row (b, t) lets token t
+ *         see drafted token j; bits at T and above are ignored.  A token without its own bit
+ *         does not see itself; a row with no visible key at all gets zeros (so sequences with
+ *         fewer drafted tokens are padded with empty rows).
+ * cache_k, cache_v  [B,S_max,n_kv,128] bf16, read only.  Positions that no row sees may hold
+ *         anything; the values of a drafted position that some row of the sequence sees have
+ *         to be finite also for the rows that do not see it.
+ * prefix_len [B] int32: 0 .. S_max - T.  Out of range: that sequence's rows of h are NaN and
+ *         attn_sync_status reports GQA_ERR_SHAPE.
+ * h       [B,T,512 n_kv] bf16 output, fully overwritten; must not overlap the inputs.
+ * Requires 1 <= B <= 1024, 1 <= T <= GQA_MAX_TREE, T <= S_max <= 1048576.
+ */
+gqa_status attn_tree_attention(gqa_ctx *ctx, const void *q_r, int B, int T, const unsigned *tree_mask,
+                               const void *cache_k, const void *cache_v, int S_max, const int *prefix_len,
+                               void *h, gqa_stream_t stream);
+
+/*
+ * attn_prefill_tree — the block for a drafted tree: Delta_attn of T drafted tokens per
+ * sequence.  Writes their K_r and V at positions prefix_len[b] + t, then attends as
+ * attn_tree_attention does.
+ *
+ * x       [B,T,4096] bf16 block input of the drafted tokens.
+ * R       [B,T,64,2] fp32: (cos, sin) for each token's own position (prefix_len[b] + its depth
+ *         in the tree).
+ * delta   [B,T,4096] fp32 output, fully overwritten (NaN for a sequence whose prefix_len is
+ *         out of range; its cache is not written).
+ * Other arguments, limits and the workspace as attn_tree_attention and attn_prefill.  On a
+ * shard context delta is the shard's partial sum.
+ * attn_prefill_tree_residual — the same in the residual form (see attn_prefill_residual).
+ */
+gqa_status attn_prefill_tree(gqa_ctx *ctx, const void *x, int B, int T, const float *R, const unsigned *tree_mask,
+                             void *cache_k, void *cache_v, int S_max, const int *prefix_len, float *delta,
+                             gqa_stream_t stream);
+gqa_status attn_prefill_tree_residual(gqa_ctx *ctx, const void *x, int B, int T, const float *R,
+                                      const unsigned *tree_mask, void *cache_k, void *cache_v, int S_max,
+                                      const int *prefix_len, float *h_out, gqa_stream_t stream);
+
+/*
+ * attn_cache_commit — keep the accepted path of a verified tree: positions prefix_len[b] +
+ * path[b,i] of both caches move to prefix_len[b] + i for i < n_accept[b], in place.
+ *
+ * path    [B,T] int32: drafted tokens of the accepted path, strictly increasing, each below T;
+ *         entries from n_accept[b] on are not read.
+ * n_accept [B] int32: 0 .. T.
+ * new_len [B] int32 output: prefix_len[b] + n_accept[b]; may be the array prefix_len itself,
+ *         but not overlap it otherwise, nor path or n_accept.
+ * A sequence whose prefix_len, n_accept or path is out of range (or not increasing) is left as
+ * it is, its new_len is its prefix_len, and attn_sync_status reports GQA_ERR_SHAPE.  Positions
+ * behind the new length keep what they hold.  Limits as attn_tree_attention.
+ */
+gqa_status attn_cache_commit(gqa_ctx *ctx, void *cache_k, void *cache_v, int B, int S_max, int T,
+                             const int *prefix_len, const int *path, const int *n_accept, int *new_len,
+                             gqa_stream_t stream);
+
+/*
+ * Eviction by accumulated attention weight.  A decode step adds the softmax weight that each
+ * key received, summed over the query heads of its kv head, to a running sum; when a cache has
+ * grown past its budget, each kv head keeps its first and its most recent positions and the
+ * heaviest of the others.  Keys keep the rotation of the position they were written for.
+ */
+
+/*
+ * attn_decode_attention_weights — decode attention (one query position per sequence over keys
+ * 0 .. kv_len[b] - 1) that accumulates the key weights:
+ *     weights[b,g,s] += sum over the 4 query heads of kv head g of their softmax weight on s.
+ *
+ * q_r     [B,512 n_kv] bf16; cache_k, cache_v [B,S_max,n_kv,128] bf16, read only.
+ * kv_len  [B] int32: 0 .. S_max (0: h is zero).  Out of range: the sequence's h is NaN, its
+ *         weights stay as they are, and attn_sync_status reports GQA_ERR_SHAPE.
+ * weights [B,n_kv,S_max] fp32, updated at s < kv_len[b]; the other entries are not touched.
+ * h       [B,512 n_kv] bf16 output.
+ * Requires 1 <= B <= 1024, 1 <= S_max <= 1048576.
+ */
+gqa_status attn_decode_attention_weights(gqa_ctx *ctx, const void *q_r, const void *cache_k, const void *cache_v,
+                                         int B, int S_max, const int *kv_len, float *weights, void *h,
+                                         gqa_stream_t stream);
+
+/*
+ * attn_decode_weights — the block for one new token per sequence, at cache position kv_len[b]
+ * (0 .. S_max - 1): writes its K_r and V there, attends over keys 0 .. kv_len[b] and
+ * accumulates their weights.  kv_len itself is not changed.
+ *
+ * x [B,1,4096] bf16; R [B,64,2] fp32: rotation of each sequence's new token (its position in
+ * the text, which an eviction makes larger than kv_len[b]); delta [B,1,4096] fp32.
+ * attn_decode_weights_residual — the same in the residual form (see attn_decode_residual).
+ */
+gqa_status attn_decode_weights(gqa_ctx *ctx, const void *x, int B, const float *R, void *cache_k, void *cache_v,
+                               int S_max, const int *kv_len, float *weights, float *delta, gqa_stream_t stream);
+gqa_status attn_decode_weights_residual(gqa_ctx *ctx, const void *x, int B, const float *R, void *cache_k,
+                                        void *cache_v, int S_max, const int *kv_len, float *weights, float *h_out,
+                                        gqa_stream_t stream);
+
+/*
+ * attn_cache_evict — cut every sequence to at most `budget` positions per kv head.  A sequence
+ * with kv_len[b] <= budget keeps all its positions.  Otherwise each kv head keeps positions
+ * 0 .. n_first - 1, the last n_recent, and of those between the budget - n_first - n_recent with
+ * the largest weight (of equal weights the lower positions; a NaN counts less than any number).
+ * What is kept moves to the front in ascending order, and its weights with it.
+ *
+ * cache_k, cache_v [B,S_max,n_kv,128] bf16, weights [B,n_kv,S_max] fp32, kv_len [B] int32.
+ * out_k, out_v [B,S_out,n_kv,128], out_weights [B,n_kv,S_out]: the cut caches.  In place:
+ *         the three inputs themselves with S_out = S_max; then positions from the new length
+ *         on keep what they hold, and weights from the new length to the old one become 0.
+ *         Otherwise no output may overlap an input, positions of out_k and out_v from the new
+ *         length on are not written, and out_weights is 0 there.
+ * kept    [B,n_kv,budget] int32 output: the position that each kept one had; -1 past the new
+ *         length.
+ * new_len [B] int32 output: min(kv_len[b], budget); may be the array kv_len itself, but not
+ *         overlap it otherwise.
+ * Requires 1 <= budget <= S_out, n_first, n_recent >= 0, n_first + n_recent <= budget, and the
+ * limits of attn_decode_attention_weights.  A kv_len outside 0 .. S_max: the sequence's caches
+ * and weights stay as they are, its kept is -1, its new_len 0, and attn_sync_status reports
+ * GQA_ERR_SHAPE.
+ */
+gqa_status attn_cache_evict(gqa_ctx *ctx, const void *cache_k, const void *cache_v, const float *weights, int B,
+                            int S_max, const int *kv_len, int budget, int n_first, int n_recent, void *out_k,
+                            void *out_v, float *out_weights, int S_out, int *kept, int *new_len,
+                            gqa_stream_t stream);
+
+/*
  * attn_sync_status — synchronise `stream`, then read and clear the context's device
  * status word.  Returns GQA_OK, GQA_ERR_TIMEOUT (a bounded device wait ran out in some
- * earlier call) or GQA_ERR_CUDA (the synchronisation itself failed).
+ * earlier call), GQA_ERR_SHAPE (a per-sequence length or path of some earlier call was out
+ * of range) or GQA_ERR_CUDA (the synchronisation itself failed).
  */
 gqa_status attn_sync_status(gqa_ctx *ctx, gqa_stream_t stream);
 
@@ -227,7 +370,11 @@ enum {
     GQA_KERNEL_OUT_GEMM = 4,       /* Delta = H W_O^T (many tokens) */
     GQA_KERNEL_OUT_SPLITK = 5,     /* the same for few tokens */
     GQA_KERNEL_RMS_NORM = 6,       /* 1 / rms of each token row (residual form only) */
-    GQA_KERNEL_KINDS = 7
+    GQA_KERNEL_CACHE_ATTN = 7,     /* tree attention / decode attention with key weights */
+    GQA_KERNEL_CACHE_COMMIT = 8,   /* accepted path moved behind the prefix */
+    GQA_KERNEL_EVICT_SELECT = 9,   /* positions that an eviction keeps */
+    GQA_KERNEL_EVICT_MOVE = 10,    /* their keys and values moved */
+    GQA_KERNEL_KINDS = 11
 };
 
 /*

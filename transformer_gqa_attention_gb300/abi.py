@@ -22,11 +22,14 @@ EXPORTED = ("attn_create", "attn_create_shard", "attn_prefill", "attn_decode", "
             "attn_profile_begin", "attn_profile_end", "attn_debug_inject_timeout",
             "attn_debug_pair_schedule", "attn_debug_exp2", "attn_decode_attention_noalloc",
             "attn_decode_attention_noalloc_status", "attn_decode_attention_noalloc_debug_inject_timeout",
+           "attn_tree_attention", "attn_prefill_tree", "attn_prefill_tree_residual", "attn_cache_commit",
+           "attn_decode_attention_weights", "attn_decode_weights", "attn_decode_weights_residual",
+           "attn_cache_evict",
             "attn_destroy", "attn_strerror", "attn_last_cuda_error")
 
 # Kernel kinds of attn_profile_end (GQA_KERNEL_* in include/gqa_attn.h).
 KERNEL_KINDS = ("qkv_gemm", "qkv_splitk", "flash_prefill", "decode_attn", "out_gemm", "out_splitk",
-                "rms_norm")
+                "rms_norm", "cache_attn", "cache_commit", "evict_select", "evict_move")
 
 _lib = None
 
@@ -86,6 +89,20 @@ def lib() -> ctypes.CDLL:
     L.attn_decode_attention_noalloc_status.restype = i32
     L.attn_decode_attention_noalloc_debug_inject_timeout.argtypes = []
     L.attn_decode_attention_noalloc_debug_inject_timeout.restype = i32
+    L.attn_tree_attention.argtypes = [vp, vp, i32, i32, vp, vp, vp, i32, vp, vp, vp]
+    L.attn_tree_attention.restype = i32
+    for name in ("attn_prefill_tree", "attn_prefill_tree_residual"):
+        getattr(L, name).argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, i32, vp, vp, vp]
+        getattr(L, name).restype = i32
+    L.attn_cache_commit.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    L.attn_cache_commit.restype = i32
+    L.attn_decode_attention_weights.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, vp]
+    L.attn_decode_attention_weights.restype = i32
+    for name in ("attn_decode_weights", "attn_decode_weights_residual"):
+        getattr(L, name).argtypes = [vp, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp]
+        getattr(L, name).restype = i32
+    L.attn_cache_evict.argtypes = [vp, vp, vp, vp, i32, i32, vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp]
+    L.attn_cache_evict.restype = i32
     L.attn_destroy.argtypes = [vp]
     L.attn_destroy.restype = None
     L.attn_strerror.argtypes = [i32]
@@ -236,6 +253,68 @@ def attn_decode_attention_noalloc_debug_inject_timeout():
     """Arm the one-shot failure-path hook for the next allocation-free decode call."""
     _check("attn_decode_attention_noalloc_debug_inject_timeout",
            lib().attn_decode_attention_noalloc_debug_inject_timeout())
+
+
+def attn_tree_attention(ctx, q_r, B, T, tree_mask, cache_k, cache_v, S_max, prefix_len, h, stream=None):
+    """Attention of T drafted tokens per sequence over its prefix and their own ancestors:
+    tree_mask [B, T, ceil(T/32)] 32-bit words, prefix_len [B] int32, both on the device."""
+    _check("attn_tree_attention",
+           lib().attn_tree_attention(ctx, _ptr(q_r), int(B), int(T), _ptr(tree_mask), _ptr(cache_k), _ptr(cache_v),
+                                     int(S_max), _ptr(prefix_len), _ptr(h), _stream(stream)))
+
+
+def attn_prefill_tree(ctx, x, B, T, R, tree_mask, cache_k, cache_v, S_max, prefix_len, delta, stream=None):
+    """The block for T drafted tokens per sequence, written behind prefix_len[b]; R [B, T, 64, 2]."""
+    _check("attn_prefill_tree",
+           lib().attn_prefill_tree(ctx, _ptr(x), int(B), int(T), _ptr(R), _ptr(tree_mask), _ptr(cache_k),
+                                   _ptr(cache_v), int(S_max), _ptr(prefix_len), _ptr(delta), _stream(stream)))
+
+
+def attn_prefill_tree_residual(ctx, x, B, T, R, tree_mask, cache_k, cache_v, S_max, prefix_len, h_out, stream=None):
+    _check("attn_prefill_tree_residual",
+           lib().attn_prefill_tree_residual(ctx, _ptr(x), int(B), int(T), _ptr(R), _ptr(tree_mask), _ptr(cache_k),
+                                            _ptr(cache_v), int(S_max), _ptr(prefix_len), _ptr(h_out),
+                                            _stream(stream)))
+
+
+def attn_cache_commit(ctx, cache_k, cache_v, B, S_max, T, prefix_len, path, n_accept, new_len, stream=None):
+    """Move drafted positions path[b, :n_accept[b]] behind the prefix, in place; new_len[b] =
+    prefix_len[b] + n_accept[b] (new_len may be prefix_len)."""
+    _check("attn_cache_commit",
+           lib().attn_cache_commit(ctx, _ptr(cache_k), _ptr(cache_v), int(B), int(S_max), int(T), _ptr(prefix_len),
+                                   _ptr(path), _ptr(n_accept), _ptr(new_len), _stream(stream)))
+
+
+def attn_decode_attention_weights(ctx, q_r, cache_k, cache_v, B, S_max, kv_len, weights, h, stream=None):
+    """Decode attention over keys 0 .. kv_len[b]-1; weights [B, n_kv, S_max] fp32 += each key's
+    weight, summed over the kv head's query heads."""
+    _check("attn_decode_attention_weights",
+           lib().attn_decode_attention_weights(ctx, _ptr(q_r), _ptr(cache_k), _ptr(cache_v), int(B), int(S_max),
+                                               _ptr(kv_len), _ptr(weights), _ptr(h), _stream(stream)))
+
+
+def attn_decode_weights(ctx, x, B, R, cache_k, cache_v, S_max, kv_len, weights, delta, stream=None):
+    """The block for one new token per sequence, written at position kv_len[b]; R [B, 64, 2]."""
+    _check("attn_decode_weights",
+           lib().attn_decode_weights(ctx, _ptr(x), int(B), _ptr(R), _ptr(cache_k), _ptr(cache_v), int(S_max),
+                                     _ptr(kv_len), _ptr(weights), _ptr(delta), _stream(stream)))
+
+
+def attn_decode_weights_residual(ctx, x, B, R, cache_k, cache_v, S_max, kv_len, weights, h_out, stream=None):
+    _check("attn_decode_weights_residual",
+           lib().attn_decode_weights_residual(ctx, _ptr(x), int(B), _ptr(R), _ptr(cache_k), _ptr(cache_v),
+                                              int(S_max), _ptr(kv_len), _ptr(weights), _ptr(h_out),
+                                              _stream(stream)))
+
+
+def attn_cache_evict(ctx, cache_k, cache_v, weights, B, S_max, kv_len, budget, n_first, n_recent, out_k, out_v,
+                     out_weights, S_out, kept, new_len, stream=None):
+    """Cut every sequence to at most `budget` positions per kv head by accumulated weight; the
+    outputs may be the inputs (in place) or caches of their own length S_out."""
+    _check("attn_cache_evict",
+           lib().attn_cache_evict(ctx, _ptr(cache_k), _ptr(cache_v), _ptr(weights), int(B), int(S_max),
+                                  _ptr(kv_len), int(budget), int(n_first), int(n_recent), _ptr(out_k), _ptr(out_v),
+                                  _ptr(out_weights), int(S_out), _ptr(kept), _ptr(new_len), _stream(stream)))
 
 
 def attn_destroy(ctx):

@@ -1,0 +1,193 @@
+// cache_abi.cu — the entry points of include/gqa_attn.h that work on a cache directly: tree
+// attention, decode attention with accumulated key weights, commit of an accepted path and
+// eviction by weight.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "cache_call.h"
+#include "ctx.h"
+#include "gqa_attn.h"
+#include "launch.h"
+#include "params.h"
+
+using namespace gqa;
+
+gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t s) {
+  CacheAttnParams p{};
+  p.B = a.B;
+  p.T = a.T;
+  p.S_max = a.S_max;
+  p.n_kv = c->n_kv;
+  p.n_new = a.n_new;
+  p.mask = a.mask;
+  p.kv_len = a.kv_len;
+  p.q = a.q;
+  p.k = a.cache_k;
+  p.v = a.cache_v;
+  p.h = a.h;
+  p.weights = a.weights;
+  p.status = c->status;
+  p.scale_log2 = kScaleLog2;
+  ProfScope ps(c, GQA_KERNEL_CACHE_ATTN, s);
+  GQA_CUDA(launch_cache_attn(p, s));
+  return GQA_OK;
+}
+
+namespace {
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+extern "C" {
+
+gqa_status attn_tree_attention(gqa_ctx* c, const void* q_r, int B, int T, const unsigned* tree_mask,
+                               const void* cache_k, const void* cache_v, int S_max, const int* prefix_len, void* h,
+                               gqa_stream_t stream) {
+  if (!c || !q_r || !tree_mask || !cache_k || !cache_v || !prefix_len || !h) return GQA_ERR_INVALID_ARG;
+  if (B < 1 || B > kDecodeMaxBatch || T < 1 || T > GQA_MAX_TREE || S_max < 1 || S_max > kMaxSMax || T > S_max)
+    return GQA_ERR_SHAPE;
+  if (!aligned16(q_r) || !aligned16(tree_mask) || !aligned16(cache_k) || !aligned16(cache_v) ||
+      !aligned16(prefix_len) || !aligned16(h))
+    return GQA_ERR_ALIGN;
+  gqa_status st = check_device(c);
+  if (st != GQA_OK) return st;
+  CallRange range("gqa.attn_tree_attention");
+  CacheAttnCall a{};
+  a.B = B;
+  a.T = T;
+  a.n_new = T;
+  a.S_max = S_max;
+  a.mask = tree_mask;
+  a.kv_len = prefix_len;
+  a.q = q_r;
+  a.cache_k = cache_k;
+  a.cache_v = cache_v;
+  a.h = h;
+  return run_cache_attn(c, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+gqa_status attn_decode_attention_weights(gqa_ctx* c, const void* q_r, const void* cache_k, const void* cache_v, int B,
+                                         int S_max, const int* kv_len, float* weights, void* h,
+                                         gqa_stream_t stream) {
+  if (!c || !q_r || !cache_k || !cache_v || !kv_len || !weights || !h) return GQA_ERR_INVALID_ARG;
+  if (B < 1 || B > kDecodeMaxBatch || S_max < 1 || S_max > kMaxSMax) return GQA_ERR_SHAPE;
+  if (!aligned16(q_r) || !aligned16(cache_k) || !aligned16(cache_v) || !aligned16(kv_len) || !aligned16(weights) ||
+      !aligned16(h))
+    return GQA_ERR_ALIGN;
+  gqa_status st = check_device(c);
+  if (st != GQA_OK) return st;
+  CallRange range("gqa.attn_decode_attention_weights");
+  CacheAttnCall a{};
+  a.B = B;
+  a.T = 1;
+  a.n_new = 0;
+  a.S_max = S_max;
+  a.kv_len = kv_len;
+  a.q = q_r;
+  a.cache_k = cache_k;
+  a.cache_v = cache_v;
+  a.h = h;
+  a.weights = weights;
+  return run_cache_attn(c, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+gqa_status attn_cache_commit(gqa_ctx* c, void* cache_k, void* cache_v, int B, int S_max, int T, const int* prefix_len,
+                             const int* path, const int* n_accept, int* new_len, gqa_stream_t stream) {
+  if (!c || !cache_k || !cache_v || !prefix_len || !path || !n_accept || !new_len) return GQA_ERR_INVALID_ARG;
+  if (B < 1 || B > kDecodeMaxBatch || T < 1 || T > GQA_MAX_TREE || S_max < 1 || S_max > kMaxSMax || T > S_max)
+    return GQA_ERR_SHAPE;
+  if (!aligned16(cache_k) || !aligned16(cache_v) || !aligned16(prefix_len) || !aligned16(path) ||
+      !aligned16(n_accept) || !aligned16(new_len))
+    return GQA_ERR_ALIGN;
+  const size_t lens = static_cast<size_t>(B) * sizeof(int);
+  if ((new_len != prefix_len && overlap(new_len, lens, prefix_len, lens)) || overlap(new_len, lens, n_accept, lens) ||
+      overlap(new_len, lens, path, lens * T))
+    return GQA_ERR_INVALID_ARG;
+  gqa_status st = check_device(c);
+  if (st != GQA_OK) return st;
+  CallRange range("gqa.attn_cache_commit");
+  CommitParams p{};
+  p.B = B;
+  p.S_max = S_max;
+  p.T = T;
+  p.n_kv = c->n_kv;
+  p.k = cache_k;
+  p.v = cache_v;
+  p.prefix_len = prefix_len;
+  p.path = path;
+  p.n_accept = n_accept;
+  p.new_len = new_len;
+  p.status = c->status;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(c, GQA_KERNEL_CACHE_COMMIT, s);
+  GQA_CUDA(launch_cache_commit(p, s));
+  return GQA_OK;
+}
+
+gqa_status attn_cache_evict(gqa_ctx* c, const void* cache_k, const void* cache_v, const float* weights, int B,
+                            int S_max, const int* kv_len, int budget, int n_first, int n_recent, void* out_k,
+                            void* out_v, float* out_weights, int S_out, int* kept, int* new_len,
+                            gqa_stream_t stream) {
+  if (!c || !cache_k || !cache_v || !weights || !kv_len || !out_k || !out_v || !out_weights || !kept || !new_len)
+    return GQA_ERR_INVALID_ARG;
+  if (B < 1 || B > kDecodeMaxBatch || S_max < 1 || S_max > kMaxSMax || S_out < 1 || S_out > kMaxSMax || budget < 1 ||
+      budget > S_out || n_first < 0 || n_recent < 0 || static_cast<long long>(n_first) + n_recent > budget)
+    return GQA_ERR_SHAPE;
+  if (!aligned16(cache_k) || !aligned16(cache_v) || !aligned16(weights) || !aligned16(kv_len) || !aligned16(out_k) ||
+      !aligned16(out_v) || !aligned16(out_weights) || !aligned16(kept) || !aligned16(new_len))
+    return GQA_ERR_ALIGN;
+  // either every output is its input (in place) or none overlaps any of them
+  const bool in_place = out_k == cache_k && out_v == cache_v && out_weights == weights && S_out == S_max;
+  const void* ins[3] = {cache_k, cache_v, weights};
+  const void* outs[3] = {out_k, out_v, out_weights};
+  for (int i = 0; i < 3 && !in_place; ++i)
+    for (int j = 0; j < 3; ++j)
+      if (ins[i] == outs[j]) return GQA_ERR_INVALID_ARG;
+  const size_t lens = static_cast<size_t>(B) * sizeof(int);
+  if (new_len != kv_len && overlap(new_len, lens, kv_len, lens)) return GQA_ERR_INVALID_ARG;
+  gqa_status st = check_device(c);
+  if (st != GQA_OK) return st;
+  const size_t unit = static_cast<size_t>(B) * c->n_kv;  // (sequence, kv head) pairs
+  const size_t per_pos[3] = {256, 256, 4};               // bytes of one of their positions
+  for (int i = 0; i < 3 && !in_place; ++i)
+    for (int j = 0; j < 3; ++j)
+      if (overlap(ins[i], unit * S_max * per_pos[i], outs[j], unit * S_out * per_pos[j])) return GQA_ERR_INVALID_ARG;
+  CallRange range("gqa.attn_cache_evict");
+  EvictParams p{};
+  p.B = B;
+  p.S_max = S_max;
+  p.S_out = S_out;
+  p.n_kv = c->n_kv;
+  p.budget = budget;
+  p.n_first = n_first;
+  p.n_recent = n_recent;
+  p.in_place = in_place ? 1 : 0;
+  p.k = cache_k;
+  p.v = cache_v;
+  p.weights = weights;
+  p.kv_len = kv_len;
+  p.out_k = out_k;
+  p.out_v = out_v;
+  p.out_weights = out_weights;
+  p.kept = kept;
+  p.new_len = new_len;
+  p.status = c->status;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  {
+    ProfScope ps(c, GQA_KERNEL_EVICT_SELECT, s);
+    GQA_CUDA(launch_evict_select(p, s));
+  }
+  {
+    ProfScope ps(c, GQA_KERNEL_EVICT_MOVE, s);
+    GQA_CUDA(launch_evict_move(p, s));
+  }
+  return GQA_OK;
+}
+
+}  // extern "C"

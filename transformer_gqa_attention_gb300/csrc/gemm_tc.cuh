@@ -70,6 +70,7 @@ __device__ __forceinline__ void stage_chunk(float* stage, int lane, const uint32
 // 8k + lane/4 of the warp's 32 rows, columns 8 (lane & 3) .. +7 of the chunk.
 struct QkvRows {
   int m[4], b[4], t[4];
+  int pos[4];   // cache position of the row (-1: not written)
   float rs[4];  // row scale (1 / rms of the token row under attention_norm; 1 for the block alone)
 };
 
@@ -81,6 +82,11 @@ __device__ __forceinline__ QkvRows qkv_rows(const GemmParams& p, int lane, int m
     const int mc = min(q.m[k], p.M - 1);
     q.b[k] = mc / p.T;
     q.t[k] = mc - q.b[k] * p.T;
+    q.pos[k] = p.start_pos + q.t[k];
+    if (p.seq_start) {
+      q.pos[k] = q.t[k];  // offset from the sequence's start, added by qkv_row_starts
+      q.t[k] = mc;        // R has a row per token
+    }
     q.rs[k] = 1.f;
   }
   return q;
@@ -92,6 +98,17 @@ __device__ __forceinline__ void qkv_row_scales(const GemmParams& p, QkvRows& q) 
   if (!p.row_scale) return;
 #pragma unroll
   for (int k = 0; k < 4; ++k) q.rs[k] = __ldg(p.row_scale + min(q.m[k], p.M - 1));
+}
+
+// The rows' cache positions where every sequence has its own start.  The starts may come from the
+// previous kernel: read, like the row scales, after the accumulator wait.
+__device__ __forceinline__ void qkv_row_starts(const GemmParams& p, QkvRows& q) {
+  if (!p.seq_start) return;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int start = __ldcg(p.seq_start + q.b[k]);
+    q.pos[k] = start >= 0 && start <= p.S_max - p.T ? start + q.pos[k] : -1;
+  }
 }
 
 // (cos, sin) of the 4 RoPE pairs a lane rotates in chunk-column block cc (0..3) of a head
@@ -140,7 +157,8 @@ __device__ __forceinline__ void store_qkv_chunk(const GemmParams& p, const float
     if (col0 < k_col0) {
       dst = static_cast<__nv_bfloat16*>(p.out0) + static_cast<size_t>(q.m[k]) * p.q_cols + col;
     } else {
-      const size_t cache_row = static_cast<size_t>(q.b[k]) * p.S_max + p.start_pos + q.t[k];
+      if (q.pos[k] < 0) continue;
+      const size_t cache_row = static_cast<size_t>(q.b[k]) * p.S_max + q.pos[k];
       dst = static_cast<__nv_bfloat16*>(is_v ? p.out2 : p.out1) + cache_row * p.kv_cols + (col - (is_v ? v_col0 : k_col0));
     }
     *reinterpret_cast<uint4*>(dst) = w;
@@ -389,7 +407,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[ab], (lt >> 1) & 1, abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
-      if constexpr (EPI == kQkvRope) qkv_row_scales(p, qr);
+      if constexpr (EPI == kQkvRope) {
+        qkv_row_scales(p, qr);
+        qkv_row_starts(p, qr);
+      }
       const uint32_t t_row = tmem_base + lane_off + ab * 256;
 #pragma unroll
       for (int cp = 0; cp < 4; ++cp) {
@@ -595,7 +616,7 @@ __global__ void __launch_bounds__(192, (STAGES <= 5 ? 2 : 1))
         const int tok = t_lo + (warp - 2) + 4 * j;
         cs[j] = make_float4(1.f, 0.f, 1.f, 0.f);  // value features: not rotated
         if (rope && tok < t_hi) {
-          const int t = tok - (tok / p.T) * p.T;
+          const int t = p.seq_start ? tok : tok - (tok / p.T) * p.T;
           cs[j] = __ldg(reinterpret_cast<const float4*>(p.R + (static_cast<size_t>(t) * 64 + ((m & 127) >> 1)) * 2));
         }
       }
@@ -691,7 +712,9 @@ __global__ void __launch_bounds__(192, (STAGES <= 5 ? 2 : 1))
         } else {
           const int v_col0 = p.q_cols + p.kv_cols;
           const bool is_v = m >= v_col0;
-          const size_t crow = static_cast<size_t>(b) * p.S_max + p.start_pos + t;
+          const int start = p.seq_start ? __ldcg(p.seq_start + b) : p.start_pos;
+          if (start < 0 || start > p.S_max - p.T) continue;  // only a sequence's own start can be
+          const size_t crow = static_cast<size_t>(b) * p.S_max + start + t;
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(is_v ? p.fin2 : p.fin1) + crow * p.kv_cols +
                                     (m - (is_v ? v_col0 : p.q_cols))) = o;
         }

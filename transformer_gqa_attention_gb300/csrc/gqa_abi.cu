@@ -1,6 +1,5 @@
-// gqa_abi.cu — the C ABI declared in include/gqa_attn.h: argument validation, the
-// context (packed weights, status word, workspace), TMA descriptors and the launch
-// sequence of one block forward.
+// gqa_abi.cu — the block's entry points of include/gqa_attn.h: argument validation, context
+// creation, TMA descriptors and the launch sequence of one block forward.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -8,48 +7,15 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <cstring>
-#include <mutex>
-#include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "cache_call.h"
+#include "ctx.h"
 #include "gqa_attn.h"
 #include "launch.h"
 #include "pair_sched.h"
 #include "params.h"
 
 using namespace gqa;
-
-struct gqa_ctx {
-  int device = -1;
-  int num_sms = 0;
-  int pair_clusters = 0;  // co-resident 2-CTA clusters of the pair GEMM
-  // kv groups of this context: 8 for the whole block, G < 8 for a head shard (4 G query
-  // heads); q_cols = 512 G query features, kv_cols = 128 G key (and value) features
-  int n_kv = 8;
-  int q_cols() const { return 512 * n_kv; }
-  int kv_cols() const { return 128 * n_kv; }
-  int qkv_rows() const { return 768 * n_kv; }
-  // weights, k-block-major: W_t[kb][row][64]
-  __nv_bfloat16* w_qkv = nullptr;  // qkv_rows x 4096: W_Q rows 0..q_cols-1, then W_K, then W_V
-  __nv_bfloat16* w_o = nullptr;    // 4096 rows x q_cols (the columns of W_O that belong to its heads)
-  // residual form: W_QKV * diag(attention_norm weight), same layout (attn_set_norm)
-  __nv_bfloat16* w_qkv_norm = nullptr;
-  float norm_eps = 0.f;
-  int* status = nullptr;           // device status word (kDevErr* bits)
-  int* counters = nullptr;         // arrival counters of the decode split merge (kCounterInts)
-  uint8_t* ws = nullptr;           // workspace
-  size_t ws_bytes = 0;
-  const void* last_q = nullptr;
-  const void* last_h = nullptr;
-  // per-kernel device timing
-  bool profiling = false;
-  std::vector<cudaEvent_t> ev;        // 2 per recorded launch
-  std::vector<int> ev_kind;           // kind of each recorded launch
-  size_t ev_used = 0;                 // launches recorded so far
-  int fault_kind = -1;                // test hook armed by attn_debug_inject_timeout
-};
 
 namespace {
 thread_local int g_last_cuda_error = 0;
@@ -59,23 +25,7 @@ void gqa::set_last_cuda_error(cudaError_t e) { g_last_cuda_error = static_cast<i
 
 namespace {
 
-gqa_status cuda_fail(cudaError_t e) {
-  set_last_cuda_error(e);
-  return GQA_ERR_CUDA;
-}
-
-#define GQA_CUDA(call)                          \
-  do {                                          \
-    cudaError_t e_ = (call);                    \
-    if (e_ != cudaSuccess) return cuda_fail(e_); \
-  } while (0)
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-constexpr long long kMaxTokens = 262144;
-constexpr long long kMaxSMax = 1048576;
 constexpr int kSkinnyMaxTokens = 64;     // at or below: swap-AB split-K projections
-constexpr int kDecodeMaxBatch = 1024;
 // Arrival counters of the decode split merge, one per (sequence, kv group, position group).
 constexpr int kCounterInts = kDecodeMaxBatch * 8;
 // Prefills of at most this many tokens per sequence run the decode attention kernel with
@@ -90,44 +40,6 @@ constexpr int kShortMaxT = 16;
 constexpr int kShortPos = 4;
 constexpr int kShortAlwaysKeys = 256;     // at most this many keys: the short kernel
 constexpr int kFlashMinCtas = 32;         // longer caches: flash once its grid has this many CTAs
-
-// ------------------------------------------------------------------ tensor maps
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                   CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
-// bf16 tensor map with 128-byte swizzle; dims[0] innermost; strides in bytes for dims 1..
-bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-              const uint32_t* box) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t d[5], s[4];
-  cuuint32_t b[5], e[5];
-  for (int i = 0; i < rank; ++i) {
-    d[i] = dims[i];
-    b[i] = box[i];
-    e[i] = 1;
-  }
-  for (int i = 0; i < rank - 1; ++i) s[i] = strides[i];
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, s, b, e,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // GEMM operands are addressed as (column c < 64, row r, k block kb) with box 64 x box_rows x 1.
 // Row-major [rows, k_cols] activation: element (c, r, kb) at r*2*k_cols + kb*128 + 2c bytes.
@@ -159,17 +71,6 @@ cudaError_t copy_weight_tiled(void* dst, const void* src, size_t rows, size_t ro
   }
   return cudaSuccess;
 }
-
-// KV cache [B, S_max, n_kv, 128] bf16 seen as (d, g, s < kv_len, b); box 64 d x key_rows.
-bool map_cache(CUtensorMap* m, const void* base, int B, int S_max, int n_kv, int kv_len, uint32_t key_rows) {
-  const uint64_t dims[4] = {128, static_cast<uint64_t>(n_kv), static_cast<uint64_t>(kv_len), static_cast<uint64_t>(B)};
-  const uint64_t strides[3] = {128 * 2, static_cast<uint64_t>(n_kv) * 128 * 2,
-                               static_cast<uint64_t>(S_max) * n_kv * 128 * 2};
-  const uint32_t box[4] = {64, 1, key_rows, 1};
-  return make_map(m, base, 4, dims, strides, box);
-}
-
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // ------------------------------------------------------------------ workspace
 struct WsLayout {
@@ -239,84 +140,11 @@ WsLayout ws_layout(long long n_tok, int n_kv, const SkinnyPlan* sk, const Decode
   return w;
 }
 
-gqa_status ensure_ws(gqa_ctx* c, size_t bytes, cudaStream_t s) {
-  if (bytes <= c->ws_bytes) return GQA_OK;
-  GQA_CUDA(cudaStreamSynchronize(s));
-  if (c->ws) GQA_CUDA(cudaFree(c->ws));
-  c->ws = nullptr;
-  c->ws_bytes = 0;
-  const size_t want = round_up(bytes, 1 << 20);
-  if (cudaMalloc(&c->ws, want) != cudaSuccess) {
-    cudaGetLastError();
-    c->ws = nullptr;
-    return GQA_ERR_OOM;
-  }
-  c->ws_bytes = want;
-  return GQA_OK;
-}
-
-gqa_status check_device(gqa_ctx* c) {
-  int dev = -1;
-  GQA_CUDA(cudaGetDevice(&dev));
-  if (dev != c->device) return GQA_ERR_DEVICE;
-  return GQA_OK;
-}
-
-// One-shot test hook: 1 if the next launch of `kind` should skip its first unit's loads.
-int take_fault(gqa_ctx* c, int kind) {
-  if (c->fault_kind != kind) return 0;
-  c->fault_kind = -1;
-  return 1;
-}
-
-constexpr size_t kMaxProfiledLaunches = 65536;
-
-// RAII bracket of one kernel launch with two events when profiling is on.
-// NVTX range names of the kernel kinds (host-side ranges around each launch; without a tool
-// attached an NVTX call returns at once).
-const char* const kKindNames[GQA_KERNEL_KINDS] = {"gqa.qkv_gemm", "gqa.qkv_splitk", "gqa.flash_prefill",
-                                                  "gqa.decode_attn", "gqa.out_gemm", "gqa.out_splitk",
-                                                  "gqa.rms_norm"};
-
-// RAII NVTX range around one entry point's host work (its launches nest inside it).
-struct CallRange {
-  explicit CallRange(const char* name) { nvtxRangePushA(name); }
-  ~CallRange() { nvtxRangePop(); }
-};
-
-struct ProfScope {
-  gqa_ctx* c;
-  cudaStream_t s;
-  bool on;
-  ProfScope(gqa_ctx* c_, int kind, cudaStream_t s_) : c(c_), s(s_), on(false) {
-    nvtxRangePushA(kind >= 0 && kind < GQA_KERNEL_KINDS ? kKindNames[kind] : "gqa.kernel");
-    if (c->profiling && c->ev_used < kMaxProfiledLaunches) {
-      if (c->ev.size() < 2 * (c->ev_used + 1)) {
-        cudaEvent_t a, b;
-        if (cudaEventCreate(&a) != cudaSuccess) return;
-        if (cudaEventCreate(&b) != cudaSuccess) { cudaEventDestroy(a); return; }
-        c->ev.push_back(a);
-        c->ev.push_back(b);
-        c->ev_kind.push_back(kind);
-      }
-      c->ev_kind[c->ev_used] = kind;
-      on = cudaEventRecord(c->ev[2 * c->ev_used], s) == cudaSuccess;
-    }
-  }
-  ~ProfScope() {
-    if (on) {
-      cudaEventRecord(c->ev[2 * c->ev_used + 1], s);
-      ++c->ev_used;
-    }
-    nvtxRangePop();
-  }
-};
-
-const float kScaleLog2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
-
-// Q/K/V projection + RoPE + cache write for n_tok tokens laid out [B, T] (steps 1-5).
+// Q/K/V projection + RoPE + cache write for n_tok tokens laid out [B, T] (steps 1-5).  The T
+// positions start at start_pos with R [T,64,2], or, with seq_start, at seq_start[b] (device)
+// with R [n_tok,64,2].
 gqa_status run_qkv(gqa_ctx* c, const void* x, int n_tok, int T, const float* R, void* ck, void* cv,
-                   int S_max, int start_pos, void* q_out, const WsLayout& w, const SkinnyPlan* sk,
+                   int S_max, int start_pos, const int* seq_start, void* q_out, const WsLayout& w, const SkinnyPlan* sk,
                    const float* row_scale, cudaStream_t s) {
   GemmParams p{};
   // residual form: the folded weights, each token row scaled by its 1 / rms
@@ -325,6 +153,7 @@ gqa_status run_qkv(gqa_ctx* c, const void* x, int n_tok, int T, const float* R, 
   p.T = T;
   p.S_max = S_max;
   p.start_pos = start_pos;
+  p.seq_start = seq_start;
   p.status = c->status;
   p.num_kb = 64;
   p.q_cols = c->q_cols();
@@ -498,7 +327,7 @@ namespace {
 
 // 1 / rms of each of the n_tok token rows of x (residual form), into the workspace.
 gqa_status run_rms(gqa_ctx* c, const void* x, int n_tok, const WsLayout& w, cudaStream_t s) {
-  float* r = reinterpret_cast<float*>(c->ws + w.rstd_off);
+  float* r = reinterpret_cast<float*>(c->ws.p + w.rstd_off);
   { ProfScope ps(c, GQA_KERNEL_RMS_NORM, s); GQA_CUDA(launch_rms_rstd(x, n_tok, c->norm_eps, r, s)); }
   return GQA_OK;
 }
@@ -529,19 +358,19 @@ gqa_status prefill_impl(gqa_ctx* c, const void* x, int B, int T, const float* R,
   const DecodePlan dp = decode_plan(B * n_pg, G, kv_len, c->num_sms, 1);
   const WsLayout w = short_path ? ws_layout(n_tok, G, sk, &dp, static_cast<long long>(B) * n_pg * 4 * kShortPos)
                                 : ws_layout(n_tok, G, sk, nullptr, 0);
-  st = ensure_ws(c, w.total, s);
+  st = ensure_buffer(c, c->ws, w.total, s);
   if (st != GQA_OK) return st;
-  void* q_r = c->ws + w.q_off;
-  void* h = c->ws + w.h_off;
+  void* q_r = c->ws.p + w.q_off;
+  void* h = c->ws.p + w.h_off;
   c->last_q = q_r;
   c->last_h = h;
 
   const float* row_scale = nullptr;
   if (residual) {
     if ((st = run_rms(c, x, n_tok, w, s)) != GQA_OK) return st;
-    row_scale = reinterpret_cast<const float*>(c->ws + w.rstd_off);
+    row_scale = reinterpret_cast<const float*>(c->ws.p + w.rstd_off);
   }
-  st = run_qkv(c, x, n_tok, T, R, cache_k, cache_v, S_max, start_pos, q_r, w, sk, row_scale, s);
+  st = run_qkv(c, x, n_tok, T, R, cache_k, cache_v, S_max, start_pos, nullptr, q_r, w, sk, row_scale, s);
   if (st != GQA_OK) return st;
 
   if (short_path) {
@@ -561,8 +390,8 @@ gqa_status prefill_impl(gqa_ctx* c, const void* x, int B, int T, const float* R,
     p.causal = causal ? 1 : 0;
     p.n_pg = n_pg;
     p.q = q_r;
-    p.part_o = reinterpret_cast<float*>(c->ws + w.dec_o_off);
-    p.part_ml = reinterpret_cast<float*>(c->ws + w.dec_ml_off);
+    p.part_o = reinterpret_cast<float*>(c->ws.p + w.dec_o_off);
+    p.part_ml = reinterpret_cast<float*>(c->ws.p + w.dec_ml_off);
     p.H = h;
     p.status = c->status;
     p.scale_log2 = kScaleLog2;
@@ -634,10 +463,10 @@ gqa_status decode_impl(gqa_ctx* c, const void* x, int B, int start_pos, const fl
   const SkinnyPlan* sk = B <= kSkinnyMaxTokens ? &sk_v : nullptr;
   const DecodePlan dp = decode_plan(B, G, kv_len, c->num_sms);
   const WsLayout w = ws_layout(B, G, sk, &dp, static_cast<long long>(B) * 4);
-  st = ensure_ws(c, w.total, s);
+  st = ensure_buffer(c, c->ws, w.total, s);
   if (st != GQA_OK) return st;
-  void* q_r = c->ws + w.q_off;
-  void* h = c->ws + w.h_off;
+  void* q_r = c->ws.p + w.q_off;
+  void* h = c->ws.p + w.h_off;
   c->last_q = q_r;
   c->last_h = h;
 
@@ -645,9 +474,9 @@ gqa_status decode_impl(gqa_ctx* c, const void* x, int B, int start_pos, const fl
   const float* row_scale = nullptr;
   if (residual) {
     if ((st = run_rms(c, x, B, w, s)) != GQA_OK) return st;
-    row_scale = reinterpret_cast<const float*>(c->ws + w.rstd_off);
+    row_scale = reinterpret_cast<const float*>(c->ws.p + w.rstd_off);
   }
-  st = run_qkv(c, x, B, 1, R_row, cache_k, cache_v, S_max, start_pos, q_r, w, sk, row_scale, s);
+  st = run_qkv(c, x, B, 1, R_row, cache_k, cache_v, S_max, start_pos, nullptr, q_r, w, sk, row_scale, s);
   if (st != GQA_OK) return st;
 
   // steps 6-13 against the cache (no mask: every key 0..start_pos is visible)
@@ -666,8 +495,8 @@ gqa_status decode_impl(gqa_ctx* c, const void* x, int B, int start_pos, const fl
   p.causal = 0;  // the new position sees the whole cache
   p.n_pg = 1;
   p.q = q_r;
-  p.part_o = reinterpret_cast<float*>(c->ws + w.dec_o_off);
-  p.part_ml = reinterpret_cast<float*>(c->ws + w.dec_ml_off);
+  p.part_o = reinterpret_cast<float*>(c->ws.p + w.dec_o_off);
+  p.part_ml = reinterpret_cast<float*>(c->ws.p + w.dec_ml_off);
   p.H = h;
   p.status = c->status;
   p.scale_log2 = kScaleLog2;
@@ -677,6 +506,55 @@ gqa_status decode_impl(gqa_ctx* c, const void* x, int B, int start_pos, const fl
 
   // step 14
   return run_out(c, h, B, delta, w, sk, residual ? x : nullptr, s);
+}
+
+// The block over sequences of different lengths: T new positions of each sequence written behind
+// its own kv_len[b], then attention over the cache (a tree's rows by their mask; weights: one
+// position per sequence, each key's weight accumulated).
+gqa_status ragged_impl(gqa_ctx* c, const void* x, int B, int T, const float* R, const uint32_t* mask, void* cache_k,
+                       void* cache_v, int S_max, const int* kv_len, float* weights, float* delta, bool residual,
+                       cudaStream_t s) {
+  if (!c || !x || !R || !cache_k || !cache_v || !kv_len || !delta) return GQA_ERR_INVALID_ARG;
+  if (B < 1 || B > kDecodeMaxBatch || T < 1 || T > GQA_MAX_TREE || S_max < 1 || S_max > kMaxSMax || T > S_max)
+    return GQA_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(R) || !aligned16(mask) || !aligned16(cache_k) || !aligned16(cache_v) ||
+      !aligned16(kv_len) || !aligned16(weights) || !aligned16(delta))
+    return GQA_ERR_ALIGN;
+  if (residual && !c->w_qkv_norm) return GQA_ERR_INVALID_ARG;  // attn_set_norm not called (never on a shard)
+  gqa_status st = check_device(c);
+  if (st != GQA_OK) return st;
+
+  const int n_tok = B * T;
+  SkinnyPlan sk_v = skinny_plan(n_tok);
+  const SkinnyPlan* sk = n_tok <= kSkinnyMaxTokens ? &sk_v : nullptr;
+  const WsLayout w = ws_layout(n_tok, c->n_kv, sk, nullptr, 0);
+  st = ensure_buffer(c, c->ws, w.total, s);
+  if (st != GQA_OK) return st;
+  void* q_r = c->ws.p + w.q_off;
+  void* h = c->ws.p + w.h_off;
+  c->last_q = q_r;
+  c->last_h = h;
+  const float* row_scale = nullptr;
+  if (residual) {
+    if ((st = run_rms(c, x, n_tok, w, s)) != GQA_OK) return st;
+    row_scale = reinterpret_cast<const float*>(c->ws.p + w.rstd_off);
+  }
+  st = run_qkv(c, x, n_tok, T, R, cache_k, cache_v, S_max, 0, kv_len, q_r, w, sk, row_scale, s);
+  if (st != GQA_OK) return st;
+  CacheAttnCall a{};
+  a.B = B;
+  a.T = T;
+  a.n_new = T;
+  a.S_max = S_max;
+  a.mask = mask;
+  a.kv_len = kv_len;
+  a.q = q_r;
+  a.cache_k = cache_k;
+  a.cache_v = cache_v;
+  a.h = h;
+  a.weights = weights;
+  if ((st = run_cache_attn(c, a, s)) != GQA_OK) return st;
+  return run_out(c, h, n_tok, delta, w, sk, residual ? x : nullptr, s);
 }
 
 }  // namespace
@@ -712,6 +590,41 @@ gqa_status attn_decode_residual(gqa_ctx* c, const void* x, int B, int start_pos,
                      reinterpret_cast<cudaStream_t>(stream));
 }
 
+gqa_status attn_prefill_tree(gqa_ctx* c, const void* x, int B, int T, const float* R, const unsigned* tree_mask,
+                             void* cache_k, void* cache_v, int S_max, const int* prefix_len, float* delta,
+                             gqa_stream_t stream) {
+  CallRange range("gqa.attn_prefill_tree");
+  if (!tree_mask) return GQA_ERR_INVALID_ARG;
+  return ragged_impl(c, x, B, T, R, tree_mask, cache_k, cache_v, S_max, prefix_len, nullptr, delta, false,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+gqa_status attn_prefill_tree_residual(gqa_ctx* c, const void* x, int B, int T, const float* R,
+                                      const unsigned* tree_mask, void* cache_k, void* cache_v, int S_max,
+                                      const int* prefix_len, float* h_out, gqa_stream_t stream) {
+  CallRange range("gqa.attn_prefill_tree_residual");
+  if (!tree_mask) return GQA_ERR_INVALID_ARG;
+  return ragged_impl(c, x, B, T, R, tree_mask, cache_k, cache_v, S_max, prefix_len, nullptr, h_out, true,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+gqa_status attn_decode_weights(gqa_ctx* c, const void* x, int B, const float* R, void* cache_k, void* cache_v,
+                               int S_max, const int* kv_len, float* weights, float* delta, gqa_stream_t stream) {
+  CallRange range("gqa.attn_decode_weights");
+  if (!weights) return GQA_ERR_INVALID_ARG;
+  return ragged_impl(c, x, B, 1, R, nullptr, cache_k, cache_v, S_max, kv_len, weights, delta, false,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+gqa_status attn_decode_weights_residual(gqa_ctx* c, const void* x, int B, const float* R, void* cache_k,
+                                        void* cache_v, int S_max, const int* kv_len, float* weights, float* h_out,
+                                        gqa_stream_t stream) {
+  CallRange range("gqa.attn_decode_weights_residual");
+  if (!weights) return GQA_ERR_INVALID_ARG;
+  return ragged_impl(c, x, B, 1, R, nullptr, cache_k, cache_v, S_max, kv_len, weights, h_out, true,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
 gqa_status attn_set_norm(gqa_ctx* c, const void* norm_w, float eps, gqa_stream_t stream) {
   if (!c || !norm_w || !(eps > 0.f) || !std::isfinite(eps)) return GQA_ERR_INVALID_ARG;
   if (!aligned16(norm_w)) return GQA_ERR_ALIGN;
@@ -741,6 +654,7 @@ gqa_status attn_sync_status(gqa_ctx* c, gqa_stream_t stream) {
     GQA_CUDA(cudaMemset(c->counters, 0, kCounterInts * sizeof(int)));
     GQA_CUDA(cudaMemset(c->status, 0, sizeof(int)));
     if (v & kDevErrTimeout) return GQA_ERR_TIMEOUT;
+    if (v & kDevErrRange) return GQA_ERR_SHAPE;
   }
   return GQA_OK;
 }
@@ -841,7 +755,8 @@ void attn_destroy(gqa_ctx* c) {
   if (c->w_qkv_norm) cudaFree(c->w_qkv_norm);
   if (c->status) cudaFree(c->status);
   if (c->counters) cudaFree(c->counters);
-  if (c->ws) cudaFree(c->ws);
+  if (c->ws.p) cudaFree(c->ws.p);
+  for (void* p : c->retired) cudaFree(p);
   delete c;
 }
 

@@ -73,6 +73,11 @@ cudaError_t launch_short_attn(const CUtensorMap& k, const CUtensorMap& v, const 
                               cudaStream_t s);
 cudaError_t launch_decode_combine(const DecodeParams& p, int B, cudaStream_t s);
 cudaError_t launch_exp2_compare(const float* a, float* out_fma, float* out_mufu, int n, cudaStream_t s);
+// Attention over caches of per-sequence length, and the cache's own upkeep.
+cudaError_t launch_cache_attn(const CacheAttnParams& p, cudaStream_t s);
+cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t s);
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s);
+cudaError_t launch_evict_move(const EvictParams& p, cudaStream_t s);
 cudaError_t launch_rms_rstd(const void* x, int rows, float eps, float* r, cudaStream_t s);
 cudaError_t launch_fold_norm_weight(const void* src, const void* w, int rows, void* dst, cudaStream_t s);
 

@@ -8,6 +8,7 @@ namespace gqa {
 
 // Status bits OR-ed into the context's device status word.
 constexpr int kDevErrTimeout = 1;
+constexpr int kDevErrRange = 2;  // a per-sequence length or path read on the device is out of range
 
 // Upper bound for any single device-side wait (wall-clock, via %globaltimer).
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
@@ -34,8 +35,11 @@ struct GemmParams {
   void* out0;        // kQkvRope: Q_r [M,q_cols] bf16 | kStoreF32: D fp32
   void* out1;        // kQkvRope: cache_k
   void* out2;        // kQkvRope: cache_v
-  const float* R;    // Q/K/V epilogues: [T,64,2]
+  const float* R;    // Q/K/V epilogues: [T,64,2] (with seq_start: [tokens,64,2])
   int T, S_max, start_pos;
+  // Q/K/V epilogues: first position of each sequence [B] (device), read in place of start_pos; a
+  // sequence whose T positions do not fit the cache is not written.  Null: start_pos for all.
+  const int* seq_start;
   int ldo;           // kStoreF32: row stride (floats)
   void* fin0;        // split-K final outputs: Q_r [N,q_cols] bf16 | Delta [N,4096] fp32
   void* fin1;        // kSplitKQkv: cache_k
@@ -78,6 +82,53 @@ struct DecodeParams {
   int* status_sticky;
   int fault;      // test hook: CTA (0, 0, 0)'s producer issues no loads (its waits run out)
   float scale_log2;
+};
+
+// Attention of a few positions per sequence over caches of per-sequence length (tree attention,
+// decode attention that accumulates key weights).  Row t of sequence b sees keys 0 ..
+// kv_len[b] - 1 and, of the n_new keys behind them, those whose bit is set in mask[b, t].
+struct CacheAttnParams {
+  int B, T, S_max;
+  int n_kv;                // kv groups of the context (4 query heads each; q and h rows are 512 n_kv wide)
+  int n_new;               // keys behind kv_len[b] (the call's own positions; at most T)
+  const uint32_t* mask;    // [B, T, ceil(T / 32)] visibility bits of the n_new keys; null: all visible
+  const int* kv_len;       // [B]
+  const void* q;           // [B, T, 512 n_kv] bf16
+  const void* k;           // caches [B, S_max, n_kv, 128] bf16
+  const void* v;
+  void* h;                 // [B, T, 512 n_kv] bf16
+  float* weights;          // [B, n_kv, S_max] accumulated key weights (T = 1), or null
+  int* status;
+  float scale_log2;        // log2(e) / sqrt(128)
+};
+
+// The accepted path of each sequence moved to the front of its drafted positions.
+struct CommitParams {
+  int B, S_max, T, n_kv;
+  void* k;
+  void* v;
+  const int* prefix_len;  // [B]
+  const int* path;        // [B, T]
+  const int* n_accept;    // [B]
+  int* new_len;           // [B], may be prefix_len
+  int* status;
+};
+
+// Selection and move of the cache positions that an eviction keeps.
+struct EvictParams {
+  int B, S_max, S_out, n_kv;
+  int budget, n_first, n_recent;
+  int in_place;
+  const void* k;
+  const void* v;
+  const float* weights;   // [B, n_kv, S_max]
+  const int* kv_len;      // [B]
+  void* out_k;            // [B, S_out, n_kv, 128]
+  void* out_v;
+  float* out_weights;     // [B, n_kv, S_out]
+  int* kept;              // [B, n_kv, budget]
+  int* new_len;           // [B], may be kv_len
+  int* status;
 };
 
 }  // namespace gqa
