@@ -371,10 +371,11 @@ enum {
     GQA_KERNEL_OUT_SPLITK = 5,     /* the same for few tokens */
     GQA_KERNEL_RMS_NORM = 6,       /* 1 / rms of each token row (residual form only) */
     GQA_KERNEL_CACHE_ATTN = 7,     /* tree attention / decode attention with key weights */
-    GQA_KERNEL_CACHE_COMMIT = 8,   /* accepted path moved behind the prefix */
-    GQA_KERNEL_EVICT_SELECT = 9,   /* positions that an eviction keeps */
-    GQA_KERNEL_EVICT_MOVE = 10,    /* their keys and values moved */
-    GQA_KERNEL_KINDS = 11
+    GQA_KERNEL_CACHE_FINISH = 8,   /* its merge of split sequences; accumulation of the key weights */
+    GQA_KERNEL_CACHE_COMMIT = 9,   /* accepted path moved behind the prefix */
+    GQA_KERNEL_EVICT_SELECT = 10,  /* positions that an eviction keeps */
+    GQA_KERNEL_EVICT_MOVE = 11,    /* their keys and values moved */
+    GQA_KERNEL_KINDS = 12
 };
 
 /*
@@ -443,7 +444,7 @@ gqa_status attn_decode_attention_noalloc_debug_inject_timeout(void);
 /*
  * attn_debug_inject_timeout — test hook for the failure path (no counterpart on the pages).
  * Arms a one-shot flag: on the next launch of kernel kind `kind` (GQA_KERNEL_QKV_GEMM,
- * _QKV_SPLITK, _FLASH_PREFILL, _DECODE_ATTN, _OUT_GEMM or _OUT_SPLITK) made through this
+ * _QKV_SPLITK, _FLASH_PREFILL, _DECODE_ATTN, _OUT_GEMM, _OUT_SPLITK or _CACHE_ATTN) made through this
  * context, the first work unit's TMA producer issues no loads.  Its consumers' bounded
  * waits then run out (about 2 s), the unit records GQA_ERR_TIMEOUT in the status word,
  * releases its tensor memory and returns; kernels queued after it on the stream may time
@@ -468,6 +469,18 @@ gqa_status attn_debug_inject_timeout(gqa_ctx *ctx, int kind);
 gqa_status attn_debug_pair_schedule(int m_tiles, int n_tiles, int n_pairs, int *full_rounds,
                                     int *tail_w, int *grid_ctas, int *items, int max_items,
                                     int *n_items);
+
+/*
+ * attn_debug_cache_schedule — how tree attention and attn_decode_attention_weights share the
+ * 128-key tiles of B sequences among n_ctas CTAs, computed on the host by the code that the
+ * kernel runs (for tests, no GPU needed).  lens [B] (host), n_new keys behind each length, units
+ * (kv heads x groups of query rows) per sequence.  Writes the pieces in order as septuples (CTA,
+ * sequence, unit, first tile, tiles, slot of its partial result or -1 for a whole unit, last CTA
+ * of the unit) into pieces[7 * max_pieces]; *n_pieces gets their count.  Errors:
+ * GQA_ERR_INVALID_ARG, GQA_ERR_SHAPE (more than max_pieces pieces; *n_pieces holds the count).
+ */
+gqa_status attn_debug_cache_schedule(const int *lens, int B, int n_new, int S_max, int units, int n_ctas,
+                                     int *pieces, int max_pieces, int *n_pieces);
 
 /*
  * attn_debug_exp2 — the two exponentials the prefill softmax uses, on n fp32 device inputs a

@@ -1,0 +1,66 @@
+"""How the attention over caches of per-sequence length shares its key tiles (host computation, the
+code the kernel runs; no GPU needed): every tile of every unit is taken once, in order, the CTAs'
+shares differ by at most a tile, and the partial results of a cut unit lie in slots that no other
+unit uses."""
+import random
+
+import pytest
+
+from transformer_gqa_attention_gb300 import _build, abi
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    _build.build()
+
+
+def check(lens, n_new, S_max, units, n_ctas):
+    pieces = abi.attn_debug_cache_schedule(lens, n_new, S_max, units, n_ctas)
+    tiles = [max(1, -(-(n + n_new) // 128)) if 0 <= n <= S_max - n_new else 1 for n in lens]
+    want = [(b, u, t) for b in range(len(lens)) for u in range(units) for t in range(tiles[b])]
+    got = [(b, u, t) for _, b, u, first, n, _, _ in pieces for t in range(first, first + n)]
+    assert got == want
+    load = [0] * min(n_ctas, len(want))
+    for c, *_, n, _, _ in pieces:
+        load[c] += n
+    assert max(load) - min(load) <= 1
+    assert [c for c, *_ in pieces] == sorted(c for c, *_ in pieces)
+    cut, used = {}, {}
+    for c, b, u, first, n, slot, last in pieces:
+        if slot < 0:
+            assert first == 0 and n == tiles[b] and last == c
+            continue
+        assert slot not in used and slot // 2 == c
+        used[slot] = (b, u)
+        cut.setdefault((b, u), []).append((c, first, slot, last))
+    for parts in cut.values():  # slots 2 f + 1, then 2 c of every CTA up to the last
+        f = parts[0][0]
+        assert len({p[3] for p in parts}) == 1
+        assert [p[2] for p in parts] == [2 * f + 1] + [2 * c for c in range(f + 1, parts[0][3] + 1)]
+        assert parts[0][1] == 0 and len(parts) >= 2
+
+
+@pytest.mark.parametrize("n_ctas", [1, 2, 7, 148, 152])
+@pytest.mark.parametrize("lens", [[0], [1], [127], [128], [129], [32000], [0, 0, 0], [5, 4000, 128, 1], [-1, 70, 2 ** 31 - 1],
+                                  [300] * 33])
+def test_small_batches(lens, n_ctas):
+    for units in (1, 8, 16, 32):
+        for n_new in (0, 1, 26):
+            check(lens, n_new, 40000, units, n_ctas)
+
+
+def test_random_batches():
+    rng = random.Random(1)
+    for _ in range(40):
+        B = rng.choice([1, 3, 40, 385, 800, 1024])
+        top = rng.choice([10, 1000, 20000])
+        check([rng.randint(-1, top) for _ in range(B)], rng.choice([0, 1, 64]), top + 64, rng.choice([1, 2, 8]), 152)
+
+
+def test_arguments():
+    for kw in (dict(units=0), dict(n_ctas=0), dict(n_new=-1), dict(S_max=0)):
+        a = dict(n_new=1, S_max=10, units=1, n_ctas=2) | kw
+        with pytest.raises(abi.GQAError):
+            abi.attn_debug_cache_schedule([1], **a)
+    with pytest.raises(abi.GQAError):
+        abi.attn_debug_cache_schedule([], 1, 10, 1, 2)

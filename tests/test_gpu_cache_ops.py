@@ -164,6 +164,12 @@ def test_tree_attention_over_a_long_prefix():
     run_tree(92, [9000, 12000], 64, n_kv=1)
 
 
+@pytest.mark.parametrize("T", [2, 20, 48, 100])
+def test_tree_attention_with_more_units_than_ctas(T):
+    # whole units of several key tiles beside cut ones
+    run_tree(94, [(53 * b) % 700 for b in range(40)], T)
+
+
 def test_causal_chain_equals_the_prefill_mask():
     # a chain (every token sees all before it) is a causal prefill of T positions
     T, L = 24, 200
@@ -416,3 +422,29 @@ def test_evict_refuses_partial_overlaps():
         assert err.value.status == 1
     abi.attn_cache_evict(ctx, k, v, w, 1, 64, lens, 16, 0, 0, a, c, ow, 32, kept, torch.zeros_like(lens))
     abi.attn_sync_status(ctx)
+
+
+# ------------------------------------------------------------------------------- failure path
+@pytest.mark.parametrize("weights", [False, True])
+def test_a_wait_that_runs_out_is_reported(weights):
+    # CTA 0 issues no loads: its waits run out, the status says so, and the next call is right
+    ctx = context()
+    gen = torch.Generator().manual_seed(11)
+    k, v = (t.to(DEV) for t in draw_cache(gen, 2, 900, 8, [800, 800]))
+    q = torch.randn(2, 3, 4096, generator=gen).to(torch.bfloat16).to(DEV)
+    h = torch.zeros(2, 3, 4096, dtype=torch.bfloat16, device=DEV)
+    words = torch.from_numpy(co.mask_words(np.stack([np.eye(3, dtype=bool)] * 2))).to(DEV)
+    abi.attn_debug_inject_timeout(ctx, "cache_attn")
+    if weights:
+        w = torch.zeros(2, 8, 900, device=DEV)
+        abi.attn_decode_attention_weights(ctx, q, k, v, 2, 900, ints([700, 700]), w, h)
+    else:
+        abi.attn_tree_attention(ctx, q, 2, 3, words, k, v, 900, ints([700, 700]), h)
+    with pytest.raises(abi.GQAError) as err:
+        abi.attn_sync_status(ctx)
+    assert err.value.status == 5
+    abi.attn_sync_status(ctx)
+    if weights:
+        run_weights(12, [700, 700], S=900)
+    else:
+        run_tree(12, [700, 700], 3, S=900)

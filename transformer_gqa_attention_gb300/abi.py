@@ -24,12 +24,12 @@ EXPORTED = ("attn_create", "attn_create_shard", "attn_prefill", "attn_decode", "
             "attn_decode_attention_noalloc_status", "attn_decode_attention_noalloc_debug_inject_timeout",
            "attn_tree_attention", "attn_prefill_tree", "attn_prefill_tree_residual", "attn_cache_commit",
            "attn_decode_attention_weights", "attn_decode_weights", "attn_decode_weights_residual",
-           "attn_cache_evict",
+           "attn_cache_evict", "attn_debug_cache_schedule",
             "attn_destroy", "attn_strerror", "attn_last_cuda_error")
 
 # Kernel kinds of attn_profile_end (GQA_KERNEL_* in include/gqa_attn.h).
 KERNEL_KINDS = ("qkv_gemm", "qkv_splitk", "flash_prefill", "decode_attn", "out_gemm", "out_splitk",
-                "rms_norm", "cache_attn", "cache_commit", "evict_select", "evict_move")
+                "rms_norm", "cache_attn", "cache_finish", "cache_commit", "evict_select", "evict_move")
 
 _lib = None
 
@@ -103,6 +103,8 @@ def lib() -> ctypes.CDLL:
         getattr(L, name).restype = i32
     L.attn_cache_evict.argtypes = [vp, vp, vp, vp, i32, i32, vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp]
     L.attn_cache_evict.restype = i32
+    L.attn_debug_cache_schedule.argtypes = [ip, i32, i32, i32, i32, i32, ip, i32, ip]
+    L.attn_debug_cache_schedule.restype = i32
     L.attn_destroy.argtypes = [vp]
     L.attn_destroy.restype = None
     L.attn_strerror.argtypes = [i32]
@@ -315,6 +317,22 @@ def attn_cache_evict(ctx, cache_k, cache_v, weights, B, S_max, kv_len, budget, n
            lib().attn_cache_evict(ctx, _ptr(cache_k), _ptr(cache_v), _ptr(weights), int(B), int(S_max),
                                   _ptr(kv_len), int(budget), int(n_first), int(n_recent), _ptr(out_k), _ptr(out_v),
                                   _ptr(out_weights), int(S_out), _ptr(kept), _ptr(new_len), _stream(stream)))
+
+
+def attn_debug_cache_schedule(lens, n_new, S_max, units, n_ctas):
+    """The pieces in which CTAs share the sequences' key tiles (host computation, no GPU needed):
+    a list of (CTA, sequence, unit, first tile, tiles, partial slot or -1, unit's last CTA)."""
+    i32 = ctypes.c_int
+    B = len(lens)
+    arr, n = (i32 * B)(*lens), i32()
+    L = lib()
+    st = L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, n_ctas, None, 0, ctypes.byref(n))
+    if st not in (0, 2):  # GQA_ERR_SHAPE: the count is in n
+        _check("attn_debug_cache_schedule", st)
+    buf = (i32 * (7 * max(n.value, 1)))()
+    _check("attn_debug_cache_schedule",
+           L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, n_ctas, buf, n.value, ctypes.byref(n)))
+    return [tuple(buf[7 * i:7 * i + 7]) for i in range(n.value)]
 
 
 def attn_destroy(ctx):

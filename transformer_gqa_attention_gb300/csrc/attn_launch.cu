@@ -11,6 +11,8 @@ cudaError_t configure_gemm_kernels();
 cudaError_t configure_kernels() {
   cudaError_t e = configure_gemm_kernels();
   if (e != cudaSuccess) return e;
+  e = configure_cache_attn();
+  if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(flash_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            FlashSmem::kBytes);
   if (e != cudaSuccess) return e;

@@ -48,6 +48,7 @@ struct gqa_ctx {
   int* status = nullptr;           // device status word (kDevErr* bits)
   int* counters = nullptr;         // arrival counters of the decode split merge (kCounterInts)
   gqa::DeviceBuffer ws;            // workspace of the block forms
+  gqa::DeviceBuffer cache_ws;      // scratch of the attention over caches of per-sequence length
   std::vector<void*> retired;      // outgrown buffers that a captured graph may still use
   const void* last_q = nullptr;
   const void* last_h = nullptr;
@@ -188,7 +189,7 @@ constexpr size_t kMaxProfiledLaunches = 65536;
 // attached an NVTX call returns at once).
 inline const char* const kKindNames[GQA_KERNEL_KINDS] = {"gqa.qkv_gemm", "gqa.qkv_splitk", "gqa.flash_prefill",
                                                   "gqa.decode_attn", "gqa.out_gemm", "gqa.out_splitk",
-                                                  "gqa.rms_norm", "gqa.cache_attn", "gqa.cache_commit", "gqa.evict_select",
+                                                  "gqa.rms_norm", "gqa.cache_attn", "gqa.cache_finish", "gqa.cache_commit", "gqa.evict_select",
                                                          "gqa.evict_move"};
 
 // RAII NVTX range around one entry point's host work (its launches nest inside it).

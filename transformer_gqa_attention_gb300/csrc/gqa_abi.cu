@@ -675,6 +675,7 @@ gqa_status attn_debug_inject_timeout(gqa_ctx* c, int kind) {
     case GQA_KERNEL_DECODE_ATTN:
     case GQA_KERNEL_OUT_GEMM:
     case GQA_KERNEL_OUT_SPLITK:
+    case GQA_KERNEL_CACHE_ATTN:
       c->fault_kind = kind;
       return GQA_OK;
     default:
@@ -756,6 +757,7 @@ void attn_destroy(gqa_ctx* c) {
   if (c->status) cudaFree(c->status);
   if (c->counters) cudaFree(c->counters);
   if (c->ws.p) cudaFree(c->ws.p);
+  if (c->cache_ws.p) cudaFree(c->cache_ws.p);
   for (void* p : c->retired) cudaFree(p);
   delete c;
 }

@@ -1,0 +1,83 @@
+// kv_sched.h — how the attention over caches of per-sequence length shares its key tiles among
+// CTAs.  Host and device use the same code (the host's for tests).
+//
+// A unit is (sequence b, kv head, group of query rows); it reads the ceil(end_b / 128) key tiles
+// of its sequence (at least one, so that every unit writes its rows).  The units' tiles, unit
+// after unit and sequence after sequence, form one row of `total` tiles, of which CTA c of n takes
+// tiles c total / n .. (c + 1) total / n - 1: equal work whatever the lengths are, without the
+// host knowing them.  What a CTA takes of one unit is a piece; a unit cut over several CTAs is
+// merged from its pieces' partial results.
+#pragma once
+
+#ifdef __CUDACC__
+#define GQA_HD __host__ __device__ __forceinline__
+#else
+#define GQA_HD inline
+#endif
+
+namespace gqa {
+
+constexpr int kKvTile = 128;
+
+// Keys that sequence b reads: its length and the n_new positions behind it; -1: out of range.
+GQA_HD int kv_end(int len, int n_new, int S_max) { return len < 0 || len > S_max - n_new ? -1 : len + n_new; }
+
+GQA_HD int kv_tiles(int end) { return end <= kKvTile ? 1 : (end + kKvTile - 1) / kKvTile; }
+
+// CTAs that share the row: no more than tiles, so that every one of them has a range and a unit's
+// pieces lie in consecutive CTAs.
+GQA_HD int range_ctas(int total, int grid) { return total < grid ? total : grid; }
+
+GQA_HD int range_start(int total, int n_ctas, int c) {
+  return static_cast<int>(static_cast<long long>(c) * total / n_ctas);
+}
+
+// The CTA whose range holds tile x: the last c with range_start(c) <= x, c total < (x + 1) n.
+GQA_HD int range_owner(int total, int n_ctas, int x) {
+  return static_cast<int>(((static_cast<long long>(x) + 1) * n_ctas - 1) / total);
+}
+
+// The pieces of one CTA's range, in order.
+struct KvWalk {
+  int b, u;       // sequence, unit in it (kv head x row groups + row group)
+  int tiles;      // key tiles of each of the sequence's units
+  int first;      // the piece's first tile
+  int n;          // its tiles
+  int left;       // tiles of the range from the piece on
+  int units;      // units of a sequence
+
+  // offset: tiles of sequence b before the range's start
+  GQA_HD void start(int b_, int offset, int tiles_, int units_, int range) {
+    b = b_;
+    units = units_;
+    tiles = tiles_;
+    u = offset / tiles;
+    first = offset - u * tiles;
+    left = range;
+    n = min_(tiles - first, left);
+  }
+  GQA_HD bool done() const { return left <= 0; }
+  GQA_HD bool whole() const { return n == tiles; }
+  // tiles_of(b): key tiles of sequence b
+  template <typename F>
+  GQA_HD void next(F tiles_of) {
+    left -= n;
+    if (left <= 0) return;
+    first = 0;
+    if (++u == units) {
+      u = 0;
+      tiles = tiles_of(++b);
+    }
+    n = min_(tiles, left);
+  }
+
+ private:
+  GQA_HD static int min_(int x, int y) { return x < y ? x : y; }
+};
+
+// Slots of partial results: a CTA has at most two pieces that are not whole units, the one its
+// range starts in the middle of (slot 2c) and the one that runs on past its range (2c + 1).  The
+// pieces of a cut unit are slot 2f + 1 of its first CTA f and slots 2c of the CTAs after it.
+GQA_HD int partial_slot(int cta, bool from_the_middle) { return 2 * cta + (from_the_middle ? 0 : 1); }
+
+}  // namespace gqa

@@ -2,6 +2,8 @@
 // code (no device code here).
 #pragma once
 
+#include <vector_types.h>
+
 #include <cstdint>
 
 namespace gqa {
@@ -93,13 +95,26 @@ struct CacheAttnParams {
   int n_new;               // keys behind kv_len[b] (the call's own positions; at most T)
   const uint32_t* mask;    // [B, T, ceil(T / 32)] visibility bits of the n_new keys; null: all visible
   const int* kv_len;       // [B]
-  const void* q;           // [B, T, 512 n_kv] bf16
-  const void* k;           // caches [B, S_max, n_kv, 128] bf16
-  const void* v;
   void* h;                 // [B, T, 512 n_kv] bf16
   float* weights;          // [B, n_kv, S_max] accumulated key weights (T = 1), or null
   int* status;
+  int fault;               // test hook: CTA 0 issues no loads (its waits run out)
   float scale_log2;        // log2(e) / sqrt(128)
+  // rows: a kv head's T positions in row_groups groups of group_pos (32, or 64 on two row tiles)
+  int row_groups, group_pos;
+  // scratch: per CTA the unit it began and did not finish (sequence or -1, unit, last CTA), the
+  // partial results of cut units [2 CTAs][32 float4 columns][part_rows] and their (maximum, sum)
+  int4* merge;
+  float* part_o;
+  float2* part_ml;
+  int part_rows;
+  // with weights: scores [tile][4 heads][128 keys], each tile's (unit, index in it), each unit's
+  // (first, last CTA) and, for whole units, each head's (maximum, sum)
+  float* scores;
+  int2* tile_unit;
+  int2* unit_ctas;
+  float2* unit_ml;
+  int* total_tiles;
 };
 
 // The accepted path of each sequence moved to the front of its drafted positions.
