@@ -371,11 +371,12 @@ enum {
     GQA_KERNEL_OUT_SPLITK = 5,     /* the same for few tokens */
     GQA_KERNEL_RMS_NORM = 6,       /* 1 / rms of each token row (residual form only) */
     GQA_KERNEL_CACHE_ATTN = 7,     /* tree attention / decode attention with key weights */
-    GQA_KERNEL_CACHE_FINISH = 8,   /* its merge of split sequences; accumulation of the key weights */
-    GQA_KERNEL_CACHE_COMMIT = 9,   /* accepted path moved behind the prefix */
-    GQA_KERNEL_EVICT_SELECT = 10,  /* positions that an eviction keeps */
-    GQA_KERNEL_EVICT_MOVE = 11,    /* their keys and values moved */
-    GQA_KERNEL_KINDS = 12
+    GQA_KERNEL_CACHE_MERGE = 8,    /* its merge of sequences that several workers share */
+    GQA_KERNEL_CACHE_WEIGHTS = 9,  /* accumulation of the key weights */
+    GQA_KERNEL_CACHE_COMMIT = 10,  /* accepted path moved behind the prefix */
+    GQA_KERNEL_EVICT_SELECT = 11,  /* positions that an eviction keeps */
+    GQA_KERNEL_EVICT_MOVE = 12,    /* their keys and values moved */
+    GQA_KERNEL_KINDS = 13
 };
 
 /*
@@ -472,14 +473,14 @@ gqa_status attn_debug_pair_schedule(int m_tiles, int n_tiles, int n_pairs, int *
 
 /*
  * attn_debug_cache_schedule — how tree attention and attn_decode_attention_weights share the
- * 128-key tiles of B sequences among n_ctas CTAs, computed on the host by the code that the
- * kernel runs (for tests, no GPU needed).  lens [B] (host), n_new keys behind each length, units
- * (kv heads x groups of query rows) per sequence.  Writes the pieces in order as septuples (CTA,
- * sequence, unit, first tile, tiles, slot of its partial result or -1 for a whole unit, last CTA
- * of the unit) into pieces[7 * max_pieces]; *n_pieces gets their count.  Errors:
+ * 128-key tiles of B sequences among `workers` workers (CTAs or their softmax slots), computed
+ * on the host by the code that the kernel runs (for tests, no GPU needed).  lens [B] (host), n_new
+ * keys behind each length, units (kv heads x groups of query rows) per sequence.  Writes the
+ * pieces in order as septuples (worker, sequence, unit, first tile, tiles, slot of its partial
+ * result or -1 for a whole unit, last worker of the unit) into pieces[7 * max_pieces]; *n_pieces gets their count.  Errors:
  * GQA_ERR_INVALID_ARG, GQA_ERR_SHAPE (more than max_pieces pieces; *n_pieces holds the count).
  */
-gqa_status attn_debug_cache_schedule(const int *lens, int B, int n_new, int S_max, int units, int n_ctas,
+gqa_status attn_debug_cache_schedule(const int *lens, int B, int n_new, int S_max, int units, int workers,
                                      int *pieces, int max_pieces, int *n_pieces);
 
 /*

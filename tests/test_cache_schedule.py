@@ -1,5 +1,5 @@
 """How the attention over caches of per-sequence length shares its key tiles (host computation, the
-code the kernel runs; no GPU needed): every tile of every unit is taken once, in order, the CTAs'
+code the kernel runs; no GPU needed): every tile of every unit is taken once, in order, the workers'
 shares differ by at most a tile, and the partial results of a cut unit lie in slots that no other
 unit uses."""
 import random
@@ -14,13 +14,13 @@ def _built():
     _build.build()
 
 
-def check(lens, n_new, S_max, units, n_ctas):
-    pieces = abi.attn_debug_cache_schedule(lens, n_new, S_max, units, n_ctas)
+def check(lens, n_new, S_max, units, workers):
+    pieces = abi.attn_debug_cache_schedule(lens, n_new, S_max, units, workers)
     tiles = [max(1, -(-(n + n_new) // 128)) if 0 <= n <= S_max - n_new else 1 for n in lens]
     want = [(b, u, t) for b in range(len(lens)) for u in range(units) for t in range(tiles[b])]
     got = [(b, u, t) for _, b, u, first, n, _, _ in pieces for t in range(first, first + n)]
     assert got == want
-    load = [0] * min(n_ctas, len(want))
+    load = [0] * min(workers, len(want))
     for c, *_, n, _, _ in pieces:
         load[c] += n
     assert max(load) - min(load) <= 1
@@ -40,13 +40,13 @@ def check(lens, n_new, S_max, units, n_ctas):
         assert parts[0][1] == 0 and len(parts) >= 2
 
 
-@pytest.mark.parametrize("n_ctas", [1, 2, 7, 148, 152])
+@pytest.mark.parametrize("workers", [1, 2, 7, 148, 152])
 @pytest.mark.parametrize("lens", [[0], [1], [127], [128], [129], [32000], [0, 0, 0], [5, 4000, 128, 1], [-1, 70, 2 ** 31 - 1],
                                   [300] * 33])
-def test_small_batches(lens, n_ctas):
+def test_small_batches(lens, workers):
     for units in (1, 8, 16, 32):
         for n_new in (0, 1, 26):
-            check(lens, n_new, 40000, units, n_ctas)
+            check(lens, n_new, 40000, units, workers)
 
 
 def test_random_batches():
@@ -58,8 +58,8 @@ def test_random_batches():
 
 
 def test_arguments():
-    for kw in (dict(units=0), dict(n_ctas=0), dict(n_new=-1), dict(S_max=0)):
-        a = dict(n_new=1, S_max=10, units=1, n_ctas=2) | kw
+    for kw in (dict(units=0), dict(workers=0), dict(n_new=-1), dict(S_max=0)):
+        a = dict(n_new=1, S_max=10, units=1, workers=2) | kw
         with pytest.raises(abi.GQAError):
             abi.attn_debug_cache_schedule([1], **a)
     with pytest.raises(abi.GQAError):

@@ -29,7 +29,7 @@ EXPORTED = ("attn_create", "attn_create_shard", "attn_prefill", "attn_decode", "
 
 # Kernel kinds of attn_profile_end (GQA_KERNEL_* in include/gqa_attn.h).
 KERNEL_KINDS = ("qkv_gemm", "qkv_splitk", "flash_prefill", "decode_attn", "out_gemm", "out_splitk",
-                "rms_norm", "cache_attn", "cache_finish", "cache_commit", "evict_select", "evict_move")
+                "rms_norm", "cache_attn", "cache_merge", "cache_weights", "cache_commit", "evict_select", "evict_move")
 
 _lib = None
 
@@ -125,8 +125,12 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
+        # the current stream's handle as torch.cuda.current_stream().cuda_stream gives it, without
+        # building a Stream object (3 us of a call's host time)
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -319,19 +323,20 @@ def attn_cache_evict(ctx, cache_k, cache_v, weights, B, S_max, kv_len, budget, n
                                   _ptr(out_weights), int(S_out), _ptr(kept), _ptr(new_len), _stream(stream)))
 
 
-def attn_debug_cache_schedule(lens, n_new, S_max, units, n_ctas):
-    """The pieces in which CTAs share the sequences' key tiles (host computation, no GPU needed):
-    a list of (CTA, sequence, unit, first tile, tiles, partial slot or -1, unit's last CTA)."""
+def attn_debug_cache_schedule(lens, n_new, S_max, units, workers):
+    """The pieces in which workers share the sequences' key tiles (host computation, no GPU
+    needed): a list of (worker, sequence, unit, first tile, tiles, partial slot or -1, the unit's
+    last worker)."""
     i32 = ctypes.c_int
     B = len(lens)
     arr, n = (i32 * B)(*lens), i32()
     L = lib()
-    st = L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, n_ctas, None, 0, ctypes.byref(n))
+    st = L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, workers, None, 0, ctypes.byref(n))
     if st not in (0, 2):  # GQA_ERR_SHAPE: the count is in n
         _check("attn_debug_cache_schedule", st)
     buf = (i32 * (7 * max(n.value, 1)))()
     _check("attn_debug_cache_schedule",
-           L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, n_ctas, buf, n.value, ctypes.byref(n)))
+           L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, workers, buf, n.value, ctypes.byref(n)))
     return [tuple(buf[7 * i:7 * i + 7]) for i in range(n.value)]
 
 

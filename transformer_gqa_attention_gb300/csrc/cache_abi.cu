@@ -32,7 +32,7 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   p.status = c->status;
   p.scale_log2 = kScaleLog2;
   // up to 32 positions fill one 128-row tile; more run on two tiles that share each key tile
-  p.group_pos = a.T <= 32 ? 32 : 64;
+  p.group_pos = a.T <= kFewPos ? kFewPos : a.T <= 32 ? 32 : 64;
   p.row_groups = (a.T + p.group_pos - 1) / p.group_pos;
   p.part_rows = static_cast<int>(round_up(4 * std::min(a.T, p.group_pos), 32));
 
@@ -42,18 +42,20 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
     off = round_up(off + bytes, 256);
     return at;
   };
-  const size_t slots = 2 * static_cast<size_t>(n_ctas);
-  const size_t merge = take(n_ctas * sizeof(int4));
+  // workers: CTAs, or with one row tile their softmax slots; each may hold two partial results
+  const size_t workers = static_cast<size_t>(n_ctas) * (p.group_pos > 32 ? 1 : 2);
+  const size_t slots = 2 * workers;
+  const size_t merge = take(workers * sizeof(int4));
   const size_t part_ml = take(slots * p.part_rows * sizeof(float2));
   const size_t part_o = take(slots * p.part_rows * 128 * sizeof(float));
-  size_t total = 0, scores = 0, tile_unit = 0, unit_ctas = 0, unit_ml = 0;
+  size_t total = 0, scores = 0, tile_unit = 0, unit_workers = 0, unit_ml = 0;
   if (a.weights) {
     const size_t units = static_cast<size_t>(a.B) * G;
     const size_t tiles = units * ((a.S_max + kKvTile - 1) / kKvTile);
     total = take(sizeof(int));
     scores = take(tiles * 4 * kKvTile * sizeof(float));
     tile_unit = take(tiles * sizeof(int2));
-    unit_ctas = take(units * sizeof(int2));
+    unit_workers = take(units * sizeof(int2));
     unit_ml = take(units * 4 * sizeof(float2));
   }
   gqa_status st = ensure_buffer(c, c->cache_ws, off, s);
@@ -66,15 +68,15 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
     p.total_tiles = reinterpret_cast<int*>(ws + total);
     p.scores = reinterpret_cast<float*>(ws + scores);
     p.tile_unit = reinterpret_cast<int2*>(ws + tile_unit);
-    p.unit_ctas = reinterpret_cast<int2*>(ws + unit_ctas);
+    p.unit_workers = reinterpret_cast<int2*>(ws + unit_workers);
     p.unit_ml = reinterpret_cast<float2*>(ws + unit_ml);
   }
 
   CUtensorMap tq, tk, tv;
-  // queries as (d, head, position, sequence): a box is 64 d of the group's 4 heads at 32 positions
+  // queries as (d, head, position, sequence): a box is 64 d of the group's 4 heads
   const uint64_t dims[4] = {128, 4ull * G, static_cast<uint64_t>(a.T), static_cast<uint64_t>(a.B)};
   const uint64_t strides[3] = {256, static_cast<uint64_t>(G) * 1024, static_cast<uint64_t>(a.T) * G * 1024};
-  const uint32_t box[4] = {64, 4, 32, 1};
+  const uint32_t box[4] = {64, 4, static_cast<uint32_t>(cache_attn_box(p)), 1};
   if (!make_map(&tq, a.q, 4, dims, strides, box) ||
       !map_cache(&tk, a.cache_k, a.B, a.S_max, G, a.S_max, kKvTile) ||
       !map_cache(&tv, a.cache_v, a.B, a.S_max, G, a.S_max, kKvTile))
@@ -85,8 +87,12 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
     GQA_CUDA(launch_cache_attn(tq, tk, tv, p, n_ctas, s));
   }
   {
-    ProfScope ps(c, GQA_KERNEL_CACHE_FINISH, s);
-    GQA_CUDA(launch_cache_finish(p, n_ctas, s));
+    ProfScope ps(c, GQA_KERNEL_CACHE_MERGE, s);
+    GQA_CUDA(launch_cache_merge(p, static_cast<int>(workers), 2 * c->num_sms, s));
+  }
+  if (a.weights) {
+    ProfScope ps(c, GQA_KERNEL_CACHE_WEIGHTS, s);
+    GQA_CUDA(launch_cache_weights(p, 4 * c->num_sms, s));
   }
   return GQA_OK;
 }
@@ -246,26 +252,25 @@ gqa_status attn_cache_evict(gqa_ctx* c, const void* cache_k, const void* cache_v
   return GQA_OK;
 }
 
-gqa_status attn_debug_cache_schedule(const int* lens, int B, int n_new, int S_max, int units, int n_ctas, int* pieces,
+gqa_status attn_debug_cache_schedule(const int* lens, int B, int n_new, int S_max, int units, int workers, int* pieces,
                                      int max_pieces, int* n_pieces) {
   if (!lens || !n_pieces || (!pieces && max_pieces > 0) || B < 1 || n_new < 0 || S_max < 1 || units < 1 ||
-      n_ctas < 1 || max_pieces < 0)
+      workers < 1 || max_pieces < 0)
     return GQA_ERR_INVALID_ARG;
-  auto tiles_of = [&](int b) { return b < B ? kv_tiles(kv_end(lens[b], n_new, S_max)) : 1; };
-  long long total = 0;
-  for (int b = 0; b < B; ++b) total += static_cast<long long>(tiles_of(b)) * units;
-  if (total > 0x7FFFFFFF) return GQA_ERR_SHAPE;
+  auto len_of = [&](int b) { return b < B ? lens[b] : 0; };
+  auto tiles_of = [&](int b) { return kv_tiles(kv_end(len_of(b), n_new, S_max)); };
+  long long all = 0;
+  for (int b = 0; b < B; ++b) all += static_cast<long long>(tiles_of(b)) * units;
+  if (all > 0x7FFFFFFF) return GQA_ERR_SHAPE;
+  const int total = static_cast<int>(all), n_work = range_workers(total, workers);
   int n = 0;
-  n_ctas = range_ctas(static_cast<int>(total), n_ctas);
-  for (int c = 0; c < n_ctas; ++c) {
-    const int lo = range_start(static_cast<int>(total), n_ctas, c);
-    const int hi = range_start(static_cast<int>(total), n_ctas, c + 1);
+  for (int c = 0; c < n_work; ++c) {
+    const int lo = range_start(total, n_work, c), hi = range_start(total, n_work, c + 1);
     int b = 0, at = 0;
     while (at + tiles_of(b) * units <= lo) at += tiles_of(b++) * units;
     KvWalk w;
     int flat = lo;
-    for (w.start(b, lo - at, tiles_of(b), units, hi - lo); !w.done(); w.next(tiles_of), ++n) {
-      const int last = range_owner(static_cast<int>(total), n_ctas, flat - w.first + w.tiles - 1);
+    for (w.start(b, lo - at, len_of(b), n_new, S_max, hi - lo); !w.done(); w.next(units, n_new, S_max, len_of), ++n) {
       if (n < max_pieces) {
         int* o = pieces + 7 * n;
         o[0] = c;
@@ -274,7 +279,7 @@ gqa_status attn_debug_cache_schedule(const int* lens, int B, int n_new, int S_ma
         o[3] = w.first;
         o[4] = w.n;
         o[5] = w.whole() ? -1 : partial_slot(c, w.first > 0);
-        o[6] = last;
+        o[6] = range_owner(total, n_work, flat - w.first + w.tiles - 1);
       }
       flat += w.n;
     }

@@ -1,0 +1,411 @@
+// cache_roles.cuh — what the kernels of the attention over caches of per-sequence length share: the
+// barriers, the search for a CTA's ranges of key tiles, the order in which its roles walk them, and
+// the roles that do not depend on how the products are laid out (TMA producers, and the warp that
+// clears V rows which nobody sees).
+//
+// Warps of a CTA (384 threads):
+//   warp 0      TMA producer of the 128-key K tiles, running ahead over the ends of units
+//   warp 1      TMEM owner and UMMA issuer
+//   warp 2      zeroes the rows of a V tile that no row sees (past the end of the sequence, or
+//               drafted positions that nobody's mask names): their weight is 0, but 0 x NaN is not
+//   warp 3      TMA producer of the V tiles (a tile's V is needed a softmax later than its K) and
+//               of each unit's queries, once the last S of the unit before has read its own
+//   warps 4..7, 8..11  two softmax slots
+// A CTA has kWork workers (kv_sched.h): two, one per softmax slot, or one whose slots share every
+// key tile.
+#pragma once
+
+#include <type_traits>
+
+#include "kv_sched.h"
+#include "params.h"
+#include "ptx.cuh"
+
+namespace gqa {
+
+constexpr int kKvTileBytes = kKvTile * 128 * 2;  // 128 keys x 128 bf16, two 64-column halves
+constexpr int kKvHalfBytes = kKvTileBytes / 2;
+constexpr int kKStages = 2;
+constexpr int kVStages = 3;
+
+struct CacheBars {
+  static constexpr int kCount = 28;
+  static constexpr int kBytes = 256;  // barriers, TMEM address, abort flag
+  uint64_t* bars;
+  __device__ __forceinline__ explicit CacheBars(uint8_t* at) : bars(reinterpret_cast<uint64_t*>(at)) {}
+  __device__ __forceinline__ uint64_t* q_full(int slot) const { return bars + slot; }
+  __device__ __forceinline__ uint64_t* q_empty(int slot) const { return bars + 2 + slot; }
+  __device__ __forceinline__ uint64_t* k_full(int stage) const { return bars + 4 + stage; }
+  __device__ __forceinline__ uint64_t* k_empty(int stage) const { return bars + 6 + stage; }
+  __device__ __forceinline__ uint64_t* v_full(int stage) const { return bars + 8 + stage; }
+  __device__ __forceinline__ uint64_t* v_fixed(int stage) const { return bars + 11 + stage; }
+  __device__ __forceinline__ uint64_t* s_full(int slot) const { return bars + 14 + slot; }
+  __device__ __forceinline__ uint64_t* o_full(int slot) const { return bars + 16 + slot; }
+  __device__ __forceinline__ uint64_t* drain() const { return bars + 18; }
+  // 2 arrivals: the PV that used the tile, and warp 2
+  __device__ __forceinline__ uint64_t* v_empty(int stage) const { return bars + 19 + stage; }
+  // 128 arrivals: P of the tile's first and second 64 keys (or of all of them: lo), O of the piece read
+  __device__ __forceinline__ uint64_t* p_lo(int slot) const { return bars + 22 + slot; }
+  __device__ __forceinline__ uint64_t* p_hi(int slot) const { return bars + 24 + slot; }
+  __device__ __forceinline__ uint64_t* o_empty(int slot) const { return bars + 26 + slot; }
+  __device__ __forceinline__ uint32_t* tmem_holder() const { return reinterpret_cast<uint32_t*>(bars + kCount); }
+  __device__ __forceinline__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(tmem_holder() + 1); }
+  __device__ __forceinline__ void init() const {
+    for (int i = 0; i < kCount; ++i) mbar_init(&bars[i], i < 19 ? 1u : i < 22 ? 2u : 128u);
+    *abort_flag() = 0;
+    fence_mbar_init();
+  }
+};
+
+// The CTA's ranges of key tiles, in shared memory: thread i sums the tiles of sequences i per ..
+// i per + per - 1 (B <= 1024: per <= 3); a scan over the CTA gives the total and finds where the
+// ranges start and where their last tiles lie.  Called by all 384 threads; also publishes, for the
+// merge, the unit that each worker begins and does not finish.
+struct CacheRanges {
+  static constexpr int kBytes = 128;
+  int* scan;   // [12] per-warp sums
+  int* where;  // total, workers, then per worker: first tile, tiles, sequence, offset in it, its length
+
+  __device__ __forceinline__ explicit CacheRanges(uint8_t* at) : scan(reinterpret_cast<int*>(at)), where(scan + 16) {}
+  __device__ __forceinline__ int total() const { return where[0]; }
+  __device__ __forceinline__ int workers() const { return where[1]; }
+  __device__ __forceinline__ int first_tile(int s) const { return where[2 + 5 * s]; }
+  __device__ __forceinline__ KvWalk walk(int s, const CacheAttnParams& p) const {
+    KvWalk w;
+    w.left = where[3 + 5 * s];
+    if (w.left > 0) w.start(where[4 + 5 * s], where[5 + 5 * s], where[6 + 5 * s], p.n_new, p.S_max, w.left);
+    return w;
+  }
+
+  template <int kWork>
+  __device__ __forceinline__ void find(const CacheAttnParams& p) const {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int units = p.n_kv * p.row_groups;
+    const int per = (p.B + 383) / 384;
+    const int b0 = threadIdx.x * per;
+    int lens[3], tiles[3], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const bool in = i < per && b0 + i < p.B;
+      lens[i] = in ? __ldcg(p.kv_len + b0 + i) : 0;
+      tiles[i] = in ? kv_tiles(kv_end(lens[i], p.n_new, p.S_max)) : 0;
+      mine += tiles[i] * units;
+    }
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    int before = x - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < 12; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    const int n_work = range_workers(total, kWork * gridDim.x);
+    if (threadIdx.x == 0) {
+      where[0] = total;
+      where[1] = n_work;
+      if (p.total_tiles && blockIdx.x == 0) *p.total_tiles = total;
+    }
+#pragma unroll
+    for (int s = 0; s < kWork; ++s) {
+      const int v = kWork * blockIdx.x + s;
+      const int lo = v < n_work ? range_start(total, n_work, v) : total;
+      const int hi = v < n_work ? range_start(total, n_work, v + 1) : total;
+      if (threadIdx.x == 0) {
+        where[2 + 5 * s] = lo;
+        where[3 + 5 * s] = hi - lo;
+        if (hi == lo) p.merge[v] = make_int4(-1, 0, 0, 0);
+      }
+      if (hi == lo || lo >= before + mine || hi - 1 < before) continue;
+      int at = before;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int n = tiles[i] * units;
+        if (n > 0 && lo >= at && lo < at + n) {
+          where[4 + 5 * s] = b0 + i;
+          where[5 + 5 * s] = lo - at;
+          where[6 + 5 * s] = lens[i];
+        }
+        if (n > 0 && hi - 1 >= at && hi - 1 < at + n) {  // the last tile's unit: cut by the range's end?
+          const int u = (hi - 1 - at) / tiles[i];
+          const int u_lo = at + u * tiles[i], u_hi = u_lo + tiles[i];
+          p.merge[v] = u_hi > hi && u_lo >= lo ? make_int4(b0 + i, u, range_owner(total, n_work, u_hi - 1), 0)
+                                               : make_int4(-1, 0, 0, 0);
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+  }
+};
+
+// One worker's place in its range.
+struct CacheLane {
+  KvWalk w;
+  int j, piece;  // tile inside the piece, piece
+};
+
+// A CTA's tiles in the order in which every role takes them: the workers in turn.
+template <int kWork>
+struct CacheTiles {
+  const CacheAttnParams& p;
+  CacheLane l0, l1;
+  __device__ __forceinline__ CacheTiles(const CacheAttnParams& p_, const CacheRanges& r)
+      : p(p_), l0{r.walk(0, p_), 0, 0}, l1{r.walk(kWork - 1, p_), 0, 0} {}
+  __device__ __forceinline__ void advance(CacheLane& l) {
+    if (++l.j == l.w.n) {
+      l.j = 0;
+      ++l.piece;
+      l.w.next(p.n_kv * p.row_groups, p.n_new, p.S_max, [&](int b) { return __ldcg(p.kv_len + b); });
+    }
+  }
+  // step(slot constant, lane) -> go on; false if a step gave up
+  template <typename F>
+  __device__ __forceinline__ bool each(F step) {
+    while (true) {
+      const bool d0 = l0.w.done(), d1 = kWork == 1 || l1.w.done();
+      if (d0 && d1) return true;
+      if (!d0) {
+        if (!step(std::integral_constant<int, 0>{}, l0)) return false;
+        advance(l0);
+      }
+      if (!d1) {
+        if (!step(std::integral_constant<int, 1>{}, l1)) return false;
+        advance(l1);
+      }
+    }
+  }
+};
+
+// Lane 0 of warp 0.
+template <int kWork>
+__device__ __forceinline__ void produce_k(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
+                                          const CUtensorMap* tmK, uint8_t* ring) {
+  CacheTiles<kWork> tiles(p, ranges);
+  volatile int* abort_flag = bar.abort_flag();
+  int it = 0;
+  tiles.each([&](auto, CacheLane& l) {
+    const int st = it % kKStages;
+    if (!mbar_wait(bar.k_empty(st), ((it / kKStages) & 1) ^ 1u, abort_flag, p.status)) return false;
+    mbar_arrive_expect_tx(bar.k_full(st), kKvTileBytes);
+    uint8_t* dst = ring + st * kKvTileBytes;
+    const int g = l.w.u / p.row_groups, key0 = (l.w.first + l.j) * kKvTile;
+    tma_load_4d(dst, tmK, bar.k_full(st), 0, g, key0, l.w.b);
+    tma_load_4d(dst + kKvHalfBytes, tmK, bar.k_full(st), 64, g, key0, l.w.b);
+    ++it;
+    return true;
+  });
+  if (*abort_flag)  // let copies still in flight land before the CTA leaves
+    for (int i = max(0, it - kKStages); i < it; ++i) mbar_wait_drain(bar.k_full(i % kKStages), (i / kKStages) & 1);
+}
+
+// Lane 0 of warp 3.  A slot's queries are q_rows rows (positions x 4 heads; the box of tmQ) in two
+// halves of 64 columns, q_half bytes apart; a unit has kSlots = 2 / kWork slots of them.
+template <int kWork>
+__device__ __forceinline__ void produce_vq(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
+                                           const CUtensorMap* tmQ, const CUtensorMap* tmV, uint8_t* q, int q_rows,
+                                           int q_half, uint8_t* ring) {
+  constexpr int kSlots = 2 / kWork;
+  CacheTiles<kWork> tiles(p, ranges);
+  volatile int* abort_flag = bar.abort_flag();
+  int it = 0, asked = 0;  // queries asked for: slot 0 in the low half, slot 1 in the high
+  tiles.each([&](auto S, CacheLane& l) {
+    const int g = l.w.u / p.row_groups;
+    if (l.j == 0) {
+      const int t0 = (l.w.u - g * p.row_groups) * p.group_pos;
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        const int slot = kWork == 1 ? i : S.value;
+        if (l.piece > 0 && !mbar_wait(bar.q_empty(slot), (l.piece - 1) & 1, abort_flag, p.status)) return false;
+        mbar_arrive_expect_tx(bar.q_full(slot), q_rows * 256);
+        uint8_t* dst = q + slot * 2 * q_half;
+        tma_load_4d(dst, tmQ, bar.q_full(slot), 0, 4 * g, t0 + 32 * i, l.w.b);
+        tma_load_4d(dst + q_half, tmQ, bar.q_full(slot), 64, 4 * g, t0 + 32 * i, l.w.b);
+        asked += slot ? 0x10000 : 1;
+      }
+    }
+    const int st = it % kVStages;
+    if (!mbar_wait(bar.v_empty(st), ((it / kVStages) & 1) ^ 1u, abort_flag, p.status)) return false;
+    mbar_arrive_expect_tx(bar.v_full(st), kKvTileBytes);
+    uint8_t* dst = ring + st * kKvTileBytes;
+    const int key0 = (l.w.first + l.j) * kKvTile;
+    tma_load_4d(dst, tmV, bar.v_full(st), 0, g, key0, l.w.b);
+    tma_load_4d(dst + kKvHalfBytes, tmV, bar.v_full(st), 64, g, key0, l.w.b);
+    ++it;
+    return true;
+  });
+  if (*abort_flag) {
+    for (int i = max(0, it - kVStages); i < it; ++i) mbar_wait_drain(bar.v_full(i % kVStages), (i / kVStages) & 1);
+    if (asked & 0xFFFF) mbar_wait_drain(bar.q_full(0), ((asked & 0xFFFF) - 1) & 1);
+    if (asked >> 16) mbar_wait_drain(bar.q_full(1), ((asked >> 16) - 1) & 1);
+  }
+}
+
+// Keys of the sequence that every row sees (a length out of range: none).
+__device__ __forceinline__ int keys_all_see(const CacheAttnParams& p, int len) {
+  return kv_end(len, p.n_new, p.S_max) < 0 ? 0 : len;
+}
+
+// Whole warp 2.  A tile needs it if it reaches past the keys that every row sees.
+template <int kWork>
+__device__ __forceinline__ void clear_v(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
+                                        uint8_t* ring) {
+  CacheTiles<kWork> tiles(p, ranges);
+  volatile int* abort_flag = bar.abort_flag();
+  const int lane = threadIdx.x & 31;
+  const int W = (p.T + 31) / 32;
+  int it = 0, seen_b = -1;
+  uint32_t seen = 0;  // drafted positions of sequence seen_b that some row sees: word i in lane i
+  tiles.each([&](auto, CacheLane& l) {
+    const int end = kv_end(l.w.len, p.n_new, p.S_max);
+    const int safe = keys_all_see(p, l.w.len);
+    const int key0 = (l.w.first + l.j) * kKvTile;
+    const bool fix = key0 + kKvTile > safe;
+    if (fix && seen_b != l.w.b) {
+      seen_b = l.w.b;
+      seen = 0xFFFFFFFFu;
+      if (p.mask && end >= 0) {
+        const uint32_t* m = p.mask + static_cast<size_t>(seen_b) * p.T * W;
+        seen = 0u;
+        for (int i = 0; i < W; ++i) {
+          uint32_t a = 0u;
+          for (int t = lane; t < p.T; t += 32) a |= __ldcg(m + t * W + i);
+          a = __reduce_or_sync(0xffffffffu, a);
+          if (lane == i) seen = a;
+        }
+      }
+    }
+    // every tile is waited for and released, so that this warp stays in step with the ring
+    const int st = it % kVStages;
+    if (!__all_sync(0xffffffffu, mbar_wait(bar.v_full(st), (it / kVStages) & 1, abort_flag, p.status))) return false;
+    if (fix) {
+      uint8_t* tile = ring + st * kKvTileBytes;
+      for (int r0 = 0; r0 < kKvTile; r0 += 32) {
+        const int d = key0 + r0 + lane - safe;  // drafted index of this lane's row
+        const uint32_t word = __shfl_sync(0xffffffffu, seen, (d >> 5) & 7);
+        const bool dead = d >= 0 && (end < 0 || d >= p.n_new || !((word >> (d & 31)) & 1u));
+        uint32_t todo = __ballot_sync(0xffffffffu, dead);
+        while (todo) {  // two rows at a time, 16 lanes each (a row is 8 chunks in either half)
+          const int ra = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const int rb = todo ? __ffs(todo) - 1 : ra;
+          todo &= todo - 1;
+          const int r = r0 + (lane < 16 ? ra : rb), c = lane & 15;
+          *reinterpret_cast<uint4*>(tile + (c >> 3) * kKvHalfBytes + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.v_fixed(st));
+    }
+    if (lane == 0) mbar_arrive(bar.v_empty(st));
+    ++it;
+    return true;
+  });
+}
+
+// The whole of warp 1.  In turn for each tile and slot: S (issued by `issue_s`), then the PV of the
+// item before (`issue_pv`), so that the tensor core works while a softmax runs.
+//   issue_s(slot, K stage): the UMMAs of S;  issue_pv(slot, V stage, half, first): those of O += P V
+//   for keys 64 half .. + 63 (kHalves = 2) or all keys (kHalves = 1), O anew if first.
+template <int kWork, int kHalves, typename FS, typename FP>
+__device__ __forceinline__ void issue_all(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
+                                          FS issue_s, FP issue_pv_mma) {
+  CacheTiles<kWork> tiles(p, ranges);
+  volatile int* abort_flag = bar.abort_flag();
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.status));
+  };
+  uint32_t fix_par = 0;  // bit v: parity of V stage v's next v_fixed
+  uint32_t p_par = 0;    // bit i: parity of slot i's next P
+  struct Pending {
+    int slot, it, piece;             // softmax slot, tile count, the slot's piece
+    bool first, last, fix, release;  // first / last tile of the piece; V tile to be cleared; V tile done
+  } pend{};
+  bool has_pend = false;
+  auto issue_pv = [&] {
+    const Pending d = pend;
+    has_pend = false;
+    const int vs = d.it % kVStages;
+    // a new O takes the place of the last piece's
+    if (d.first && d.piece > 0 && !wait(bar.o_empty(d.slot), (d.piece - 1) & 1)) return false;
+    if (!wait(bar.v_full(vs), (d.it / kVStages) & 1)) return false;
+    if (d.fix) {
+      if (!wait(bar.v_fixed(vs), (fix_par >> vs) & 1)) return false;
+      fix_par ^= 1u << vs;
+    }
+    const uint32_t ph = (p_par >> d.slot) & 1;
+    p_par ^= 1u << d.slot;
+#pragma unroll
+    for (int hf = 0; hf < kHalves; ++hf) {
+      if (!wait(hf ? bar.p_hi(d.slot) : bar.p_lo(d.slot), ph)) return false;
+      tc_fence_after();
+      if (elect_one_sync()) {
+        issue_pv_mma(d.slot, vs, hf, d.first);
+        if (hf == kHalves - 1) {
+          if (d.release) umma_commit(bar.v_empty(vs));
+          if (d.last) umma_commit(bar.o_full(d.slot));
+        }
+      }
+      __syncwarp();
+    }
+    return true;
+  };
+  int it = 0;
+  const bool ok = tiles.each([&](auto S, CacheLane& l) {
+    const bool fix = (l.w.first + l.j + 1) * kKvTile > keys_all_see(p, l.w.len);
+    const bool first = l.j == 0, last = l.j == l.w.n - 1;
+    const int ks = it % kKStages;
+#pragma unroll
+    for (int i = 0; i < 2 / kWork; ++i) {
+      const int slot = kWork == 1 ? i : S.value;
+      // P of the slot's last tile is used up before the softmax of S takes its place (the other
+      // worker has no more tiles in between)
+      if (has_pend && pend.slot == slot && !issue_pv()) return false;
+      if (first && !wait(bar.q_full(slot), l.piece & 1)) return false;
+      if (i == 0 && !wait(bar.k_full(ks), (it / kKStages) & 1)) return false;
+      tc_fence_after();
+      const bool last_slot = kWork == 2 || i == 1;
+      if (elect_one_sync()) {
+        issue_s(slot, ks);
+        umma_commit(bar.s_full(slot));
+        if (last_slot) umma_commit(bar.k_empty(ks));
+        if (last) umma_commit(bar.q_empty(slot));
+      }
+      __syncwarp();
+      if (has_pend && !issue_pv()) return false;
+      pend = Pending{slot, it, l.piece, first, last, fix && i == 0, last_slot};
+      has_pend = true;
+    }
+    ++it;
+    return true;
+  });
+  if (ok && has_pend) issue_pv();
+  if (__any_sync(0xffffffffu, *abort_flag != 0)) {  // let issued UMMAs finish before TMEM is released
+    if (elect_one_sync()) umma_commit(bar.drain());
+    __syncwarp();
+    mbar_wait_drain(bar.drain(), 0);
+  }
+}
+
+// Visibility bits of the 32 keys whose drafted index starts at `base` (negative: prefix, always
+// seen) for a mask row of W words over n_new drafted positions; a row without a mask (null) that
+// is live sees all n_new.
+__device__ __forceinline__ uint32_t key_bits(const uint32_t* mask, int W, int n_new, int base, bool live) {
+  if (base <= -32) return 0xFFFFFFFFu;
+  if (base >= n_new) return 0u;
+  const int q = base >> 5;  // floor: -1 where the word straddles the prefix
+  const uint32_t none = !live ? 0u : 0xFFFFFFFFu;
+  const uint32_t lo = q < 0 ? 0xFFFFFFFFu : (mask ? (live ? __ldcg(mask + q) : 0u) : none);
+  const uint32_t hi = q + 1 < W ? (mask ? (live ? __ldcg(mask + q + 1) : 0u) : none) : 0u;
+  const uint32_t bits = __funnelshift_r(lo, hi, base & 31);
+  const int rem = n_new - base;
+  return rem < 32 ? bits & ((1u << rem) - 1u) : bits;
+}
+
+}  // namespace gqa

@@ -189,7 +189,7 @@ constexpr size_t kMaxProfiledLaunches = 65536;
 // attached an NVTX call returns at once).
 inline const char* const kKindNames[GQA_KERNEL_KINDS] = {"gqa.qkv_gemm", "gqa.qkv_splitk", "gqa.flash_prefill",
                                                   "gqa.decode_attn", "gqa.out_gemm", "gqa.out_splitk",
-                                                  "gqa.rms_norm", "gqa.cache_attn", "gqa.cache_finish", "gqa.cache_commit", "gqa.evict_select",
+                                                  "gqa.rms_norm", "gqa.cache_attn", "gqa.cache_merge", "gqa.cache_weights", "gqa.cache_commit", "gqa.evict_select",
                                                          "gqa.evict_move"};
 
 // RAII NVTX range around one entry point's host work (its launches nest inside it).

@@ -3,10 +3,11 @@
 //
 // A unit is (sequence b, kv head, group of query rows); it reads the ceil(end_b / 128) key tiles
 // of its sequence (at least one, so that every unit writes its rows).  The units' tiles, unit
-// after unit and sequence after sequence, form one row of `total` tiles, of which CTA c of n takes
-// tiles c total / n .. (c + 1) total / n - 1: equal work whatever the lengths are, without the
-// host knowing them.  What a CTA takes of one unit is a piece; a unit cut over several CTAs is
-// merged from its pieces' partial results.
+// after unit and sequence after sequence, form one row of `total` tiles, of which worker c of n
+// takes tiles c total / n .. (c + 1) total / n - 1: equal work whatever the lengths are, without
+// the host knowing them.  What a worker takes of one unit is a piece; a unit cut over several
+// workers is merged from its pieces' partial results.  A worker is a CTA, or one of a CTA's two
+// softmax slots.
 #pragma once
 
 #ifdef __CUDACC__
@@ -24,60 +25,58 @@ GQA_HD int kv_end(int len, int n_new, int S_max) { return len < 0 || len > S_max
 
 GQA_HD int kv_tiles(int end) { return end <= kKvTile ? 1 : (end + kKvTile - 1) / kKvTile; }
 
-// CTAs that share the row: no more than tiles, so that every one of them has a range and a unit's
-// pieces lie in consecutive CTAs.
-GQA_HD int range_ctas(int total, int grid) { return total < grid ? total : grid; }
+// Workers that share the row: no more than tiles, so that every one of them has a range and a
+// unit's pieces lie with consecutive workers.
+GQA_HD int range_workers(int total, int most) { return total < most ? total : most; }
 
-GQA_HD int range_start(int total, int n_ctas, int c) {
-  return static_cast<int>(static_cast<long long>(c) * total / n_ctas);
+GQA_HD int range_start(int total, int n, int c) {
+  return static_cast<int>(static_cast<long long>(c) * total / n);
 }
 
-// The CTA whose range holds tile x: the last c with range_start(c) <= x, c total < (x + 1) n.
-GQA_HD int range_owner(int total, int n_ctas, int x) {
-  return static_cast<int>(((static_cast<long long>(x) + 1) * n_ctas - 1) / total);
+// The worker whose range holds tile x: the last c with range_start(c) <= x, c total < (x + 1) n.
+GQA_HD int range_owner(int total, int n, int x) {
+  return static_cast<int>(((static_cast<long long>(x) + 1) * n - 1) / total);
 }
 
-// The pieces of one CTA's range, in order.
+// The pieces of one range, in order.
 struct KvWalk {
   int b, u;       // sequence, unit in it (kv head x row groups + row group)
+  int len;        // the sequence's length
   int tiles;      // key tiles of each of the sequence's units
   int first;      // the piece's first tile
   int n;          // its tiles
-  int left;       // tiles of the range from the piece on
-  int units;      // units of a sequence
+  int left;       // tiles of the range from the piece on (0: done)
 
   // offset: tiles of sequence b before the range's start
-  GQA_HD void start(int b_, int offset, int tiles_, int units_, int range) {
+  GQA_HD void start(int b_, int offset, int len_, int n_new, int S_max, int range) {
     b = b_;
-    units = units_;
-    tiles = tiles_;
+    len = len_;
+    tiles = kv_tiles(kv_end(len, n_new, S_max));
     u = offset / tiles;
     first = offset - u * tiles;
     left = range;
-    n = min_(tiles - first, left);
+    n = tiles - first < left ? tiles - first : left;
   }
   GQA_HD bool done() const { return left <= 0; }
   GQA_HD bool whole() const { return n == tiles; }
-  // tiles_of(b): key tiles of sequence b
+  // units of a sequence; len_of(b): its length
   template <typename F>
-  GQA_HD void next(F tiles_of) {
+  GQA_HD void next(int units, int n_new, int S_max, F len_of) {
     left -= n;
     if (left <= 0) return;
     first = 0;
     if (++u == units) {
       u = 0;
-      tiles = tiles_of(++b);
+      len = len_of(++b);
+      tiles = kv_tiles(kv_end(len, n_new, S_max));
     }
-    n = min_(tiles, left);
+    n = tiles < left ? tiles : left;
   }
-
- private:
-  GQA_HD static int min_(int x, int y) { return x < y ? x : y; }
 };
 
-// Slots of partial results: a CTA has at most two pieces that are not whole units, the one its
+// Slots of partial results: a worker has at most two pieces that are not whole units, the one its
 // range starts in the middle of (slot 2c) and the one that runs on past its range (2c + 1).  The
-// pieces of a cut unit are slot 2f + 1 of its first CTA f and slots 2c of the CTAs after it.
-GQA_HD int partial_slot(int cta, bool from_the_middle) { return 2 * cta + (from_the_middle ? 0 : 1); }
+// pieces of a cut unit are slot 2f + 1 of its first worker f and slots 2c of the workers after it.
+GQA_HD int partial_slot(int worker, bool from_the_middle) { return 2 * worker + (from_the_middle ? 0 : 1); }
 
 }  // namespace gqa

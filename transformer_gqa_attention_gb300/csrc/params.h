@@ -86,6 +86,10 @@ struct DecodeParams {
   float scale_log2;
 };
 
+// At most this many positions per sequence run with the keys, not the rows, on the tensor core's
+// 128 rows.
+constexpr int kFewPos = 16;
+
 // Attention of a few positions per sequence over caches of per-sequence length (tree attention,
 // decode attention that accumulates key weights).  Row t of sequence b sees keys 0 ..
 // kv_len[b] - 1 and, of the n_new keys behind them, those whose bit is set in mask[b, t].
@@ -100,19 +104,21 @@ struct CacheAttnParams {
   int* status;
   int fault;               // test hook: CTA 0 issues no loads (its waits run out)
   float scale_log2;        // log2(e) / sqrt(128)
-  // rows: a kv head's T positions in row_groups groups of group_pos (32, or 64 on two row tiles)
+  // rows: a kv head's T positions in row_groups groups of group_pos (16: kFewPos, 32, or 64 on two
+  // row tiles)
   int row_groups, group_pos;
-  // scratch: per CTA the unit it began and did not finish (sequence or -1, unit, last CTA), the
-  // partial results of cut units [2 CTAs][32 float4 columns][part_rows] and their (maximum, sum)
+  // scratch: per worker the unit it began and did not finish (sequence or -1, unit, last worker),
+  // the partial results of cut units ([2 workers][32 float4 columns][part_rows], or with at most
+  // kFewPos positions [2 workers][part_rows][128]) and their (maximum, sum)
   int4* merge;
   float* part_o;
   float2* part_ml;
   int part_rows;
-  // with weights: scores [tile][4 heads][128 keys], each tile's (unit, index in it), each unit's
-  // (first, last CTA) and, for whole units, each head's (maximum, sum)
+  // with weights: scores [tile][128 keys][4 heads], each tile's (unit, index in it), each unit's
+  // (first, last worker) and, for whole units, each head's (maximum, sum)
   float* scores;
   int2* tile_unit;
-  int2* unit_ctas;
+  int2* unit_workers;
   float2* unit_ml;
   int* total_tiles;
 };
