@@ -372,7 +372,7 @@ enum {
     GQA_KERNEL_RMS_NORM = 6,       /* 1 / rms of each token row (residual form only) */
     GQA_KERNEL_CACHE_ATTN = 7,     /* tree attention / decode attention with key weights */
     GQA_KERNEL_CACHE_MERGE = 8,    /* its merge of sequences that several workers share */
-    GQA_KERNEL_CACHE_WEIGHTS = 9,  /* accumulation of the key weights */
+    GQA_KERNEL_CACHE_WEIGHTS = 9,  /* with key weights: the merge and their accumulation */
     GQA_KERNEL_CACHE_COMMIT = 10,  /* accepted path moved behind the prefix */
     GQA_KERNEL_EVICT_SELECT = 11,  /* positions that an eviction keeps */
     GQA_KERNEL_EVICT_MOVE = 12,    /* their keys and values moved */

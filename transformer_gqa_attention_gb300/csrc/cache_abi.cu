@@ -86,13 +86,12 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
     ProfScope ps(c, GQA_KERNEL_CACHE_ATTN, s);
     GQA_CUDA(launch_cache_attn(tq, tk, tv, p, n_ctas, s));
   }
-  {
-    ProfScope ps(c, GQA_KERNEL_CACHE_MERGE, s);
-    GQA_CUDA(launch_cache_merge(p, static_cast<int>(workers), 2 * c->num_sms, s));
-  }
   if (a.weights) {
     ProfScope ps(c, GQA_KERNEL_CACHE_WEIGHTS, s);
-    GQA_CUDA(launch_cache_weights(p, 4 * c->num_sms, s));
+    GQA_CUDA(launch_cache_weights(p, static_cast<int>(workers), 4 * c->num_sms, s));
+  } else {
+    ProfScope ps(c, GQA_KERNEL_CACHE_MERGE, s);
+    GQA_CUDA(launch_cache_merge(p, static_cast<int>(workers), s));
   }
   return GQA_OK;
 }

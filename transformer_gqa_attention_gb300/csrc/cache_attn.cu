@@ -1,4 +1,6 @@
 // cache_attn.cu — instantiations of the attention over caches of per-sequence length.
+#include <algorithm>
+
 #include "cache_attn.cuh"
 #include "cache_attn_few.cuh"
 #include "launch.h"
@@ -45,14 +47,14 @@ cudaError_t launch_cache_attn(const CUtensorMap& q, const CUtensorMap& k, const 
   return launch_pdl(kAttn[i], dim3(n_ctas), dim3(384), smem_of(i), s, 0, q, k, v, p);
 }
 
-cudaError_t launch_cache_merge(const CacheAttnParams& p, int workers, int n_blocks, cudaStream_t s) {
-  if (workers > kMergeMax) return cudaErrorInvalidValue;
-  if (p.T <= kFewPos) return launch_pdl(cache_merge_kernel<true>, dim3(n_blocks), dim3(256), 0, s, 0, p, workers);
-  return launch_pdl(cache_merge_kernel<false>, dim3(n_blocks), dim3(256), 0, s, 0, p, workers);
+cudaError_t launch_cache_merge(const CacheAttnParams& p, int workers, cudaStream_t s) {
+  if (p.T <= kFewPos)
+    return launch_pdl(cache_merge_kernel<true>, dim3(workers, std::min(p.T, kMergeFewY)), dim3(256), 0, s, 0, p);
+  return launch_pdl(cache_merge_kernel<false>, dim3(workers, kMergeY), dim3(256), 0, s, 0, p);
 }
 
-cudaError_t launch_cache_weights(const CacheAttnParams& p, int n_blocks, cudaStream_t s) {
-  return launch_pdl(cache_weights_kernel, dim3(n_blocks), dim3(256), 0, s, 0, p);
+cudaError_t launch_cache_weights(const CacheAttnParams& p, int workers, int n_blocks, cudaStream_t s) {
+  return launch_pdl(cache_weights_kernel, dim3(workers + n_blocks), dim3(256), 0, s, 0, p, workers);
 }
 
 }  // namespace gqa

@@ -27,7 +27,8 @@ struct CacheAttnSmem {
   static constexpr int kV = kK + kKStages * kKvTileBytes;
   static constexpr int kBar = kV + kVStages * kKvTileBytes;
   static constexpr int kRanges = kBar + CacheBars::kBytes;
-  static constexpr int kBytes = kRanges + CacheRanges::kBytes + 1024;
+  static constexpr int kWalks = kRanges + CacheRanges::kBytes;
+  static constexpr int kBytes = kWalks + 8 * CacheWalk::kBytes + 1024;
 };
 
 template <bool kPair>
@@ -63,9 +64,9 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t tmem_base = *bar.tmem_holder();
   const bool no_loads = p.fault && blockIdx.x == 0;  // test hook: CTA 0's consumers wait out and abort
 
-  // registers: 168 x 384 at launch >= 72 x 128 + 208 x 256
+  // registers: 168 x 384 at launch = 88 x 128 + 208 x 256
   if (warp < 4) {
-    setmaxnreg_dec<72>();
+    setmaxnreg_dec<88>();
     if (warp == 0) {
       if (lane == 0 && !no_loads) produce_k<kWork>(p, ranges, bar, &tmK, smem + L::kK);
     } else if (warp == 3) {
@@ -106,25 +107,20 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem_base + lane_off + slot * 128;
     const uint32_t t_o = tmem_base + lane_off + 256 + slot * 128;
-    const int W = (p.T + 31) / 32;
-    const int worker = kPair ? blockIdx.x : 2 * blockIdx.x + slot;
-    const int units = p.n_kv * p.row_groups;
-    KvWalk w = ranges.walk(kPair ? 0 : slot, p);
+    const CacheWalk walk{reinterpret_cast<volatile int*>(smem + L::kWalks) + (warp - 4) * (CacheWalk::kBytes / 4)};
+    walk.put(ranges.walk(kPair ? 0 : slot, p));
     int items = 0, piece = 0;
     bool ok = true;
-    for (; ok && !w.done(); w.next(units, p.n_new, p.S_max, [&](int b) { return __ldcg(p.kv_len + b); }), ++piece) {
-      const int end = kv_end(w.len, p.n_new, p.S_max);
-      const int safe = keys_all_see(p, w.len);
-      const int n_new = end < 0 ? 0 : p.n_new;
-      const int g = w.u / p.row_groups;
-      const int t0 = (w.u - g * p.row_groups) * p.group_pos + (kPair ? 32 * slot : 0);
-      const int t = t0 + (r >> 2);
-      const bool live = t < p.T;
-      const bool warp_live = t0 + quarter * 8 < p.T;
-      const uint32_t* mask = p.mask ? p.mask + (static_cast<size_t>(w.b) * p.T + (live ? t : 0)) * W : nullptr;
+    // first position of the slot's rows
+    auto first_pos = [&](int u) { return u % p.row_groups * p.group_pos + (kPair ? 32 * slot : 0); };
+    for (; ok && walk.v[6] > 0; walk.next(p), ++piece) {
+      const bool warp_live = first_pos(walk.v[1]) + quarter * 8 < p.T;
+      const int n = walk.v[5];
+      const int safe = keys_all_see(p, walk.v[2]);
+      int key0 = walk.v[4] * kKvTile;
       float m_used = -INFINITY;
       float l_sum = 0.f;
-      for (int j = 0; j < w.n; ++j, ++items) {
+      for (int j = 0; j < n; ++j, ++items, key0 += kKvTile) {
         ok = __all_sync(0xffffffffu, mbar_wait(bar.s_full(slot), items & 1, abort_flag, p.status));
         if (!ok) break;
         if (!warp_live) {  // rows past the last position: whatever their P is, their O is not used
@@ -139,8 +135,12 @@ __global__ void __launch_bounds__(384, 1)
         tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
         tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
         tmem_ld_wait();
-        const int key0 = (w.first + j) * kKvTile;
         if (key0 + kKvTile > safe) {
+          const int n_new = kv_end(walk.v[2], p.n_new, p.S_max) < 0 ? 0 : p.n_new;
+          const int t = first_pos(walk.v[1]) + (r >> 2);
+          const int W = (p.T + 31) / 32;
+          const bool live = t < p.T;
+          const uint32_t* mask = p.mask ? p.mask + (static_cast<size_t>(walk.v[0]) * p.T + (live ? t : 0)) * W : nullptr;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t bits = key_bits(mask, W, n_new, key0 + 32 * i - safe, live);
@@ -220,7 +220,11 @@ __global__ void __launch_bounds__(384, 1)
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(bar.o_empty(slot));
-        if (live) {
+        const KvWalk w = walk.get();
+        const int g = w.u / p.row_groups;
+        const int t = first_pos(w.u) + (r >> 2);
+        const int end = kv_end(w.len, p.n_new, p.S_max);
+        if (t < p.T) {
           const int row = (kPair ? 128 * slot : 0) + r;
           if (w.whole()) {
             // no visible key: zeros; a length out of range: NaN
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(384, 1)
                                   pack_bf16x2(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv),
                                   pack_bf16x2(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv));
           } else {
-            const size_t ps = partial_slot(worker, w.first > 0);
+            const size_t ps = partial_slot(kPair ? blockIdx.x : 2 * blockIdx.x + slot, w.first > 0);
             float4* part = reinterpret_cast<float4*>(p.part_o) + ps * 32 * p.part_rows + row;
 #pragma unroll
             for (int k = 0; k < 32; ++k)
@@ -257,178 +261,167 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
-constexpr int kMergeMax = 512;  // workers at most (two per SM)
-constexpr int kMergeWide = 8;   // a unit of at least this many pieces is shared by a CTA's eight warps
-
-// Unnormalised sum over pieces k0, k0 + step, ... of a block of a cut unit's O, eight float4 per
-// lane: with kByRow (scratch [row][128 d], few rows) rows row0 .. row0 + 7 with lane = float4 column,
-// else (scratch [float4 column][row]) float4 columns col0 .. col0 + 7 with lane = row.  M and l: the
-// rows' maximum and sum; acc is relative to M.
-template <bool kByRow>
-__device__ __forceinline__ void merge_pieces(const CacheAttnParams& p, int first, int n, int row0, int rows, int col0,
-                                             int k0, int step, float (&M)[8], float (&l)[8], float4 (&acc)[8]) {
-  const int lane = threadIdx.x & 31;
-  const int R = p.part_rows;
-  constexpr int kStats = kByRow ? 8 : 1;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    M[i] = -INFINITY;
-    l[i] = 0.f;
-    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-#pragma unroll 2
-  for (int k = k0; k < n; k += step) {
-    const size_t s = k ? partial_slot(first + k, true) : partial_slot(first, false);
-    float2 ml[kStats];
-    float4 v[8];
-#pragma unroll
-    for (int i = 0; i < kStats; ++i)
-      ml[i] = !kByRow || i < rows ? __ldcg(p.part_ml + s * R + row0 + (kByRow ? i : lane)) : make_float2(-INFINITY, 0.f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const size_t at = kByRow ? (s * R + row0 + i) * 32 + lane : (s * 32 + col0 + i) * R + row0 + lane;
-      v[i] = !kByRow || i < rows ? __ldcg(reinterpret_cast<const float4*>(p.part_o) + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    float wa[kStats], wb[kStats];
+// Unnormalised sum of pieces k0, k0 + step, ... of a block of a cut unit's O, N float4 per lane:
+// with kByRow (scratch [row][128 d], at most kFewPos positions) rows row0 .. row0 + rows - 1 (at
+// most N), lane = float4 column; else (scratch [float4 column][row]) float4 columns col0 .. col0 +
+// N - 1 of row row0 + lane.  M and l: the rows' maximum and sum; acc is relative to M.
+template <bool kByRow, int N>
+struct Merge {
+  static constexpr int kStats = kByRow ? N : 1;
+  float M[kStats], l[kStats];
+  float4 acc[N];
+  __device__ __forceinline__ void run(const CacheAttnParams& p, int first, int n, int row0, int rows, int col0, int k0,
+                                      int step) {
+    const int lane = threadIdx.x & 31;
+    const int R = p.part_rows;
 #pragma unroll
     for (int i = 0; i < kStats; ++i) {
-      const float top = fmaxf(M[i], ml[i].x), tz = top == -INFINITY ? 0.f : top;
-      wa[i] = fast_exp2(M[i] - tz);
-      wb[i] = fast_exp2(ml[i].x - tz);
-      M[i] = top;
-      l[i] = l[i] * wa[i] + ml[i].y * wb[i];
+      M[i] = -INFINITY;
+      l[i] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = wa[kByRow ? i : 0], b = wb[kByRow ? i : 0];
-      acc[i] = make_float4(acc[i].x * a + v[i].x * b, acc[i].y * a + v[i].y * b, acc[i].z * a + v[i].z * b,
-                           acc[i].w * a + v[i].w * b);
+    for (int i = 0; i < N; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = k0; k < n; k += step) {
+      const size_t s = k ? partial_slot(first + k, true) : partial_slot(first, false);
+      // (rows past the last read the last: loads without conditions are all in flight together)
+      float2 ml[kStats];
+      float4 v[N];
+#pragma unroll
+      for (int i = 0; i < kStats; ++i) ml[i] = __ldcg(p.part_ml + s * R + row0 + (kByRow ? min(i, rows - 1) : lane));
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const size_t at = kByRow ? (s * R + row0 + min(i, rows - 1)) * 32 + lane : (s * 32 + col0 + i) * R + row0 + lane;
+        v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + at);
+      }
+      float wa[kStats], wb[kStats];
+#pragma unroll
+      for (int i = 0; i < kStats; ++i) {
+        const float top = fmaxf(M[i], ml[i].x), tz = top == -INFINITY ? 0.f : top;
+        wa[i] = fast_exp2(M[i] - tz);
+        wb[i] = fast_exp2(ml[i].x - tz);
+        M[i] = top;
+        l[i] = l[i] * wa[i] + ml[i].y * wb[i];
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float a = wa[kByRow ? i : 0], b = wb[kByRow ? i : 0];
+        acc[i] = make_float4(acc[i].x * a + v[i].x * b, acc[i].y * a + v[i].y * b, acc[i].z * a + v[i].z * b,
+                             acc[i].w * a + v[i].w * b);
+      }
     }
   }
-}
+};
 
 __device__ __forceinline__ uint2 pack4(float4 v, float f) {
   return make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
 }
 
-// Joins the pieces of cut units.  Every CTA collects the units that a worker began and did not
-// finish; a task is a block of one of them (merge_pieces).  A unit of few pieces is one warp's
-// task; the pieces of a longer one are shared by a CTA's warps, which add up through shared memory.
-// Every sum has a fixed order.
+constexpr int kMergeY = 8;      // blocks per worker
+constexpr int kMergeFewY = 4;   // at most kFewPos positions
+
+// Joins the pieces of the unit that goes on past worker v's range, described by d.  A unit of n
+// pieces goes on past n - 1 workers, whose blocks share it: of theirs, this is block i of `blocks`.
+// A task is N rows x 128 columns with kByRow, else 32 rows x 16 columns (N = 4); ks of a block's
+// eight warps share a task's pieces and add up through shared memory in a fixed order.
 template <bool kByRow>
-__global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttnParams p, int workers) {
-  __shared__ int4 units[kMergeMax];  // (sequence, unit, first worker, pieces): few pieces from the front, many from the back
-  __shared__ int count[2];
-  __shared__ float4 sum[8][8][32];   // [warp][i][lane]
-  __shared__ float2 sum_ml[8][32];   // [warp][row: i or lane]
+__device__ __forceinline__ void merge_unit(const CacheAttnParams& p, const int4& d, int i, int blocks) {
+  constexpr int N = 4;
+  __shared__ float4 sum[8][N][32];  // [warp][i][lane]
+  __shared__ float2 sum_ml[8][32];  // [warp][row: i or lane]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  griddep_launch_dependents();
-  griddep_wait();
-  // after a wait that ran out the scratch may be unwritten
-  if (*reinterpret_cast<volatile const int*>(p.status) & kDevErrTimeout) return;
-  if (warp == 0) {
-    int few = 0, many = 0;
-#pragma unroll 4
-    for (int v0 = 0; v0 < workers; v0 += 32) {
-      const int v = v0 + lane;
-      const int4 d = v < workers ? __ldcg(p.merge + v) : make_int4(-1, 0, 0, 0);
-      const int n = d.z - v + 1;
-      const uint32_t a = __ballot_sync(0xffffffffu, d.x >= 0 && n < kMergeWide);
-      const uint32_t b = __ballot_sync(0xffffffffu, d.x >= 0 && n >= kMergeWide);
-      const uint32_t below = (1u << lane) - 1u;
-      if ((a >> lane) & 1u) units[few + __popc(a & below)] = make_int4(d.x, d.y, v, n);
-      if ((b >> lane) & 1u) units[kMergeMax - 1 - many - __popc(b & below)] = make_int4(d.x, d.y, v, n);
-      few += __popc(a);
-      many += __popc(b);
-    }
-    if (lane == 0) {
-      count[0] = few;
-      count[1] = many;
-    }
-  }
-  __syncthreads();
-  const int all_rows = 4 * min(p.T, p.group_pos);
-  const int per = kByRow ? (all_rows + 7) / 8 : (all_rows + 31) / 32 * 4;  // tasks of a unit
-  struct Task {
-    int row0, rows, col0;
-    int g, t0;
-  };
-  auto task_of = [&](int i, const int4& u) {
-    Task k;
-    k.g = u.y / p.row_groups;
-    k.t0 = (u.y - k.g * p.row_groups) * p.group_pos;
-    const int live = min(4 * (p.T - k.t0), 4 * p.group_pos);
-    k.row0 = kByRow ? 8 * i : (i >> 2) * 32;
-    k.rows = min(max(live - k.row0, 0), kByRow ? 8 : 32);
-    k.col0 = kByRow ? 0 : (i & 3) * 8;
-    return k;
-  };
-  // element (i, lane) of a task's block in h
-  auto out = [&](const Task& k, int b, int i) {
-    const int row = k.row0 + (kByRow ? i : lane), col = k.col0 + (kByRow ? lane : i);
-    return reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.h) +
-                                    (static_cast<size_t>(b) * p.T + k.t0 + (row >> 2)) * (p.n_kv * 512) +
-                                    (k.g * 4 + (row & 3)) * 128 + 4 * col);
-  };
-  float M[8], l[8];
-  float4 acc[8];
-  for (int i = warp * gridDim.x + blockIdx.x; i < count[0] * per; i += 8 * gridDim.x) {
-    const int4 u = units[i / per];
-    const Task k = task_of(i % per, u);
-    if (!kByRow && lane >= k.rows) continue;
-    merge_pieces<kByRow>(p, u.z, u.w, k.row0, k.rows, k.col0, 0, 1, M, l, acc);
+  const int n = d.w - d.z + 1;
+  const int g = d.y / p.row_groups;
+  const int t0 = (d.y - g * p.row_groups) * p.group_pos;
+  const int live = 4 * min(p.T - t0, p.group_pos);
+  const int row_tasks = kByRow ? (live + N - 1) / N : (live + 31) / 32;
+  const int tasks = kByRow ? row_tasks : 8 * row_tasks;
+  // a warp for each task and share: with n - 1 workers' blocks there are enough of them
+  const int ks = kByRow ? 8 : n > 8 ? 8 : n > 4 ? 4 : n > 2 ? 2 : 1;
+  for (int first = i * (8 / ks); first < tasks; first += blocks * (8 / ks)) {
+    const int task = first + warp / ks, share = warp % ks;
+    const int row0 = (kByRow ? N : 32) * (task % row_tasks), col0 = kByRow ? 0 : N * (task / row_tasks);
+    const int rows = task < tasks ? min(live - row0, kByRow ? N : 32) : 0;
+    Merge<kByRow, N> m;
+    m.run(p, d.z, rows > 0 && (kByRow || lane < rows) ? n : 0, row0, rows, col0, share, ks);
+    if (ks > 1) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float sum_l = l[kByRow ? j : 0];
-      if (!kByRow || j < k.rows) *out(k, u.x, j) = pack4(acc[j], sum_l == 0.f ? 0.f : 1.f / sum_l);
+      for (int j = 0; j < N; ++j) sum[warp][j][lane] = m.acc[j];
+      if (kByRow) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (lane == j) sum_ml[warp][j] = make_float2(m.M[kByRow ? j : 0], m.l[kByRow ? j : 0]);
+      } else {
+        sum_ml[warp][lane] = make_float2(m.M[0], m.l[0]);
+      }
+      __syncthreads();
     }
-  }
-  for (int i = blockIdx.x; i < count[1] * per; i += gridDim.x) {
-    const int4 u = units[kMergeMax - 1 - i / per];
-    const Task k = task_of(i % per, u);
-    // (a row past the last has nothing: no piece is read for it)
-    merge_pieces<kByRow>(p, u.z, !kByRow && lane >= k.rows ? 0 : u.w, k.row0, k.rows, k.col0, warp, 8, M, l, acc);
-    if (kByRow) {
+    // element (row, float4 column) in h
+    auto out = [&](int row, int col) {
+      return reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.h) +
+                                      (static_cast<size_t>(d.x) * p.T + t0 + (row >> 2)) * (p.n_kv * 512) +
+                                      (g * 4 + (row & 3)) * 128 + 4 * col);
+    };
+    // the task's warp j of ks finishes element i = j, j + ks, ... of every lane
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (lane == j) sum_ml[warp][j] = make_float2(M[j], l[j]);
-    } else {
-      sum_ml[warp][lane] = make_float2(M[0], l[0]);
+    for (int e = 0; e < N; ++e) {
+      if (ks > 1 && e % ks != share) continue;
+      float4 a = m.acc[e];
+      float l = m.l[kByRow ? e : 0];
+      if (ks > 1) {
+        const int at = kByRow ? e : lane, w0 = warp - share;
+        float top = -INFINITY;
+        for (int j = 0; j < ks; ++j) top = fmaxf(top, sum_ml[w0 + j][at].x);
+        const float tz = top == -INFINITY ? 0.f : top;
+        a = make_float4(0.f, 0.f, 0.f, 0.f);
+        l = 0.f;
+        for (int j = 0; j < ks; ++j) {
+          const float2 ml = sum_ml[w0 + j][at];
+          const float f = fast_exp2(ml.x - tz);
+          const float4 v = sum[w0 + j][e][lane];
+          a = make_float4(a.x + f * v.x, a.y + f * v.y, a.z + f * v.z, a.w + f * v.w);
+          l += f * ml.y;
+        }
+      }
+      if (kByRow ? e < rows : lane < rows)
+        *(kByRow ? out(row0 + e, lane) : out(row0 + lane, col0 + e)) = pack4(a, l == 0.f ? 0.f : 1.f / l);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum[warp][j][lane] = acc[j];
-    __syncthreads();
-    // warp w: i = w of the block
-    const int at = kByRow ? warp : lane;
-    float top = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, sum_ml[j][at].x);
-    const float tz = top == -INFINITY ? 0.f : top;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum_l = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float f = fast_exp2(sum_ml[j][at].x - tz);
-      const float4 v = sum[j][warp][lane];
-      a = make_float4(a.x + f * v.x, a.y + f * v.y, a.z + f * v.z, a.w + f * v.w);
-      sum_l += f * sum_ml[j][at].y;
-    }
-    if (kByRow ? warp < k.rows : lane < k.rows) *out(k, u.x, warp) = pack4(a, sum_l == 0.f ? 0.f : 1.f / sum_l);
-    __syncthreads();
+    if (ks > 1) __syncthreads();
   }
 }
 
-// Adds each key's weight, the sum over the four heads of 2^(c s - M) / l, to the running sums: one
-// key tile per warp at a time.
-__global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnParams p) {
+template <bool kByRow>
+__global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttnParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int v = blockIdx.x;
+  const int4 d = __ldcg(p.merge + v);
+  const int st = *reinterpret_cast<volatile const int*>(p.status);
+  // after a wait that ran out the scratch may be unwritten
+  if (d.x < 0 || (st & kDevErrTimeout)) return;
+  merge_unit<kByRow>(p, d, (v - d.z) * gridDim.y + blockIdx.y, (d.w - d.z) * gridDim.y);
+}
+
+// The decode step with key weights: blocks 0 .. workers - 1 merge, the others add each key's
+// weight, the sum over the four heads of 2^(c s - M) / l, to the running sums, one key tile per warp
+// at a time.
+__global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnParams p, int workers) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_launch_dependents();
   griddep_wait();
-  if (*reinterpret_cast<volatile const int*>(p.status) & kDevErrTimeout) return;
+  if (blockIdx.x < workers) {
+    const int v = blockIdx.x;
+    const int4 d = __ldcg(p.merge + v);
+    const int st = *reinterpret_cast<volatile const int*>(p.status);
+    if (d.x >= 0 && !(st & kDevErrTimeout)) merge_unit<true>(p, d, v - d.z, d.w - d.z);
+    return;
+  }
   const int total = __ldcg(p.total_tiles);
-  const int n_warps = gridDim.x * 8;
+  const int n_warps = (gridDim.x - workers) * 8;
   const int R = p.part_rows;
-  for (int i = blockIdx.x * 8 + warp; i < total; i += n_warps) {
+  if (*reinterpret_cast<volatile const int*>(p.status) & kDevErrTimeout) return;
+  // tiles of a warp are n_warps apart: neighbouring warps read neighbouring scores
+  for (int i = (blockIdx.x - workers) * 8 + warp; i < total; i += n_warps) {
     const int2 tu = __ldcg(p.tile_unit + i);
     const float4* s = reinterpret_cast<const float4*>(p.scores) + static_cast<size_t>(i) * kKvTile;
     float x[4][4];

@@ -103,10 +103,10 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t tmem_base = *bar.tmem_holder();
   const bool no_loads = p.fault && blockIdx.x == 0;  // test hook: CTA 0's consumers wait out and abort
 
-  // 64 columns take more registers than 384 threads can all have: 168 x 384 at launch >= 72 x 128
-  // + 208 x 256
+  // 64 columns take more registers than 384 threads can all have: 168 x 384 at launch = 88 x 128 +
+  // 208 x 256
   if (warp < 4) {
-    if constexpr (kCols == 64) setmaxnreg_dec<72>();
+    if constexpr (kCols == 64) setmaxnreg_dec<88>();
     if (warp == 0) {
       if (lane == 0 && !no_loads) produce_k<kWork>(p, ranges, bar, &tmK, smem + L::kK);
     } else if (warp == 3) {

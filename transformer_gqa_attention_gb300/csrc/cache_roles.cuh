@@ -59,8 +59,7 @@ struct CacheBars {
 
 // The CTA's ranges of key tiles, in shared memory: thread i sums the tiles of sequences i per ..
 // i per + per - 1 (B <= 1024: per <= 3); a scan over the CTA gives the total and finds where the
-// ranges start and where their last tiles lie.  Called by all 384 threads; also publishes, for the
-// merge, the unit that each worker begins and does not finish.
+// ranges start.  Called by all 384 threads.
 struct CacheRanges {
   static constexpr int kBytes = 128;
   int* scan;   // [12] per-warp sums
@@ -70,6 +69,7 @@ struct CacheRanges {
   __device__ __forceinline__ int total() const { return where[0]; }
   __device__ __forceinline__ int workers() const { return where[1]; }
   __device__ __forceinline__ int first_tile(int s) const { return where[2 + 5 * s]; }
+  __device__ __forceinline__ int tiles(int s) const { return where[3 + 5 * s]; }
   __device__ __forceinline__ KvWalk walk(int s, const CacheAttnParams& p) const {
     KvWalk w;
     w.left = where[3 + 5 * s];
@@ -119,25 +119,16 @@ struct CacheRanges {
       if (threadIdx.x == 0) {
         where[2 + 5 * s] = lo;
         where[3 + 5 * s] = hi - lo;
-        if (hi == lo) p.merge[v] = make_int4(-1, 0, 0, 0);
       }
-      if (hi == lo || lo >= before + mine || hi - 1 < before) continue;
       int at = before;
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
-        const int n = tiles[i] * units;
-        if (n > 0 && lo >= at && lo < at + n) {
+        if (lo >= at && lo < at + tiles[i] * units) {
           where[4 + 5 * s] = b0 + i;
           where[5 + 5 * s] = lo - at;
           where[6 + 5 * s] = lens[i];
         }
-        if (n > 0 && hi - 1 >= at && hi - 1 < at + n) {  // the last tile's unit: cut by the range's end?
-          const int u = (hi - 1 - at) / tiles[i];
-          const int u_lo = at + u * tiles[i], u_hi = u_lo + tiles[i];
-          p.merge[v] = u_hi > hi && u_lo >= lo ? make_int4(b0 + i, u, range_owner(total, n_work, u_hi - 1), 0)
-                                               : make_int4(-1, 0, 0, 0);
-        }
-        at += n;
+        at += tiles[i] * units;
       }
     }
     __syncthreads();
@@ -179,6 +170,42 @@ struct CacheTiles {
         advance(l1);
       }
     }
+  }
+};
+
+// A softmax warp's walk, kept in shared memory (its registers go to the scores): every lane reads
+// it, lane 0 moves it on.
+struct CacheWalk {
+  static constexpr int kBytes = 32;  // per warp
+  volatile int* v;                   // b, u, len, tiles, first, n, left
+  __device__ __forceinline__ void put(const KvWalk& w) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      v[0] = w.b;
+      v[1] = w.u;
+      v[2] = w.len;
+      v[3] = w.tiles;
+      v[4] = w.first;
+      v[5] = w.n;
+      v[6] = w.left;
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ KvWalk get() const {
+    KvWalk w;
+    w.b = v[0];
+    w.u = v[1];
+    w.len = v[2];
+    w.tiles = v[3];
+    w.first = v[4];
+    w.n = v[5];
+    w.left = v[6];
+    return w;
+  }
+  __device__ __forceinline__ void next(const CacheAttnParams& p) const {
+    KvWalk w = get();
+    w.next(p.n_kv * p.row_groups, p.n_new, p.S_max, [&](int b) { return __ldcg(p.kv_len + b); });
+    put(w);
   }
 };
 
@@ -251,7 +278,8 @@ __device__ __forceinline__ int keys_all_see(const CacheAttnParams& p, int len) {
   return kv_end(len, p.n_new, p.S_max) < 0 ? 0 : len;
 }
 
-// Whole warp 2.  A tile needs it if it reaches past the keys that every row sees.
+// Whole warp 2.  A tile needs clearing if it reaches past the keys that every row sees.  Also
+// publishes, for the merge, the unit that goes on past each worker's range.
 template <int kWork>
 __device__ __forceinline__ void clear_v(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
                                         uint8_t* ring) {
@@ -261,7 +289,17 @@ __device__ __forceinline__ void clear_v(const CacheAttnParams& p, const CacheRan
   const int W = (p.T + 31) / 32;
   int it = 0, seen_b = -1;
   uint32_t seen = 0;  // drafted positions of sequence seen_b that some row sees: word i in lane i
-  tiles.each([&](auto, CacheLane& l) {
+  if (lane < kWork && ranges.tiles(lane) == 0) p.merge[kWork * blockIdx.x + lane] = make_int4(-1, 0, 0, 0);
+  tiles.each([&](auto S, CacheLane& l) {
+    if (l.j == 0 && l.w.left == l.w.n && lane == 0) {  // the worker's last piece: does its unit go on?
+      int4 d = make_int4(-1, 0, 0, 0);
+      if (l.w.first + l.w.n < l.w.tiles) {
+        const int lo = ranges.first_tile(S.value) + ranges.tiles(S.value) - l.w.left - l.w.first;  // the unit's first tile
+        d = make_int4(l.w.b, l.w.u, l.w.first > 0 ? range_owner(ranges.total(), ranges.workers(), lo) : kWork * blockIdx.x + S.value,
+                      range_owner(ranges.total(), ranges.workers(), lo + l.w.tiles - 1));
+      }
+      p.merge[kWork * blockIdx.x + S.value] = d;
+    }
     const int end = kv_end(l.w.len, p.n_new, p.S_max);
     const int safe = keys_all_see(p, l.w.len);
     const int key0 = (l.w.first + l.j) * kKvTile;

@@ -29,13 +29,20 @@ GQA_HD int kv_tiles(int end) { return end <= kKvTile ? 1 : (end + kKvTile - 1) /
 // unit's pieces lie with consecutive workers.
 GQA_HD int range_workers(int total, int most) { return total < most ? total : most; }
 
+// floor(c total / n) in 32-bit arithmetic (n <= 32768)
 GQA_HD int range_start(int total, int n, int c) {
-  return static_cast<int>(static_cast<long long>(c) * total / n);
+  const unsigned q = static_cast<unsigned>(total) / static_cast<unsigned>(n);
+  const unsigned rem = static_cast<unsigned>(total) - q * n;
+  return static_cast<int>(c * q + c * rem / static_cast<unsigned>(n));
 }
 
-// The worker whose range holds tile x: the last c with range_start(c) <= x, c total < (x + 1) n.
+// The worker whose range holds tile x: the last c with range_start(c) <= x.
 GQA_HD int range_owner(int total, int n, int x) {
-  return static_cast<int>(((static_cast<long long>(x) + 1) * n - 1) / total);
+  int c = static_cast<int>(static_cast<float>(x) * static_cast<float>(n) / static_cast<float>(total));  // off by 1 or so
+  c = c < n - 1 ? c : n - 1;
+  while (c > 0 && range_start(total, n, c) > x) --c;
+  while (c + 1 < n && range_start(total, n, c + 1) <= x) ++c;
+  return c;
 }
 
 // The pieces of one range, in order.

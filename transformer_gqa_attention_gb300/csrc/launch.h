@@ -78,8 +78,8 @@ cudaError_t configure_cache_attn();
 int cache_attn_box(const CacheAttnParams& p);
 cudaError_t launch_cache_attn(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                               const CacheAttnParams& p, int n_ctas, cudaStream_t s);
-cudaError_t launch_cache_merge(const CacheAttnParams& p, int workers, int n_blocks, cudaStream_t s);
-cudaError_t launch_cache_weights(const CacheAttnParams& p, int n_blocks, cudaStream_t s);
+cudaError_t launch_cache_merge(const CacheAttnParams& p, int workers, cudaStream_t s);
+cudaError_t launch_cache_weights(const CacheAttnParams& p, int workers, int n_blocks, cudaStream_t s);
 cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t s);
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s);
 cudaError_t launch_evict_move(const EvictParams& p, cudaStream_t s);
