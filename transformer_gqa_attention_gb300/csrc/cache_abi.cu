@@ -42,8 +42,8 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
     off = round_up(off + bytes, 256);
     return at;
   };
-  // workers: CTAs, or with one row tile their softmax slots; each may hold two partial results
-  const size_t workers = static_cast<size_t>(n_ctas) * (p.group_pos > 32 ? 1 : 2);
+  // workers: CTAs, or with few positions their softmax slots; each may hold two partial results
+  const size_t workers = static_cast<size_t>(n_ctas) * (a.T <= kFewPos ? 2 : 1);
   const size_t slots = 2 * workers;
   const size_t merge = take(workers * sizeof(int4));
   const size_t part_ml = take(slots * p.part_rows * sizeof(float2));

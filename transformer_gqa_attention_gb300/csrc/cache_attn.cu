@@ -14,8 +14,8 @@ namespace {
 using CacheAttnFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CacheAttnParams);
 constexpr CacheAttnFn kAttn[] = {cache_attn_few_kernel<4, true>,   cache_attn_few_kernel<4, false>,
                                  cache_attn_few_kernel<16, false>, cache_attn_few_kernel<32, false>,
-                                 cache_attn_few_kernel<64, false>, cache_attn_kernel<false>,
-                                 cache_attn_kernel<true>};
+                                 cache_attn_few_kernel<64, false>, cache_attn_kernel<kOneTile>,
+                                 cache_attn_kernel<kTwoTiles>};
 constexpr int kFewKernels = 5;
 
 int attn_of(const CacheAttnParams& p) {

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(384, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) bar.init();
+  if (threadIdx.x == 0) bar.init(128);
   if (warp == 1) {
     tmem_alloc(bar.tmem_holder(), 256);
     tmem_relinquish();
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(384, 1)
       if (lane == 0 && !no_loads) produce_k<kWork>(p, ranges, bar, &tmK, smem + L::kK);
     } else if (warp == 3) {
       // rows of the product past the queries' box hold whatever was there: their columns are not used
-      if (lane == 0 && !no_loads) produce_vq<kWork>(p, ranges, bar, &tmQ, &tmV, smem, kCols, L::kQHalf, smem + L::kV);
+      if (lane == 0 && !no_loads) produce_vq<kTwoWorkers>(p, ranges, bar, &tmQ, &tmV, smem, kCols, L::kQHalf, smem + L::kV);
     } else if (warp == 2) {
       clear_v<kWork>(p, ranges, bar, smem + L::kV);
     } else {
@@ -119,9 +119,9 @@ __global__ void __launch_bounds__(384, 1)
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 64, 1, 1);  // V^T (d contiguous), P (rows contiguous)
       const uint32_t q_addr = smem_u32(smem), p_addr = smem_u32(smem + L::kP);
       const uint32_t k_addr = smem_u32(smem + L::kK), v_addr = smem_u32(smem + L::kV);
-      issue_all<kWork, 1>(
+      issue_all<kTwoWorkers, 1>(
           p, ranges, bar,
-          [&](int slot, int ks) {
+          [&](int slot, int, int ks) {
             const uint64_t kd = sdesc_sw128(k_addr + ks * kKvTileBytes, 0, 1024);
             const uint64_t qd = sdesc_sw128(q_addr + slot * 2 * L::kQHalf, 0, 1024);
 #pragma unroll
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(384, 1)
               umma_ss(tmem_base + slot * 64, kd + (((kk >> 2) * kKvHalfBytes + (kk & 3) * 32) >> 4),
                       qd + (((kk >> 2) * L::kQHalf + (kk & 3) * 32) >> 4), idesc_s, kk != 0);
           },
-          [&](int slot, int vs, int, bool first) {
+          [&](int slot, int, int vs, int, bool first) {
             const uint64_t vd = sdesc_sw128(v_addr + vs * kKvTileBytes, kKvHalfBytes, 1024);
             const uint64_t pd = sdesc_sw128(p_addr + slot * L::kPBytes, L::kPBytes, 1024);
 #pragma unroll

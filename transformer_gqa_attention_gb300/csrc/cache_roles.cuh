@@ -10,9 +10,13 @@
 //               drafted positions that nobody's mask names): their weight is 0, but 0 x NaN is not
 //   warp 3      TMA producer of the V tiles (a tile's V is needed a softmax later than its K) and
 //               of each unit's queries, once the last S of the unit before has read its own
-//   warps 4..7, 8..11  two softmax slots
-// A CTA has kWork workers (kv_sched.h): two, one per softmax slot, or one whose slots share every
-// key tile.
+//   warps 4..11 softmax
+// Which products they work on is the kernel's mode:
+//   kTwoWorkers  warps 4..7 and 8..11 are workers of their own (kv_sched.h), each with its own range
+//                of tiles, queries, S and O (cache_attn_few.cuh)
+//   kOneTile     one worker and one row tile: S alternates between two buffers from tile to tile,
+//                queries and O from piece to piece
+//   kTwoTiles    one worker, two row tiles on every key tile, each with its queries, S and O
 #pragma once
 
 #include <type_traits>
@@ -22,6 +26,20 @@
 #include "ptx.cuh"
 
 namespace gqa {
+
+enum CacheMode : int { kTwoWorkers, kOneTile, kTwoTiles };
+constexpr int mode_workers(int mode) { return mode == kTwoWorkers ? 2 : 1; }
+constexpr int mode_items(int mode) { return mode == kTwoTiles ? 2 : 1; }  // S per key tile and worker
+
+// Buffer (0 or 1) that queries and O of piece `piece` take, and how many pieces had it before.
+template <int kMode>
+__device__ __forceinline__ int piece_buffer(int worker, int item, int piece) {
+  return kMode == kTwoWorkers ? worker : kMode == kOneTile ? piece & 1 : item;
+}
+template <int kMode>
+__device__ __forceinline__ int piece_turn(int piece) {
+  return kMode == kOneTile ? piece >> 1 : piece;
+}
 
 constexpr int kKvTileBytes = kKvTile * 128 * 2;  // 128 keys x 128 bf16, two 64-column halves
 constexpr int kKvHalfBytes = kKvTileBytes / 2;
@@ -44,14 +62,15 @@ struct CacheBars {
   __device__ __forceinline__ uint64_t* drain() const { return bars + 18; }
   // 2 arrivals: the PV that used the tile, and warp 2
   __device__ __forceinline__ uint64_t* v_empty(int stage) const { return bars + 19 + stage; }
-  // 128 arrivals: P of the tile's first and second 64 keys (or of all of them: lo), O of the piece read
+  // 128 arrivals: P of the tile's first and second 64 keys (or of all of them: lo)
   __device__ __forceinline__ uint64_t* p_lo(int slot) const { return bars + 22 + slot; }
   __device__ __forceinline__ uint64_t* p_hi(int slot) const { return bars + 24 + slot; }
+  // an arrival of every thread that reads O
   __device__ __forceinline__ uint64_t* o_empty(int slot) const { return bars + 26 + slot; }
   __device__ __forceinline__ uint32_t* tmem_holder() const { return reinterpret_cast<uint32_t*>(bars + kCount); }
   __device__ __forceinline__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(tmem_holder() + 1); }
-  __device__ __forceinline__ void init() const {
-    for (int i = 0; i < kCount; ++i) mbar_init(&bars[i], i < 19 ? 1u : i < 22 ? 2u : 128u);
+  __device__ __forceinline__ void init(uint32_t o_readers) const {
+    for (int i = 0; i < kCount; ++i) mbar_init(&bars[i], i < 19 ? 1u : i < 22 ? 2u : i < 26 ? 128u : o_readers);
     *abort_flag() = 0;
     fence_mbar_init();
   }
@@ -173,42 +192,6 @@ struct CacheTiles {
   }
 };
 
-// A softmax warp's walk, kept in shared memory (its registers go to the scores): every lane reads
-// it, lane 0 moves it on.
-struct CacheWalk {
-  static constexpr int kBytes = 32;  // per warp
-  volatile int* v;                   // b, u, len, tiles, first, n, left
-  __device__ __forceinline__ void put(const KvWalk& w) const {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-      v[0] = w.b;
-      v[1] = w.u;
-      v[2] = w.len;
-      v[3] = w.tiles;
-      v[4] = w.first;
-      v[5] = w.n;
-      v[6] = w.left;
-    }
-    __syncwarp();
-  }
-  __device__ __forceinline__ KvWalk get() const {
-    KvWalk w;
-    w.b = v[0];
-    w.u = v[1];
-    w.len = v[2];
-    w.tiles = v[3];
-    w.first = v[4];
-    w.n = v[5];
-    w.left = v[6];
-    return w;
-  }
-  __device__ __forceinline__ void next(const CacheAttnParams& p) const {
-    KvWalk w = get();
-    w.next(p.n_kv * p.row_groups, p.n_new, p.S_max, [&](int b) { return __ldcg(p.kv_len + b); });
-    put(w);
-  }
-};
-
 // Lane 0 of warp 0.
 template <int kWork>
 __device__ __forceinline__ void produce_k(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
@@ -231,29 +214,28 @@ __device__ __forceinline__ void produce_k(const CacheAttnParams& p, const CacheR
     for (int i = max(0, it - kKStages); i < it; ++i) mbar_wait_drain(bar.k_full(i % kKStages), (i / kKStages) & 1);
 }
 
-// Lane 0 of warp 3.  A slot's queries are q_rows rows (positions x 4 heads; the box of tmQ) in two
-// halves of 64 columns, q_half bytes apart; a unit has kSlots = 2 / kWork slots of them.
-template <int kWork>
+// Lane 0 of warp 3.  An item's queries are q_rows rows (positions x 4 heads; the box of tmQ) in two
+// halves of 64 columns, q_half bytes apart.
+template <int kMode>
 __device__ __forceinline__ void produce_vq(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
                                            const CUtensorMap* tmQ, const CUtensorMap* tmV, uint8_t* q, int q_rows,
                                            int q_half, uint8_t* ring) {
-  constexpr int kSlots = 2 / kWork;
-  CacheTiles<kWork> tiles(p, ranges);
+  CacheTiles<mode_workers(kMode)> tiles(p, ranges);
   volatile int* abort_flag = bar.abort_flag();
-  int it = 0, asked = 0;  // queries asked for: slot 0 in the low half, slot 1 in the high
+  int it = 0, asked = 0;  // queries asked for: buffer 0 in the low half, 1 in the high
   tiles.each([&](auto S, CacheLane& l) {
     const int g = l.w.u / p.row_groups;
     if (l.j == 0) {
       const int t0 = (l.w.u - g * p.row_groups) * p.group_pos;
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        const int slot = kWork == 1 ? i : S.value;
-        if (l.piece > 0 && !mbar_wait(bar.q_empty(slot), (l.piece - 1) & 1, abort_flag, p.status)) return false;
-        mbar_arrive_expect_tx(bar.q_full(slot), q_rows * 256);
-        uint8_t* dst = q + slot * 2 * q_half;
-        tma_load_4d(dst, tmQ, bar.q_full(slot), 0, 4 * g, t0 + 32 * i, l.w.b);
-        tma_load_4d(dst + q_half, tmQ, bar.q_full(slot), 64, 4 * g, t0 + 32 * i, l.w.b);
-        asked += slot ? 0x10000 : 1;
+      for (int i = 0; i < mode_items(kMode); ++i) {
+        const int at = piece_buffer<kMode>(S.value, i, l.piece), turn = piece_turn<kMode>(l.piece);
+        if (turn > 0 && !mbar_wait(bar.q_empty(at), (turn - 1) & 1, abort_flag, p.status)) return false;
+        mbar_arrive_expect_tx(bar.q_full(at), q_rows * 256);
+        uint8_t* dst = q + at * 2 * q_half;
+        tma_load_4d(dst, tmQ, bar.q_full(at), 0, 4 * g, t0 + 32 * i, l.w.b);
+        tma_load_4d(dst + q_half, tmQ, bar.q_full(at), 64, 4 * g, t0 + 32 * i, l.w.b);
+        asked += at ? 0x10000 : 1;
       }
     }
     const int st = it % kVStages;
@@ -347,22 +329,24 @@ __device__ __forceinline__ void clear_v(const CacheAttnParams& p, const CacheRan
   });
 }
 
-// The whole of warp 1.  In turn for each tile and slot: S (issued by `issue_s`), then the PV of the
-// item before (`issue_pv`), so that the tensor core works while a softmax runs.
-//   issue_s(slot, K stage): the UMMAs of S;  issue_pv(slot, V stage, half, first): those of O += P V
-//   for keys 64 half .. + 63 (kHalves = 2) or all keys (kHalves = 1), O anew if first.
-template <int kWork, int kHalves, typename FS, typename FP>
+// The whole of warp 1.  In turn for each tile and item: S (issue_s), then the PV of the item before
+// (issue_pv_mma), so that the tensor core works while a softmax runs.
+//   issue_s(S buffer, query buffer, K stage): the UMMAs of S
+//   issue_pv_mma(S buffer, O buffer, V stage, half, first): those of O += P V for keys 64 half .. + 63
+//   (kHalves = 2) or all keys (kHalves = 1), O anew if first
+template <int kMode, int kHalves, typename FS, typename FP>
 __device__ __forceinline__ void issue_all(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
                                           FS issue_s, FP issue_pv_mma) {
-  CacheTiles<kWork> tiles(p, ranges);
+  constexpr int kItems = mode_items(kMode);
+  CacheTiles<mode_workers(kMode)> tiles(p, ranges);
   volatile int* abort_flag = bar.abort_flag();
   auto wait = [&](uint64_t* b, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.status));
   };
   uint32_t fix_par = 0;  // bit v: parity of V stage v's next v_fixed
-  uint32_t p_par = 0;    // bit i: parity of slot i's next P
+  uint32_t p_par = 0;    // bit i: parity of S buffer i's next P
   struct Pending {
-    int slot, it, piece;             // softmax slot, tile count, the slot's piece
+    int slot, o, turn, it;           // S and O buffer, pieces that had the O before, tile count
     bool first, last, fix, release;  // first / last tile of the piece; V tile to be cleared; V tile done
   } pend{};
   bool has_pend = false;
@@ -370,8 +354,8 @@ __device__ __forceinline__ void issue_all(const CacheAttnParams& p, const CacheR
     const Pending d = pend;
     has_pend = false;
     const int vs = d.it % kVStages;
-    // a new O takes the place of the last piece's
-    if (d.first && d.piece > 0 && !wait(bar.o_empty(d.slot), (d.piece - 1) & 1)) return false;
+    // a new O takes the place of an earlier piece's
+    if (d.first && d.turn > 0 && !wait(bar.o_empty(d.o), (d.turn - 1) & 1)) return false;
     if (!wait(bar.v_full(vs), (d.it / kVStages) & 1)) return false;
     if (d.fix) {
       if (!wait(bar.v_fixed(vs), (fix_par >> vs) & 1)) return false;
@@ -384,10 +368,10 @@ __device__ __forceinline__ void issue_all(const CacheAttnParams& p, const CacheR
       if (!wait(hf ? bar.p_hi(d.slot) : bar.p_lo(d.slot), ph)) return false;
       tc_fence_after();
       if (elect_one_sync()) {
-        issue_pv_mma(d.slot, vs, hf, d.first);
+        issue_pv_mma(d.slot, d.o, vs, hf, d.first);
         if (hf == kHalves - 1) {
           if (d.release) umma_commit(bar.v_empty(vs));
-          if (d.last) umma_commit(bar.o_full(d.slot));
+          if (d.last) umma_commit(bar.o_full(d.o));
         }
       }
       __syncwarp();
@@ -399,25 +383,27 @@ __device__ __forceinline__ void issue_all(const CacheAttnParams& p, const CacheR
     const bool fix = (l.w.first + l.j + 1) * kKvTile > keys_all_see(p, l.w.len);
     const bool first = l.j == 0, last = l.j == l.w.n - 1;
     const int ks = it % kKStages;
+    const int turn = piece_turn<kMode>(l.piece);
 #pragma unroll
-    for (int i = 0; i < 2 / kWork; ++i) {
-      const int slot = kWork == 1 ? i : S.value;
-      // P of the slot's last tile is used up before the softmax of S takes its place (the other
+    for (int i = 0; i < kItems; ++i) {
+      const int slot = kMode == kTwoWorkers ? S.value : kMode == kOneTile ? it & 1 : i;
+      const int at = piece_buffer<kMode>(S.value, i, l.piece);
+      // P of the buffer's last tile is used up before the softmax of S takes its place (the other
       // worker has no more tiles in between)
-      if (has_pend && pend.slot == slot && !issue_pv()) return false;
-      if (first && !wait(bar.q_full(slot), l.piece & 1)) return false;
+      if (kMode == kTwoWorkers && has_pend && pend.slot == slot && !issue_pv()) return false;
+      if (first && !wait(bar.q_full(at), turn & 1)) return false;
       if (i == 0 && !wait(bar.k_full(ks), (it / kKStages) & 1)) return false;
       tc_fence_after();
-      const bool last_slot = kWork == 2 || i == 1;
+      const bool last_item = i == kItems - 1;
       if (elect_one_sync()) {
-        issue_s(slot, ks);
+        issue_s(slot, at, ks);
         umma_commit(bar.s_full(slot));
-        if (last_slot) umma_commit(bar.k_empty(ks));
-        if (last) umma_commit(bar.q_empty(slot));
+        if (last_item) umma_commit(bar.k_empty(ks));
+        if (last) umma_commit(bar.q_empty(at));
       }
       __syncwarp();
       if (has_pend && !issue_pv()) return false;
-      pend = Pending{slot, it, l.piece, first, last, fix && i == 0, last_slot};
+      pend = Pending{slot, at, turn, it, first, last, fix && i == 0, last_item};
       has_pend = true;
     }
     ++it;
