@@ -386,6 +386,15 @@ def test_evict_ties_and_special_weights(S_out):
     run_evict(w, [200] * 6, 40, 2, 6, 2, 200, S_out)
 
 
+@pytest.mark.parametrize("B,n_kv,length", [(1, 1, 70000), (1, 8, 40000), (3, 5, 20000), (33, 2, 5000), (40, 8, 600)])
+def test_evict_at_every_share_of_a_head(B, n_kv, length):
+    # one to eight CTAs per head, slices of one and of several staged chunks
+    S = length + 3
+    w = heavy(5, B, n_kv, S)
+    w[0, 0, 100:4000] = 0.25                                # a plateau that the cut may fall into
+    run_evict(w, [max(0, length - 17 * b) for b in range(B)], length // 3, 3, 40, n_kv, S, length // 3 + 2)
+
+
 def test_evict_many_sequences():
     run_evict(heavy(4, 300, 1, 50), [(7 * b) % 51 for b in range(300)], 20, 1, 4, 1, 50)
 

@@ -238,6 +238,7 @@ gqa_status attn_cache_evict(gqa_ctx* c, const void* cache_k, const void* cache_v
   p.out_weights = out_weights;
   p.kept = kept;
   p.new_len = new_len;
+  p.old_len = c->old_len;
   p.status = c->status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   {

@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -61,7 +63,11 @@ cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------------------ eviction
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kSelEach = 8;                          // positions per thread of a staged chunk
+constexpr int kSelChunk = kSelThreads * kSelEach;
+constexpr int kSelBins = 2048;
+constexpr int kSelMaxCluster = 8;
 
 // Order-preserving unsigned image of a weight: larger weight, larger image; -0 equals +0, and a
 // NaN comes below everything.
@@ -73,6 +79,7 @@ __device__ __forceinline__ uint32_t weight_rank(float w) {
 
 // Exclusive prefix sum of `v` over the CTA's threads; *total gets the sum.
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
+  constexpr int kWarps = kSelThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -82,135 +89,240 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   }
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int w = lane < kSelThreads / 32 ? warp_sums[lane] : 0;
+  int before = x - v, all = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    warp_sums[lane] = w;
+  for (int w = 0; w < kWarps; ++w) {
+    const int s = warp_sums[w];
+    if (w < warp) before += s;
+    all += s;
   }
-  __syncthreads();
-  *total = warp_sums[kSelThreads / 32 - 1];
-  const int before = (warp ? warp_sums[warp - 1] : 0) + x - v;
+  *total = all;
   __syncthreads();
   return before;
 }
 
-// One CTA per (kv group, sequence): the positions to keep, ascending, and their weights.  The
-// weight of the last one picked is found digit by digit (four 8-bit counts), then one ordered
-// pass emits everything above it and the first of its equals.
+// The positions that a (sequence, kv head) keeps, ascending.  A cluster of gridDim.x CTAs shares its
+// positions, each a contiguous slice.  The rank that the last kept weight has is found in digits of
+// 11, 11 and 10 bits: every CTA counts its slice's digits in shared memory, sums the cluster's
+// counts through distributed shared memory and finds the digit; once all of a digit's positions are
+// wanted the search ends early.  Then everything above is kept, and the first of the equal ones: a
+// position's place is the number kept before it, a prefix sum over the slice and the CTAs before.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
-  __shared__ int hist[256];
-  __shared__ int warp_sums[32];
-  __shared__ int sh_digit, sh_need;
+  __shared__ __align__(16) float stage[kSelChunk];
+  __shared__ __align__(16) int hist[kSelBins];
+  __shared__ int warp_sums[kSelThreads / 32];
+  __shared__ int found[3];   // digit, still wanted of it, its count
+  __shared__ int totals[2];  // of the slice: kept for sure, equal
   griddep_wait();
-  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int rank = blockIdx.x, n_ctas = gridDim.x, g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const size_t unit = static_cast<size_t>(b) * p.n_kv + g;
   const float* w = p.weights + unit * p.S_max;
-  float* ow = p.out_weights + unit * p.S_out;
   int* kept = p.kept + unit * p.budget;
   const int len = __ldcg(p.kv_len + b);
-  if (len < 0 || len > p.S_max) {
-    if (tid == 0) atomicOr(p.status, kDevErrRange);
-    for (int i = tid; i < p.budget; i += kSelThreads) kept[i] = -1;
+  const bool bad = len < 0 || len > p.S_max;
+  if (rank == 0 && tid == 0) {
+    if (g == 0) p.old_len[b] = bad ? -1 : len;
+    if (bad) atomicOr(p.status, kDevErrRange);
+  }
+  if (bad || len <= p.budget) {  // the same for the whole cluster
+    for (int i = rank * kSelThreads + tid; i < p.budget; i += n_ctas * kSelThreads) kept[i] = !bad && i < len ? i : -1;
     return;
   }
-  const int n_keep = min(len, p.budget);
-  const int lo = p.n_first, hi = len - p.n_recent;  // the middle, of which the heaviest stay
-  uint32_t thr = 0;
-  int eq_take = 0;
-  if (len > p.budget) {
-    int need = p.budget - p.n_first - p.n_recent;
-    if (need > 0) {
-      uint32_t prefix = 0, pmask = 0;
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        for (int s = lo + tid; s < hi; s += kSelThreads) {
-          const uint32_t u = weight_rank(__ldcg(w + s));
-          if ((u & pmask) == prefix) atomicAdd(&hist[(u >> shift) & 255], 1);
-        }
-        __syncthreads();
-        if (tid == 0) {
-          int d = 255, n = need;
-          while (hist[d] < n) n -= hist[d--];
-          sh_digit = d;
-          sh_need = n;
-        }
-        __syncthreads();
-        prefix |= static_cast<uint32_t>(sh_digit) << shift;
-        pmask |= 255u << shift;
-        need = sh_need;
-        __syncthreads();
+  const int per = (len + n_ctas - 1) / n_ctas;
+  const int lo = min(len, rank * per), hi = min(len, lo + per);
+  const int mid0 = p.n_first, mid1 = len - p.n_recent;  // the heaviest of these stay
+  const bool staged = per <= kSelChunk;
+  auto load_chunk = [&](int s0) {
+    for (int i = tid; i < min(kSelChunk, hi - s0); i += kSelThreads) stage[i] = __ldcg(w + s0 + i);
+    __syncthreads();
+  };
+  auto sync_all = [&] {
+    if (n_ctas > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  };
+  if (staged) load_chunk(lo);
+
+  // ranks above prefix | ~mask stay, and the first `rem` of those whose masked bits are prefix
+  uint32_t prefix = 0xFFFFFFFFu, mask = 0xFFFFFFFFu;  // (no weight has this rank: none)
+  int rem = p.budget - p.n_first - p.n_recent;
+  if (rem > 0) {
+    prefix = mask = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digit_mask = pass == 2 ? 1023u : 2047u;
+      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      for (int s = max(lo, mid0) + tid; s < min(hi, mid1); s += kSelThreads) {
+        const uint32_t u = weight_rank(staged ? stage[s - lo] : __ldcg(w + s));
+        if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & digit_mask], 1);
       }
-      thr = prefix;
-      eq_take = need;
-    } else {
-      thr = 0xFFFFFFFFu;  // nothing of the middle stays (no rank is this high)
+      sync_all();
+      // thread t: bins from the top, 4 t .. 4 t + 3
+      const int top = kSelBins - 4 - 4 * tid;
+      int4 c = make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < kSelMaxCluster; ++r) {
+        if (r < n_ctas) {
+          const int4 o = r == rank ? *reinterpret_cast<const int4*>(hist + top)
+                                   : ld_shared_cluster_int4(mapa_shared(smem_u32(hist + top), r));
+          c = make_int4(c.x + o.x, c.y + o.y, c.z + o.z, c.w + o.w);
+        }
+      }
+      int all;
+      int above = block_scan(c.x + c.y + c.z + c.w, warp_sums, &all);
+      const int n[4] = {c.w, c.z, c.y, c.x};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (above < rem && rem <= above + n[k]) {
+          found[0] = top + 3 - k;
+          found[1] = rem - above;
+          found[2] = n[k];
+        }
+        above += n[k];
+      }
+      sync_all();  // found is written, and the counts of this CTA have been read
+      prefix |= static_cast<uint32_t>(found[0]) << shift;
+      mask |= digit_mask << shift;
+      rem = found[1];
+      if (found[2] == rem) break;
     }
   }
-  int out = 0, eq_seen = 0;
-  for (int s0 = 0; s0 < len; s0 += kSelThreads) {
-    const int s = s0 + tid;
-    float x = 0.f;
-    bool gt = false, eq = false;
-    if (s < len) {
-      x = __ldcg(w + s);
-      if (len <= p.budget || s < lo || s >= hi) {
-        gt = true;
-      } else {
-        const uint32_t u = weight_rank(x);
-        gt = u > thr;
-        eq = u == thr;
+  const uint32_t above = prefix | ~mask;
+  // flags of the thread's positions of a staged chunk: bits 0..7 kept for sure, 8..15 equal
+  auto flags = [&](int s0) {
+    uint32_t f = 0;
+    const float4 x0 = *reinterpret_cast<const float4*>(stage + tid * kSelEach);
+    const float4 x1 = *reinterpret_cast<const float4*>(stage + tid * kSelEach + 4);
+    const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+    for (int k = 0; k < kSelEach; ++k) {
+      const int s = s0 + tid * kSelEach + k;
+      if (s < hi) {
+        const uint32_t u = weight_rank(x[k]);
+        const bool edge = s < mid0 || s >= mid1;
+        if (edge || u > above)
+          f |= 1u << k;
+        else if ((u & mask) == prefix)
+          f |= 256u << k;
       }
     }
-    int n_eq;
-    const int eq_at = eq_seen + block_scan(eq, warp_sums, &n_eq);
-    const bool take = gt || (eq && eq_at < eq_take);
-    int n_take;
-    const int at = out + block_scan(take, warp_sums, &n_take);
-    if (take) {  // at <= s: in place, only positions already read are written
-      kept[at] = s;
-      ow[at] = x;
+    return f;
+  };
+  auto packed = [](uint32_t f) { return (__popc(f & 255u) << 16) | __popc(f >> 8); };  // at most 4096 each
+  // this slice's totals, then those of the CTAs before it
+  int sure = 0, equal = 0;
+  uint32_t f = 0;
+  int before = 0;
+  for (int s0 = lo; s0 < hi; s0 += kSelChunk) {
+    if (!staged) {
+      __syncthreads();
+      load_chunk(s0);
     }
-    out += n_take;
-    eq_seen += n_eq;
+    f = flags(s0);
+    int all;
+    before = block_scan(packed(f), warp_sums, &all);
+    sure += all >> 16;
+    equal += all & 0xFFFF;
   }
-  __syncthreads();
-  for (int i = n_keep + tid; i < p.budget; i += kSelThreads) kept[i] = -1;
-  // weights of what is decoded next start from zero
-  const int zero_to = p.in_place ? len : p.S_out;
-  for (int i = n_keep + tid; i < zero_to; i += kSelThreads) ow[i] = 0.f;
+  int base_sure = 0, base_equal = 0;
+  if (n_ctas > 1) {
+    if (tid == 0) {
+      totals[0] = sure;
+      totals[1] = equal;
+    }
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      base_sure += ld_shared_cluster_int(mapa_shared(smem_u32(&totals[0]), r));
+      base_equal += ld_shared_cluster_int(mapa_shared(smem_u32(&totals[1]), r));
+    }
+  }
+  for (int s0 = lo; s0 < hi; s0 += kSelChunk) {
+    if (!staged) {
+      __syncthreads();
+      load_chunk(s0);
+      f = flags(s0);
+      int all;
+      before = block_scan(packed(f), warp_sums, &all);
+      sure = all >> 16;  // of this chunk
+      equal = all & 0xFFFF;
+    }
+    int gt = base_sure + (before >> 16), eq = base_equal + (before & 0xFFFF);
+#pragma unroll
+    for (int k = 0; k < kSelEach; ++k) {
+      const bool is_gt = (f >> k) & 1u, is_eq = (f >> (8 + k)) & 1u;
+      if (is_gt || (is_eq && eq < rem)) kept[gt + min(eq, rem)] = s0 + tid * kSelEach + k;
+      gt += is_gt;
+      eq += is_eq;
+    }
+    base_sure += sure;
+    base_equal += equal;
+  }
+  if (n_ctas > 1) cluster_sync();  // no CTA leaves while another reads its totals
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveChunk = 4;   // 16-byte pieces of a row that one CTA moves
-constexpr int kMoveRows = 4;    // rows in flight per thread
+constexpr int kMovePieces = 4;   // 16-byte pieces of a row that one CTA moves
+constexpr int kMoveRows = 8;     // rows in flight per thread
+constexpr int kMoveStep = kMoveThreads / kMovePieces;
+constexpr int kMoveChunk = kMoveStep * kMoveRows;  // rows of a CTA's step
+constexpr int kMoveSlices = 2 * 16 / kMovePieces;  // of K and V; one more block moves the weights
 
-// One CTA per (64-byte column slice of K or V, kv group, sequence): rows kept[i] -> i.  kept is
-// ascending, so kept[i] >= i; in place, a step's rows are all read before any is written, and no
-// later step reads a row that it wrote.
+// Rows kept[i] -> i: one CTA per (64-byte column slice of K or V, kv group, sequence), or several
+// that take steps in turn when the outputs are other buffers.  kept is ascending, so kept[i] >= i; in
+// place, a step's rows are all read before any is written, and no later step reads a row that it
+// wrote.
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
   griddep_wait();
-  const int slice = blockIdx.x, g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int per_cache = 16 / kMoveChunk;
-  const bool is_v = slice >= per_cache;
+  const int slice = blockIdx.x % (kMoveSlices + 1), part = blockIdx.x / (kMoveSlices + 1), g = blockIdx.y, b = blockIdx.z;
+  const int parts = gridDim.x / (kMoveSlices + 1), tid = threadIdx.x;
   const size_t unit = static_cast<size_t>(b) * p.n_kv + g;
   const int* kept = p.kept + unit * p.budget;
-  const int c = (slice - (is_v ? per_cache : 0)) * kMoveChunk + tid % kMoveChunk;
+  if (slice == kMoveSlices) {  // weights, and the new length
+    if (part > 0) return;
+    const float* w = p.weights + unit * p.S_max;
+    float* ow = p.out_weights + unit * p.S_out;
+    for (int i0 = 0; i0 < p.budget; i0 += kMoveThreads * kMoveRows) {
+      float v[kMoveRows];
+      int from[kMoveRows];
+#pragma unroll
+      for (int j = 0; j < kMoveRows; ++j) {
+        const int i = i0 + j * kMoveThreads + tid;
+        from[j] = i < p.budget ? __ldcg(kept + i) : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < kMoveRows; ++j) v[j] = __ldcg(w + max(from[j], 0));
+      if (p.in_place) __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kMoveRows; ++j)
+        if (from[j] >= 0) ow[i0 + j * kMoveThreads + tid] = v[j];
+    }
+    // weights of what is decoded next start from zero
+    const int old_len = __ldcg(p.old_len + b);
+    const int n_keep = min(old_len, p.budget);
+    if (old_len >= 0) {
+      const int zero_to = p.in_place ? old_len : p.S_out;
+      for (int i = n_keep + tid; i < zero_to; i += kMoveThreads) ow[i] = 0.f;
+    }
+    if (g == 0 && tid == 0) p.new_len[b] = max(n_keep, 0);
+    return;
+  }
+  const int per_cache = kMoveSlices / 2;
+  const bool is_v = slice >= per_cache;
+  const int c = (slice - (is_v ? per_cache : 0)) * kMovePieces + tid % kMovePieces;
   const size_t row = static_cast<size_t>(p.n_kv) * 16;
   const uint4* src = static_cast<const uint4*>(is_v ? p.v : p.k) + (static_cast<size_t>(b) * p.S_max * p.n_kv + g) * 16 + c;
   uint4* dst = static_cast<uint4*>(is_v ? p.out_v : p.out_k) + (static_cast<size_t>(b) * p.S_out * p.n_kv + g) * 16 + c;
-  constexpr int kStep = kMoveThreads / kMoveChunk;
-  for (int i0 = 0; i0 < p.budget; i0 += kStep * kMoveRows) {
+  for (int i0 = part * kMoveChunk; i0 < p.budget; i0 += parts * kMoveChunk) {
     uint4 v[kMoveRows];
     int from[kMoveRows];
 #pragma unroll
     for (int j = 0; j < kMoveRows; ++j) {
-      const int i = i0 + j * kStep + tid / kMoveChunk;
+      const int i = i0 + j * kMoveStep + tid / kMovePieces;
       from[j] = i < p.budget ? __ldcg(kept + i) : -1;
+      if (p.in_place && from[j] == i) from[j] = -1;  // already there
     }
 #pragma unroll
     for (int j = 0; j < kMoveRows; ++j)
@@ -218,24 +330,25 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     if (p.in_place) __syncthreads();
 #pragma unroll
     for (int j = 0; j < kMoveRows; ++j) {
-      const int i = i0 + j * kStep + tid / kMoveChunk;
+      const int i = i0 + j * kMoveStep + tid / kMovePieces;
       if (from[j] >= 0) dst[i * row] = v[j];
-    }
-  }
-  if (slice == 0 && g == 0) {
-    for (int i = tid; i <= p.budget; i += kMoveThreads) {
-      const bool here = i < p.budget && __ldcg(kept + i) >= 0;
-      if (!here && (i == 0 || __ldcg(kept + i - 1) >= 0)) p.new_len[b] = i;
     }
   }
 }
 
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s) {
-  return launch_pdl(evict_select_kernel, dim3(p.n_kv, p.B), dim3(kSelThreads), 0, s, 0, p);
+  // CTAs per (sequence, kv head): about 512 in all
+  const long long units = static_cast<long long>(p.B) * p.n_kv;
+  const int c = units <= 64 ? 8 : units <= 128 ? 4 : units <= 256 ? 2 : 1;
+  return launch_pdl(evict_select_kernel, dim3(c, p.n_kv, p.B), dim3(kSelThreads), 0, s, c > 1 ? c : 0, p);
 }
 
 cudaError_t launch_evict_move(const EvictParams& p, cudaStream_t s) {
-  return launch_pdl(evict_move_kernel, dim3(2 * 16 / kMoveChunk, p.n_kv, p.B), dim3(kMoveThreads), 0, s, 0, p);
+  // in place the steps of a slice follow one another in one CTA; else about 1024 CTAs share them
+  const long long units = static_cast<long long>(p.B) * p.n_kv;
+  const int steps = (p.budget + kMoveChunk - 1) / kMoveChunk;
+  const int parts = p.in_place ? 1 : static_cast<int>(std::max(1LL, std::min<long long>(steps, 1024 / (units * kMoveSlices))));
+  return launch_pdl(evict_move_kernel, dim3(parts * (kMoveSlices + 1), p.n_kv, p.B), dim3(kMoveThreads), 0, s, 0, p);
 }
 
 }  // namespace gqa

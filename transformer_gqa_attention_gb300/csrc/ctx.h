@@ -46,6 +46,7 @@ struct gqa_ctx {
   __nv_bfloat16* w_qkv_norm = nullptr;
   float norm_eps = 0.f;
   int* status = nullptr;           // device status word (kDevErr* bits)
+  int* old_len = nullptr;          // [kDecodeMaxBatch] lengths before an eviction (behind the status word)
   int* counters = nullptr;         // arrival counters of the decode split merge (kCounterInts)
   gqa::DeviceBuffer ws;            // workspace of the block forms
   gqa::DeviceBuffer cache_ws;      // scratch of the attention over caches of per-sequence length

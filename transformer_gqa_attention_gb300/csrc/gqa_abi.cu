@@ -289,11 +289,12 @@ gqa_status create_impl(const void* wq, const void* wk, const void* wv, const voi
   };
   const size_t rows = c->qkv_rows(), qc = c->q_cols(), kvc = c->kv_cols();
   if (cudaMalloc(&c->w_qkv, rows * 4096 * 2) != cudaSuccess || cudaMalloc(&c->w_o, 4096 * qc * 2) != cudaSuccess ||
-      cudaMalloc(&c->status, sizeof(int)) != cudaSuccess ||
+      cudaMalloc(&c->status, (64 + kDecodeMaxBatch) * sizeof(int)) != cudaSuccess ||
       cudaMalloc(&c->counters, kCounterInts * sizeof(int)) != cudaSuccess) {
     cudaGetLastError();
     return fail(GQA_ERR_OOM);
   }
+  c->old_len = c->status + 64;
   cudaError_t e = cudaMemsetAsync(c->status, 0, sizeof(int), s);
   if (e == cudaSuccess) e = cudaMemsetAsync(c->counters, 0, kCounterInts * sizeof(int), s);
   // k-block-major copies: W_Q rows 0..qc-1, W_K qc..qc+kvc-1, W_V qc+kvc.. of W_QKV; W_O

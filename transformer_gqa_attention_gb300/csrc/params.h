@@ -149,6 +149,7 @@ struct EvictParams {
   float* out_weights;     // [B, n_kv, S_out]
   int* kept;              // [B, n_kv, budget]
   int* new_len;           // [B], may be kv_len
+  int* old_len;           // [B] scratch: kv_len as the selection read it (-1: out of range)
   int* status;
 };
 

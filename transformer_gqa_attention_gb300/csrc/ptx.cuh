@@ -403,6 +403,22 @@ __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
   return v;
 }
 
+// The same for integers, written by the other CTA before the barrier (volatile: a later read of
+// the same address, after another barrier, is another load).
+__device__ __forceinline__ int ld_shared_cluster_int(uint32_t cluster_addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ int4 ld_shared_cluster_int4(uint32_t cluster_addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
 // Bulk copy of `bytes` (multiple of 16, 16-byte aligned) from this CTA's shared memory to a
 // shared::cluster address (a peer CTA's buffer); completes as transaction bytes on the
 // mbarrier at `bar_cluster_addr` (in the destination CTA).
