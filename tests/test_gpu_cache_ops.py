@@ -78,13 +78,15 @@ def check_h(got, ref, av, mag, what=""):
     return d
 
 
-def run_tree(seed, lens, T, n_kv=8, vis=None, S=None, scale=1.0, spoil=True):
+def run_tree(seed, lens, T, n_kv=8, vis=None, S=None, scale=1.0, spoil=True, ramp=0.0):
     rng = np.random.default_rng(seed)
     gen = torch.Generator().manual_seed(seed)
     B = len(lens)
     S = S or max(lens) + T + 3
     vis = random_trees(rng, B, T) if vis is None else vis
     k, v = draw_cache(gen, B, S, n_kv, [n + T for n in lens], scale)
+    if ramp:
+        k = (k.float() * (1 + ramp * torch.arange(S)[None, :, None, None] / 128)).to(torch.bfloat16)
     if spoil:  # a drafted position that nobody sees may hold anything
         for b in range(B):
             for j in np.flatnonzero(~vis[b].any(0)):
@@ -159,6 +161,13 @@ def test_tree_attention_with_peaked_scores(T):
     run_tree(90 + T, [1500, 3, 640], T, scale=30.0)
 
 
+@pytest.mark.parametrize("T", [1, 3, 7, 12, 24, 50, 130])
+def test_tree_attention_with_rising_scores(T):
+    # scores grow from key tile to key tile, so that nearly every tile rescales O and l
+    run_tree(95 + T, [2500, 700], T, n_kv=2, ramp=4.0)
+    run_tree(96 + T, [500] * 40, T, n_kv=2, ramp=4.0)
+
+
 def test_tree_attention_over_a_long_prefix():
     run_tree(91, [20000], 20, n_kv=2)
     run_tree(92, [9000, 12000], 64, n_kv=1)
@@ -198,11 +207,13 @@ def test_tree_prefix_out_of_range(bad):
 
 
 # ------------------------------------------------------------------------------------- weights
-def run_weights(seed, lens, n_kv=8, S=None, scale=1.0, steps=1):
+def run_weights(seed, lens, n_kv=8, S=None, scale=1.0, steps=1, ramp=0.0):
     gen = torch.Generator().manual_seed(seed)
     B = len(lens)
     S = S or max(lens) + 5
     k, v = draw_cache(gen, B, S, n_kv, lens, scale)
+    if ramp:
+        k = (k.float() * (1 + ramp * torch.arange(S)[None, :, None, None] / 128)).to(torch.bfloat16)
     w0 = torch.rand(B, n_kv, S, generator=gen)
     for b, n in enumerate(lens):
         w0[b, :, n:] = NAN  # not touched
@@ -244,6 +255,8 @@ def test_decode_attention_weights_accumulate_over_steps():
 def test_decode_attention_weights_long_and_peaked():
     run_weights(231, [30000, 100], n_kv=1)
     run_weights(232, [3000, 700], scale=20.0)
+    run_weights(234, [2500, 700], ramp=4.0)
+    run_weights(235, [500] * 40, n_kv=2, ramp=4.0)
 
 
 def test_decode_attention_weights_many_sequences():

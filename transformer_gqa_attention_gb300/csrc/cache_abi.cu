@@ -18,7 +18,7 @@ using namespace gqa;
 
 gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t s) {
   const int G = c->n_kv;
-  const int n_ctas = c->num_sms;  // persistent, one per SM
+  const int n_ctas = c->num_sms & ~1;  // persistent, one per SM (the GPU's 152: even)
   CacheAttnParams p{};
   p.B = a.B;
   p.T = a.T;
@@ -31,8 +31,8 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   p.weights = a.weights;
   p.status = c->status;
   p.scale_log2 = kScaleLog2;
-  // up to 32 positions fill one 128-row tile; more run on two tiles that share each key tile
-  p.group_pos = a.T <= kFewPos ? kFewPos : a.T <= 32 ? 32 : 64;
+  const bool pair = a.T > kOneTilePos;
+  p.group_pos = a.T <= kFewPos ? kFewPos : pair ? 64 : kOneTilePos;
   p.row_groups = (a.T + p.group_pos - 1) / p.group_pos;
   p.part_rows = static_cast<int>(round_up(4 * std::min(a.T, p.group_pos), 32));
 
@@ -42,8 +42,9 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
     off = round_up(off + bytes, 256);
     return at;
   };
-  // workers: CTAs, or with few positions their softmax slots; each may hold two partial results
-  const size_t workers = static_cast<size_t>(n_ctas) * (a.T <= kFewPos ? 2 : 1);
+  // workers: CTAs, with few positions their two softmax slots, with many CTA pairs; each may hold two
+  // partial results
+  const size_t workers = a.T <= kFewPos ? 2 * n_ctas : pair ? n_ctas / 2 : n_ctas;
   const size_t slots = 2 * workers;
   const size_t merge = take(workers * sizeof(int4));
   const size_t part_ml = take(slots * p.part_rows * sizeof(float2));
@@ -78,7 +79,7 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   const uint64_t strides[3] = {256, static_cast<uint64_t>(G) * 1024, static_cast<uint64_t>(a.T) * G * 1024};
   const uint32_t box[4] = {64, 4, static_cast<uint32_t>(cache_attn_box(p)), 1};
   if (!make_map(&tq, a.q, 4, dims, strides, box) ||
-      !map_cache(&tk, a.cache_k, a.B, a.S_max, G, a.S_max, kKvTile) ||
+      !map_cache(&tk, a.cache_k, a.B, a.S_max, G, a.S_max, pair ? kKvTile / 2 : kKvTile) ||
       !map_cache(&tv, a.cache_v, a.B, a.S_max, G, a.S_max, kKvTile))
     return cuda_fail(cudaErrorInvalidValue);
   p.fault = take_fault(c, GQA_KERNEL_CACHE_ATTN);

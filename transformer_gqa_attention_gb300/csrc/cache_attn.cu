@@ -3,6 +3,8 @@
 
 #include "cache_attn.cuh"
 #include "cache_attn_few.cuh"
+#include "cache_attn_pair.cuh"
+#include "cache_merge.cuh"
 #include "launch.h"
 
 namespace gqa {
@@ -10,20 +12,22 @@ namespace gqa {
 namespace {
 
 // The attention kernel of a call and its shared memory: by positions per sequence, up to 16 keys on
-// the tensor core's rows, up to 32 one row tile per softmax slot, above two row tiles per key tile.
+// the tensor core's rows, up to 32 one row tile, above CTA pairs.
 using CacheAttnFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CacheAttnParams);
 constexpr CacheAttnFn kAttn[] = {cache_attn_few_kernel<4, true>,   cache_attn_few_kernel<4, false>,
                                  cache_attn_few_kernel<16, false>, cache_attn_few_kernel<32, false>,
-                                 cache_attn_few_kernel<64, false>, cache_attn_kernel<kOneTile>,
-                                 cache_attn_kernel<kTwoTiles>};
+                                 cache_attn_few_kernel<64, false>, cache_attn_kernel,
+                                 cache_attn_pair_kernel};
 constexpr int kFewKernels = 5;
 
 int attn_of(const CacheAttnParams& p) {
   if (p.T == 1) return p.weights ? 0 : 1;
-  return p.T <= 4 ? 2 : p.T <= 8 ? 3 : p.T <= kFewPos ? 4 : p.T <= 32 ? 5 : 6;
+  return p.T <= 4 ? 2 : p.T <= 8 ? 3 : p.T <= kFewPos ? 4 : p.T <= kOneTilePos ? 5 : 6;
 }
 
-int smem_of(int kernel) { return kernel < kFewKernels ? CacheFewSmem::kBytes : CacheAttnSmem::kBytes; }
+int smem_of(int kernel) {
+  return kernel < kFewKernels ? CacheFewSmem::kBytes : kernel == kFewKernels ? CacheAttnSmem::kBytes : CachePairSmem::kBytes;
+}
 
 }  // namespace
 

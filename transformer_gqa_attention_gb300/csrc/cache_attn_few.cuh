@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(384, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) bar.init(128);
+  if (threadIdx.x == 0) bar.init(128, 128);
   if (warp == 1) {
     tmem_alloc(bar.tmem_holder(), 256);
     tmem_relinquish();
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(384, 1)
   griddep_launch_dependents();
   griddep_wait();  // lengths, queries and the new cache entries; the scratch of the call before
   tc_fence_before();
-  ranges.find<kWork>(p);
+  ranges.find<kWork>(p, kWork * blockIdx.x, kWork * gridDim.x);
   tc_fence_after();
   const uint32_t tmem_base = *bar.tmem_holder();
   const bool no_loads = p.fault && blockIdx.x == 0;  // test hook: CTA 0's consumers wait out and abort

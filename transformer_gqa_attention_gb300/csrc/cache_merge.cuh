@@ -1,0 +1,225 @@
+// cache_merge.cuh — what finishes the attention over caches of per-sequence length: the merge of
+// units that several workers shared, and the accumulation of the key weights.
+#pragma once
+
+#include <type_traits>
+
+#include "kv_sched.h"
+#include "params.h"
+#include "ptx.cuh"
+
+namespace gqa {
+
+// Unnormalised sum of pieces k0, k0 + step, ... of a block of a cut unit's O, N float4 per lane:
+// with kByRow (scratch [row][128 d], at most kFewPos positions) rows row0 .. row0 + rows - 1 (at
+// most N), lane = float4 column; else (scratch [float4 column][row]) float4 columns col0 .. col0 +
+// N - 1 of row row0 + lane.  M and l: the rows' maximum and sum; acc is relative to M.
+template <bool kByRow, int N>
+struct Merge {
+  static constexpr int kStats = kByRow ? N : 1;
+  float M[kStats], l[kStats];
+  float4 acc[N];
+  __device__ __forceinline__ void run(const CacheAttnParams& p, int first, int n, int row0, int rows, int col0, int k0,
+                                      int step) {
+    const int lane = threadIdx.x & 31;
+    const int R = p.part_rows;
+#pragma unroll
+    for (int i = 0; i < kStats; ++i) {
+      M[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = k0; k < n; k += step) {
+      const size_t s = k ? partial_slot(first + k, true) : partial_slot(first, false);
+      // (rows past the last read the last: loads without conditions are all in flight together)
+      float2 ml[kStats];
+      float4 v[N];
+#pragma unroll
+      for (int i = 0; i < kStats; ++i) ml[i] = __ldcg(p.part_ml + s * R + row0 + (kByRow ? min(i, rows - 1) : lane));
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const size_t at = kByRow ? (s * R + row0 + min(i, rows - 1)) * 32 + lane : (s * 32 + col0 + i) * R + row0 + lane;
+        v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + at);
+      }
+      float wa[kStats], wb[kStats];
+#pragma unroll
+      for (int i = 0; i < kStats; ++i) {
+        const float top = fmaxf(M[i], ml[i].x), tz = top == -INFINITY ? 0.f : top;
+        wa[i] = fast_exp2(M[i] - tz);
+        wb[i] = fast_exp2(ml[i].x - tz);
+        M[i] = top;
+        l[i] = l[i] * wa[i] + ml[i].y * wb[i];
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float a = wa[kByRow ? i : 0], b = wb[kByRow ? i : 0];
+        acc[i] = make_float4(acc[i].x * a + v[i].x * b, acc[i].y * a + v[i].y * b, acc[i].z * a + v[i].z * b,
+                             acc[i].w * a + v[i].w * b);
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ uint2 pack4(float4 v, float f) {
+  return make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+}
+
+constexpr int kMergeY = 8;      // blocks per worker
+constexpr int kMergeFewY = 4;   // at most kFewPos positions
+
+// Joins the pieces of the unit that goes on past worker v's range, described by d.  A unit of n
+// pieces goes on past n - 1 workers, whose blocks share it: of theirs, this is block i of `blocks`.
+// A task is N rows x 128 columns with kByRow, else 32 rows x 16 columns (N = 4); ks of a block's
+// eight warps share a task's pieces and add up through shared memory in a fixed order.
+template <bool kByRow>
+__device__ __forceinline__ void merge_unit(const CacheAttnParams& p, const int4& d, int i, int blocks) {
+  constexpr int N = 4;
+  __shared__ float4 sum[8][N][32];  // [warp][i][lane]
+  __shared__ float2 sum_ml[8][32];  // [warp][row: i or lane]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = d.w - d.z + 1;
+  const int g = d.y / p.row_groups;
+  const int t0 = (d.y - g * p.row_groups) * p.group_pos;
+  const int live = 4 * min(p.T - t0, p.group_pos);
+  const int row_tasks = kByRow ? (live + N - 1) / N : (live + 31) / 32;
+  const int tasks = kByRow ? row_tasks : 8 * row_tasks;
+  // a warp for each task and share: with n - 1 workers' blocks there are enough of them
+  const int ks = kByRow ? 8 : n > 8 ? 8 : n > 4 ? 4 : n > 2 ? 2 : 1;
+  for (int first = i * (8 / ks); first < tasks; first += blocks * (8 / ks)) {
+    const int task = first + warp / ks, share = warp % ks;
+    const int row0 = (kByRow ? N : 32) * (task % row_tasks), col0 = kByRow ? 0 : N * (task / row_tasks);
+    const int rows = task < tasks ? min(live - row0, kByRow ? N : 32) : 0;
+    Merge<kByRow, N> m;
+    m.run(p, d.z, rows > 0 && (kByRow || lane < rows) ? n : 0, row0, rows, col0, share, ks);
+    if (ks > 1) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) sum[warp][j][lane] = m.acc[j];
+      if (kByRow) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (lane == j) sum_ml[warp][j] = make_float2(m.M[kByRow ? j : 0], m.l[kByRow ? j : 0]);
+      } else {
+        sum_ml[warp][lane] = make_float2(m.M[0], m.l[0]);
+      }
+      __syncthreads();
+    }
+    // element (row, float4 column) in h
+    auto out = [&](int row, int col) {
+      return reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.h) +
+                                      (static_cast<size_t>(d.x) * p.T + t0 + (row >> 2)) * (p.n_kv * 512) +
+                                      (g * 4 + (row & 3)) * 128 + 4 * col);
+    };
+    // the task's warp j of ks finishes element i = j, j + ks, ... of every lane
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if (ks > 1 && e % ks != share) continue;
+      float4 a = m.acc[e];
+      float l = m.l[kByRow ? e : 0];
+      if (ks > 1) {
+        const int at = kByRow ? e : lane, w0 = warp - share;
+        float top = -INFINITY;
+        for (int j = 0; j < ks; ++j) top = fmaxf(top, sum_ml[w0 + j][at].x);
+        const float tz = top == -INFINITY ? 0.f : top;
+        a = make_float4(0.f, 0.f, 0.f, 0.f);
+        l = 0.f;
+        for (int j = 0; j < ks; ++j) {
+          const float2 ml = sum_ml[w0 + j][at];
+          const float f = fast_exp2(ml.x - tz);
+          const float4 v = sum[w0 + j][e][lane];
+          a = make_float4(a.x + f * v.x, a.y + f * v.y, a.z + f * v.z, a.w + f * v.w);
+          l += f * ml.y;
+        }
+      }
+      if (kByRow ? e < rows : lane < rows)
+        *(kByRow ? out(row0 + e, lane) : out(row0 + lane, col0 + e)) = pack4(a, l == 0.f ? 0.f : 1.f / l);
+    }
+    if (ks > 1) __syncthreads();
+  }
+}
+
+template <bool kByRow>
+__global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttnParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int v = blockIdx.x;
+  const int4 d = __ldcg(p.merge + v);
+  const int st = *reinterpret_cast<volatile const int*>(p.status);
+  // after a wait that ran out the scratch may be unwritten
+  if (d.x < 0 || (st & kDevErrTimeout)) return;
+  merge_unit<kByRow>(p, d, (v - d.z) * gridDim.y + blockIdx.y, (d.w - d.z) * gridDim.y);
+}
+
+// The decode step with key weights: blocks 0 .. workers - 1 merge, the others add each key's
+// weight, the sum over the four heads of 2^(c s - M) / l, to the running sums, one key tile per warp
+// at a time.
+__global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnParams p, int workers) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (blockIdx.x < workers) {
+    const int v = blockIdx.x;
+    const int4 d = __ldcg(p.merge + v);
+    const int st = *reinterpret_cast<volatile const int*>(p.status);
+    if (d.x >= 0 && !(st & kDevErrTimeout)) merge_unit<true>(p, d, v - d.z, d.w - d.z);
+    return;
+  }
+  const int total = __ldcg(p.total_tiles);
+  const int n_warps = (gridDim.x - workers) * 8;
+  const int R = p.part_rows;
+  if (*reinterpret_cast<volatile const int*>(p.status) & kDevErrTimeout) return;
+  // tiles of a warp are n_warps apart: neighbouring warps read neighbouring scores
+  for (int i = (blockIdx.x - workers) * 8 + warp; i < total; i += n_warps) {
+    const int2 tu = __ldcg(p.tile_unit + i);
+    const float4* s = reinterpret_cast<const float4*>(p.scores) + static_cast<size_t>(i) * kKvTile;
+    float x[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = __ldcg(s + 32 * k + lane);
+      x[0][k] = v.x;
+      x[1][k] = v.y;
+      x[2][k] = v.z;
+      x[3][k] = v.w;
+    }
+    const int2 cs = __ldcg(p.unit_workers + tu.x);
+    float* w = p.weights + static_cast<size_t>(tu.x) * p.S_max + tu.y * kKvTile;
+    bool seen[4];
+    float a[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // -inf in all four heads: past the end (or of no weight)
+      seen[k] = x[0][k] != -INFINITY || x[1][k] != -INFINITY || x[2][k] != -INFINITY || x[3][k] != -INFINITY;
+      a[k] = seen[k] ? __ldcg(w + 32 * k + lane) : 0.f;
+    }
+    float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      float2 m = make_float2(-INFINITY, 0.f);
+      if (cs.x == cs.y) {
+        m = __ldcg(p.unit_ml + tu.x * 4 + h);
+      } else {  // a cut unit: its pieces' maxima and sums, shared by the lanes
+        for (int k = lane; k <= cs.y - cs.x; k += 32) {
+          const int ps = k ? partial_slot(cs.x + k, true) : partial_slot(cs.x, false);
+          const float2 o = __ldcg(p.part_ml + static_cast<size_t>(ps) * R + h);
+          const float top = fmaxf(m.x, o.x), tz = top == -INFINITY ? 0.f : top;
+          m = make_float2(top, m.y * fast_exp2(m.x - tz) + o.y * fast_exp2(o.x - tz));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const float2 q = make_float2(__shfl_xor_sync(0xffffffffu, m.x, o), __shfl_xor_sync(0xffffffffu, m.y, o));
+          const float top = fmaxf(m.x, q.x), tz = top == -INFINITY ? 0.f : top;
+          m = make_float2(top, m.y * fast_exp2(m.x - tz) + q.y * fast_exp2(q.x - tz));
+        }
+      }
+      const float M = m.x == -INFINITY ? 0.f : m.x;
+      const float inv = 1.f / m.y;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) add[k] += fast_exp2(fmaf(x[h][k], p.scale_log2, -M)) * inv;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (seen[k]) w[32 * k + lane] = a[k] + add[k];
+  }
+}
+
+}  // namespace gqa

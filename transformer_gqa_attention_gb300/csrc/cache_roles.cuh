@@ -14,9 +14,8 @@
 // Which products they work on is the kernel's mode:
 //   kTwoWorkers  warps 4..7 and 8..11 are workers of their own (kv_sched.h), each with its own range
 //                of tiles, queries, S and O (cache_attn_few.cuh)
-//   kOneTile     one worker and one row tile: S alternates between two buffers from tile to tile,
-//                queries and O from piece to piece
-//   kTwoTiles    one worker, two row tiles on every key tile, each with its queries, S and O
+//   kOneTile     one worker: S alternates between two buffers from tile to tile, queries and O from
+//                piece to piece (cache_attn.cuh)
 #pragma once
 
 #include <type_traits>
@@ -27,14 +26,13 @@
 
 namespace gqa {
 
-enum CacheMode : int { kTwoWorkers, kOneTile, kTwoTiles };
+enum CacheMode : int { kTwoWorkers, kOneTile };
 constexpr int mode_workers(int mode) { return mode == kTwoWorkers ? 2 : 1; }
-constexpr int mode_items(int mode) { return mode == kTwoTiles ? 2 : 1; }  // S per key tile and worker
 
 // Buffer (0 or 1) that queries and O of piece `piece` take, and how many pieces had it before.
 template <int kMode>
-__device__ __forceinline__ int piece_buffer(int worker, int item, int piece) {
-  return kMode == kTwoWorkers ? worker : kMode == kOneTile ? piece & 1 : item;
+__device__ __forceinline__ int piece_buffer(int worker, int piece) {
+  return kMode == kTwoWorkers ? worker : piece & 1;
 }
 template <int kMode>
 __device__ __forceinline__ int piece_turn(int piece) {
@@ -47,7 +45,7 @@ constexpr int kKStages = 2;
 constexpr int kVStages = 3;
 
 struct CacheBars {
-  static constexpr int kCount = 28;
+  static constexpr int kCount = 30;
   static constexpr int kBytes = 256;  // barriers, TMEM address, abort flag
   uint64_t* bars;
   __device__ __forceinline__ explicit CacheBars(uint8_t* at) : bars(reinterpret_cast<uint64_t*>(at)) {}
@@ -60,17 +58,19 @@ struct CacheBars {
   __device__ __forceinline__ uint64_t* s_full(int slot) const { return bars + 14 + slot; }
   __device__ __forceinline__ uint64_t* o_full(int slot) const { return bars + 16 + slot; }
   __device__ __forceinline__ uint64_t* drain() const { return bars + 18; }
+  // kOneTile: the PV that used the S buffer's P is done
+  __device__ __forceinline__ uint64_t* pv_done(int slot) const { return bars + 28 + slot; }
   // 2 arrivals: the PV that used the tile, and warp 2
   __device__ __forceinline__ uint64_t* v_empty(int stage) const { return bars + 19 + stage; }
-  // 128 arrivals: P of the tile's first and second 64 keys (or of all of them: lo)
+  // arrivals of its writers: P of the tile's first and second 64 keys (or of all of them: lo)
   __device__ __forceinline__ uint64_t* p_lo(int slot) const { return bars + 22 + slot; }
   __device__ __forceinline__ uint64_t* p_hi(int slot) const { return bars + 24 + slot; }
-  // an arrival of every thread that reads O
+  // arrivals of those that read O
   __device__ __forceinline__ uint64_t* o_empty(int slot) const { return bars + 26 + slot; }
   __device__ __forceinline__ uint32_t* tmem_holder() const { return reinterpret_cast<uint32_t*>(bars + kCount); }
   __device__ __forceinline__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(tmem_holder() + 1); }
-  __device__ __forceinline__ void init(uint32_t o_readers) const {
-    for (int i = 0; i < kCount; ++i) mbar_init(&bars[i], i < 19 ? 1u : i < 22 ? 2u : i < 26 ? 128u : o_readers);
+  __device__ __forceinline__ void init(uint32_t p_writers, uint32_t o_readers) const {
+    for (int i = 0; i < kCount; ++i) mbar_init(&bars[i], i < 19 ? 1u : i < 22 ? 2u : i < 26 ? p_writers : i < 28 ? o_readers : 1u);
     *abort_flag() = 0;
     fence_mbar_init();
   }
@@ -96,8 +96,9 @@ struct CacheRanges {
     return w;
   }
 
+  // of kWork workers from `first` on, `most` in all
   template <int kWork>
-  __device__ __forceinline__ void find(const CacheAttnParams& p) const {
+  __device__ __forceinline__ void find(const CacheAttnParams& p, int first, int most) const {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int units = p.n_kv * p.row_groups;
     const int per = (p.B + 383) / 384;
@@ -124,7 +125,7 @@ struct CacheRanges {
       if (w < warp) before += scan[w];
       total += scan[w];
     }
-    const int n_work = range_workers(total, kWork * gridDim.x);
+    const int n_work = range_workers(total, most);
     if (threadIdx.x == 0) {
       where[0] = total;
       where[1] = n_work;
@@ -132,7 +133,7 @@ struct CacheRanges {
     }
 #pragma unroll
     for (int s = 0; s < kWork; ++s) {
-      const int v = kWork * blockIdx.x + s;
+      const int v = first + s;
       const int lo = v < n_work ? range_start(total, n_work, v) : total;
       const int hi = v < n_work ? range_start(total, n_work, v + 1) : total;
       if (threadIdx.x == 0) {
@@ -214,7 +215,7 @@ __device__ __forceinline__ void produce_k(const CacheAttnParams& p, const CacheR
     for (int i = max(0, it - kKStages); i < it; ++i) mbar_wait_drain(bar.k_full(i % kKStages), (i / kKStages) & 1);
 }
 
-// Lane 0 of warp 3.  An item's queries are q_rows rows (positions x 4 heads; the box of tmQ) in two
+// Lane 0 of warp 3.  A unit's queries are q_rows rows (positions x 4 heads; the box of tmQ) in two
 // halves of 64 columns, q_half bytes apart.
 template <int kMode>
 __device__ __forceinline__ void produce_vq(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
@@ -227,16 +228,13 @@ __device__ __forceinline__ void produce_vq(const CacheAttnParams& p, const Cache
     const int g = l.w.u / p.row_groups;
     if (l.j == 0) {
       const int t0 = (l.w.u - g * p.row_groups) * p.group_pos;
-#pragma unroll
-      for (int i = 0; i < mode_items(kMode); ++i) {
-        const int at = piece_buffer<kMode>(S.value, i, l.piece), turn = piece_turn<kMode>(l.piece);
-        if (turn > 0 && !mbar_wait(bar.q_empty(at), (turn - 1) & 1, abort_flag, p.status)) return false;
-        mbar_arrive_expect_tx(bar.q_full(at), q_rows * 256);
-        uint8_t* dst = q + at * 2 * q_half;
-        tma_load_4d(dst, tmQ, bar.q_full(at), 0, 4 * g, t0 + 32 * i, l.w.b);
-        tma_load_4d(dst + q_half, tmQ, bar.q_full(at), 64, 4 * g, t0 + 32 * i, l.w.b);
-        asked += at ? 0x10000 : 1;
-      }
+      const int at = piece_buffer<kMode>(S.value, l.piece), turn = piece_turn<kMode>(l.piece);
+      if (turn > 0 && !mbar_wait(bar.q_empty(at), (turn - 1) & 1, abort_flag, p.status)) return false;
+      mbar_arrive_expect_tx(bar.q_full(at), q_rows * 256);
+      uint8_t* dst = q + at * 2 * q_half;
+      tma_load_4d(dst, tmQ, bar.q_full(at), 0, 4 * g, t0, l.w.b);
+      tma_load_4d(dst + q_half, tmQ, bar.q_full(at), 64, 4 * g, t0, l.w.b);
+      asked += at ? 0x10000 : 1;
     }
     const int st = it % kVStages;
     if (!mbar_wait(bar.v_empty(st), ((it / kVStages) & 1) ^ 1u, abort_flag, p.status)) return false;
@@ -260,36 +258,28 @@ __device__ __forceinline__ int keys_all_see(const CacheAttnParams& p, int len) {
   return kv_end(len, p.n_new, p.S_max) < 0 ? 0 : len;
 }
 
-// Whole warp 2.  A tile needs clearing if it reaches past the keys that every row sees.  Also
-// publishes, for the merge, the unit that goes on past each worker's range.
-template <int kWork>
-__device__ __forceinline__ void clear_v(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
-                                        uint8_t* ring) {
-  CacheTiles<kWork> tiles(p, ranges);
-  volatile int* abort_flag = bar.abort_flag();
-  const int lane = threadIdx.x & 31;
-  const int W = (p.T + 31) / 32;
-  int it = 0, seen_b = -1;
+// The unit of a worker's last piece as the merge wants it (CacheAttnParams::merge): whether it goes
+// on past the worker's range.
+__device__ __forceinline__ int4 goes_on(const CacheRanges& ranges, const KvWalk& w, int s, int worker) {
+  if (w.first + w.n == w.tiles) return make_int4(-1, 0, 0, 0);
+  const int lo = ranges.first_tile(s) + ranges.tiles(s) - w.left - w.first;  // the unit's first tile
+  return make_int4(w.b, w.u, w.first > 0 ? range_owner(ranges.total(), ranges.workers(), lo) : worker,
+                   range_owner(ranges.total(), ranges.workers(), lo + w.tiles - 1));
+}
+
+// Which rows of a V tile no row of the product sees; used by a whole warp.
+struct ClearRows {
+  int seen_b = -1;
   uint32_t seen = 0;  // drafted positions of sequence seen_b that some row sees: word i in lane i
-  if (lane < kWork && ranges.tiles(lane) == 0) p.merge[kWork * blockIdx.x + lane] = make_int4(-1, 0, 0, 0);
-  tiles.each([&](auto S, CacheLane& l) {
-    if (l.j == 0 && l.w.left == l.w.n && lane == 0) {  // the worker's last piece: does its unit go on?
-      int4 d = make_int4(-1, 0, 0, 0);
-      if (l.w.first + l.w.n < l.w.tiles) {
-        const int lo = ranges.first_tile(S.value) + ranges.tiles(S.value) - l.w.left - l.w.first;  // the unit's first tile
-        d = make_int4(l.w.b, l.w.u, l.w.first > 0 ? range_owner(ranges.total(), ranges.workers(), lo) : kWork * blockIdx.x + S.value,
-                      range_owner(ranges.total(), ranges.workers(), lo + l.w.tiles - 1));
-      }
-      p.merge[kWork * blockIdx.x + S.value] = d;
-    }
-    const int end = kv_end(l.w.len, p.n_new, p.S_max);
-    const int safe = keys_all_see(p, l.w.len);
-    const int key0 = (l.w.first + l.j) * kKvTile;
-    const bool fix = key0 + kKvTile > safe;
-    if (fix && seen_b != l.w.b) {
+  // Whether the tile reaches past the keys that every row sees.
+  __device__ __forceinline__ bool prepare(const CacheAttnParams& p, const CacheLane& l) {
+    if ((l.w.first + l.j + 1) * kKvTile <= keys_all_see(p, l.w.len)) return false;
+    if (seen_b != l.w.b) {
+      const int lane = threadIdx.x & 31;
+      const int W = (p.T + 31) / 32;
       seen_b = l.w.b;
       seen = 0xFFFFFFFFu;
-      if (p.mask && end >= 0) {
+      if (p.mask && kv_end(l.w.len, p.n_new, p.S_max) >= 0) {
         const uint32_t* m = p.mask + static_cast<size_t>(seen_b) * p.T * W;
         seen = 0u;
         for (int i = 0; i < W; ++i) {
@@ -300,25 +290,52 @@ __device__ __forceinline__ void clear_v(const CacheAttnParams& p, const CacheRan
         }
       }
     }
+    return true;
+  }
+  // at(row, c): address of 16-byte chunk c (0..15) of a tile row, or null
+  template <typename F>
+  __device__ __forceinline__ void rows(const CacheAttnParams& p, const CacheLane& l, F at) const {
+    const int lane = threadIdx.x & 31;
+    const bool bad = kv_end(l.w.len, p.n_new, p.S_max) < 0;
+    const int d0 = (l.w.first + l.j) * kKvTile - keys_all_see(p, l.w.len);  // drafted index of row 0
+    for (int r0 = 0; r0 < kKvTile; r0 += 32) {
+      const int d = d0 + r0 + lane;
+      const uint32_t word = __shfl_sync(0xffffffffu, seen, (d >> 5) & 7);
+      const bool dead = d >= 0 && (bad || d >= p.n_new || !((word >> (d & 31)) & 1u));
+      uint32_t todo = __ballot_sync(0xffffffffu, dead);
+      while (todo) {  // two rows at a time, 16 lanes each
+        const int ra = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int rb = todo ? __ffs(todo) - 1 : ra;
+        todo &= todo - 1;
+        uint8_t* dst = at(r0 + (lane < 16 ? ra : rb), lane & 15);
+        if (dst) *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+};
+
+// Whole warp 2.  Also publishes, for the merge, the unit that goes on past each worker's range.
+template <int kWork>
+__device__ __forceinline__ void clear_v(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
+                                        uint8_t* ring) {
+  CacheTiles<kWork> tiles(p, ranges);
+  volatile int* abort_flag = bar.abort_flag();
+  const int lane = threadIdx.x & 31;
+  ClearRows clear;
+  int it = 0;
+  if (lane < kWork && ranges.tiles(lane) == 0) p.merge[kWork * blockIdx.x + lane] = make_int4(-1, 0, 0, 0);
+  tiles.each([&](auto S, CacheLane& l) {
+    const int worker = kWork * blockIdx.x + S.value;
+    if (lane == 0 && l.j == 0 && l.w.left == l.w.n) p.merge[worker] = goes_on(ranges, l.w, S.value, worker);
+    const bool fix = clear.prepare(p, l);
     // every tile is waited for and released, so that this warp stays in step with the ring
     const int st = it % kVStages;
     if (!__all_sync(0xffffffffu, mbar_wait(bar.v_full(st), (it / kVStages) & 1, abort_flag, p.status))) return false;
     if (fix) {
-      uint8_t* tile = ring + st * kKvTileBytes;
-      for (int r0 = 0; r0 < kKvTile; r0 += 32) {
-        const int d = key0 + r0 + lane - safe;  // drafted index of this lane's row
-        const uint32_t word = __shfl_sync(0xffffffffu, seen, (d >> 5) & 7);
-        const bool dead = d >= 0 && (end < 0 || d >= p.n_new || !((word >> (d & 31)) & 1u));
-        uint32_t todo = __ballot_sync(0xffffffffu, dead);
-        while (todo) {  // two rows at a time, 16 lanes each (a row is 8 chunks in either half)
-          const int ra = __ffs(todo) - 1;
-          todo &= todo - 1;
-          const int rb = todo ? __ffs(todo) - 1 : ra;
-          todo &= todo - 1;
-          const int r = r0 + (lane < 16 ? ra : rb), c = lane & 15;
-          *reinterpret_cast<uint4*>(tile + (c >> 3) * kKvHalfBytes + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-      }
+      clear.rows(p, l, [&](int r, int c) {
+        return ring + st * kKvTileBytes + (c >> 3) * kKvHalfBytes + r * 128 + (c & 7) * 16;
+      });
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.v_fixed(st));
@@ -329,7 +346,7 @@ __device__ __forceinline__ void clear_v(const CacheAttnParams& p, const CacheRan
   });
 }
 
-// The whole of warp 1.  In turn for each tile and item: S (issue_s), then the PV of the item before
+// The whole of warp 1.  In turn for each tile: S (issue_s), then the PV of the tile before
 // (issue_pv_mma), so that the tensor core works while a softmax runs.
 //   issue_s(S buffer, query buffer, K stage): the UMMAs of S
 //   issue_pv_mma(S buffer, O buffer, V stage, half, first): those of O += P V for keys 64 half .. + 63
@@ -337,7 +354,6 @@ __device__ __forceinline__ void clear_v(const CacheAttnParams& p, const CacheRan
 template <int kMode, int kHalves, typename FS, typename FP>
 __device__ __forceinline__ void issue_all(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
                                           FS issue_s, FP issue_pv_mma) {
-  constexpr int kItems = mode_items(kMode);
   CacheTiles<mode_workers(kMode)> tiles(p, ranges);
   volatile int* abort_flag = bar.abort_flag();
   auto wait = [&](uint64_t* b, uint32_t parity) {
@@ -347,7 +363,7 @@ __device__ __forceinline__ void issue_all(const CacheAttnParams& p, const CacheR
   uint32_t p_par = 0;    // bit i: parity of S buffer i's next P
   struct Pending {
     int slot, o, turn, it;           // S and O buffer, pieces that had the O before, tile count
-    bool first, last, fix, release;  // first / last tile of the piece; V tile to be cleared; V tile done
+    bool first, last, fix;           // first / last tile of the piece; V tile to be cleared
   } pend{};
   bool has_pend = false;
   auto issue_pv = [&] {
@@ -370,7 +386,8 @@ __device__ __forceinline__ void issue_all(const CacheAttnParams& p, const CacheR
       if (elect_one_sync()) {
         issue_pv_mma(d.slot, d.o, vs, hf, d.first);
         if (hf == kHalves - 1) {
-          if (d.release) umma_commit(bar.v_empty(vs));
+          umma_commit(bar.v_empty(vs));
+          if (kMode == kOneTile) umma_commit(bar.pv_done(d.slot));
           if (d.last) umma_commit(bar.o_full(d.o));
         }
       }
@@ -384,28 +401,24 @@ __device__ __forceinline__ void issue_all(const CacheAttnParams& p, const CacheR
     const bool first = l.j == 0, last = l.j == l.w.n - 1;
     const int ks = it % kKStages;
     const int turn = piece_turn<kMode>(l.piece);
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int slot = kMode == kTwoWorkers ? S.value : kMode == kOneTile ? it & 1 : i;
-      const int at = piece_buffer<kMode>(S.value, i, l.piece);
-      // P of the buffer's last tile is used up before the softmax of S takes its place (the other
-      // worker has no more tiles in between)
-      if (kMode == kTwoWorkers && has_pend && pend.slot == slot && !issue_pv()) return false;
-      if (first && !wait(bar.q_full(at), turn & 1)) return false;
-      if (i == 0 && !wait(bar.k_full(ks), (it / kKStages) & 1)) return false;
-      tc_fence_after();
-      const bool last_item = i == kItems - 1;
-      if (elect_one_sync()) {
-        issue_s(slot, at, ks);
-        umma_commit(bar.s_full(slot));
-        if (last_item) umma_commit(bar.k_empty(ks));
-        if (last) umma_commit(bar.q_empty(at));
-      }
-      __syncwarp();
-      if (has_pend && !issue_pv()) return false;
-      pend = Pending{slot, at, turn, it, first, last, fix && i == 0, last_item};
-      has_pend = true;
+    const int slot = kMode == kTwoWorkers ? S.value : it & 1;
+    const int at = piece_buffer<kMode>(S.value, l.piece);
+    // P of the buffer's last tile is used up before the softmax of S takes its place (the other
+    // worker has no more tiles in between)
+    if (kMode == kTwoWorkers && has_pend && pend.slot == slot && !issue_pv()) return false;
+    if (first && !wait(bar.q_full(at), turn & 1)) return false;
+    if (!wait(bar.k_full(ks), (it / kKStages) & 1)) return false;
+    tc_fence_after();
+    if (elect_one_sync()) {
+      issue_s(slot, at, ks);
+      umma_commit(bar.s_full(slot));
+      umma_commit(bar.k_empty(ks));
+      if (last) umma_commit(bar.q_empty(at));
     }
+    __syncwarp();
+    if (has_pend && !issue_pv()) return false;
+    pend = Pending{slot, at, turn, it, first, last, fix};
+    has_pend = true;
     ++it;
     return true;
   });
