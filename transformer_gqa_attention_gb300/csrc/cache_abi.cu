@@ -32,7 +32,7 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   p.status = c->status;
   p.scale_log2 = kScaleLog2;
   const bool pair = a.T > kOneTilePos;
-  p.group_pos = a.T <= kFewPos ? kFewPos : pair ? 64 : kOneTilePos;
+  p.group_pos = pair ? 64 : kOneTilePos;
   p.row_groups = (a.T + p.group_pos - 1) / p.group_pos;
   p.part_rows = static_cast<int>(round_up(4 * std::min(a.T, p.group_pos), 32));
 
@@ -42,9 +42,9 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
     off = round_up(off + bytes, 256);
     return at;
   };
-  // workers: CTAs, with few positions their two softmax slots, with many CTA pairs; each may hold two
-  // partial results
-  const size_t workers = a.T <= kFewPos ? 2 * n_ctas : pair ? n_ctas / 2 : n_ctas;
+  // workers: CTAs, with weights their two softmax slots, with many positions CTA pairs; each may hold
+  // two partial results
+  const size_t workers = a.weights ? 2 * n_ctas : pair ? n_ctas / 2 : n_ctas;
   const size_t slots = 2 * workers;
   const size_t merge = take(workers * sizeof(int4));
   const size_t part_ml = take(slots * p.part_rows * sizeof(float2));
@@ -77,7 +77,7 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   // queries as (d, head, position, sequence): a box is 64 d of the group's 4 heads
   const uint64_t dims[4] = {128, 4ull * G, static_cast<uint64_t>(a.T), static_cast<uint64_t>(a.B)};
   const uint64_t strides[3] = {256, static_cast<uint64_t>(G) * 1024, static_cast<uint64_t>(a.T) * G * 1024};
-  const uint32_t box[4] = {64, 4, static_cast<uint32_t>(cache_attn_box(p)), 1};
+  const uint32_t box[4] = {64, 4, a.weights ? 1u : kOneTilePos, 1};
   if (!make_map(&tq, a.q, 4, dims, strides, box) ||
       !map_cache(&tk, a.cache_k, a.B, a.S_max, G, a.S_max, pair ? kKvTile / 2 : kKvTile) ||
       !map_cache(&tv, a.cache_v, a.B, a.S_max, G, a.S_max, kKvTile))
@@ -89,7 +89,7 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   }
   if (a.weights) {
     ProfScope ps(c, GQA_KERNEL_CACHE_WEIGHTS, s);
-    GQA_CUDA(launch_cache_weights(p, static_cast<int>(workers), 4 * c->num_sms, s));
+    GQA_CUDA(launch_cache_weights(p, static_cast<int>(workers), 8 * c->num_sms, s));
   } else {
     ProfScope ps(c, GQA_KERNEL_CACHE_MERGE, s);
     GQA_CUDA(launch_cache_merge(p, static_cast<int>(workers), s));

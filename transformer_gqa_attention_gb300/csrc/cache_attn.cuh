@@ -1,6 +1,5 @@
-// cache_attn.cuh — attention of 17 to 32 positions per sequence over caches whose lengths differ from
-// sequence to sequence (cache_roles.cuh has the CTA's roles; cache_attn_few.cuh the kernel for fewer
-// positions, cache_attn_pair.cuh the one for more).
+// cache_attn.cuh — attention of up to 32 positions per sequence over caches whose lengths differ from
+// sequence to sequence (cache_roles.cuh has the CTA's roles; cache_attn_pair.cuh the kernel for more).
 //
 // The four query heads of a kv head read the same keys and values, so the tensor core's 128 rows
 // are 32 positions x 4 heads: row 4t + h.  Every K/V byte then serves all rows of up to 32
@@ -108,9 +107,9 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
         m_used = m_new;
         l_sum *= alpha;
         if (j > 0) {
-          // O holds the sum through the tile before once its PV, issued behind this tile's S, is done (a
-          // wait given up shows at the next tile)
-          __all_sync(0xffffffffu, wait(bar.pv_done(slot ^ 1), ((it - 1) >> 1) & 1));
+          // O holds the sum through the tile before once its PV, issued behind this tile's S, is done and
+          // has released its V (a wait given up shows at the next tile)
+          __all_sync(0xffffffffu, wait(bar.v_empty((it - 1) % Bars::kV), ((it - 1) / Bars::kV) & 1));
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 2; ++c) {

@@ -23,14 +23,15 @@ namespace gqa {
 
 struct CachePairBars {
   static constexpr int kStages = 5;  // each of K and V
-  static constexpr int kCount = 17 + 5 * kStages;
+  static constexpr int kV = kStages;
+  static constexpr int kCount = 15 + 5 * kStages;
   static constexpr int kBytes = 384;
   uint64_t* bars;
   __device__ __forceinline__ explicit CachePairBars(uint8_t* at) : bars(reinterpret_cast<uint64_t*>(at)) {}
   // CTA 0's: both CTAs' bytes of the queries and of K, and both CTAs' word that V is there and clear
   __device__ __forceinline__ uint64_t* q_full(int i) const { return bars + i; }
-  __device__ __forceinline__ uint64_t* k_full(int i) const { return bars + 17 + i; }
-  __device__ __forceinline__ uint64_t* v_ready(int i) const { return bars + 17 + kStages + i; }
+  __device__ __forceinline__ uint64_t* k_full(int i) const { return bars + 15 + i; }
+  __device__ __forceinline__ uint64_t* v_ready(int i) const { return bars + 15 + kStages + i; }
   // CTA 0's: an arrival of every softmax warp of both CTAs that writes P's half, or reads O
   __device__ __forceinline__ uint64_t* p_lo(int i) const { return bars + 2 + i; }
   __device__ __forceinline__ uint64_t* p_hi(int i) const { return bars + 4 + i; }
@@ -40,16 +41,15 @@ struct CachePairBars {
   __device__ __forceinline__ uint64_t* s_full(int i) const { return bars + 10 + i; }
   __device__ __forceinline__ uint64_t* o_full(int i) const { return bars + 12 + i; }
   __device__ __forceinline__ uint64_t* drain() const { return bars + 14; }
-  __device__ __forceinline__ uint64_t* pv_done(int i) const { return bars + 15 + i; }
-  __device__ __forceinline__ uint64_t* k_empty(int i) const { return bars + 17 + 2 * kStages + i; }
-  __device__ __forceinline__ uint64_t* v_full(int i) const { return bars + 17 + 3 * kStages + i; }
-  __device__ __forceinline__ uint64_t* v_empty(int i) const { return bars + 17 + 4 * kStages + i; }
+  __device__ __forceinline__ uint64_t* k_empty(int i) const { return bars + 15 + 2 * kStages + i; }
+  __device__ __forceinline__ uint64_t* v_full(int i) const { return bars + 15 + 3 * kStages + i; }
+  __device__ __forceinline__ uint64_t* v_empty(int i) const { return bars + 15 + 4 * kStages + i; }
   __device__ __forceinline__ uint32_t* tmem_holder() const { return reinterpret_cast<uint32_t*>(bars + kCount); }
   __device__ __forceinline__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(tmem_holder() + 1); }
   __device__ __forceinline__ void init() const {
     for (int i = 0; i < kCount; ++i) {
       const bool p_half = i >= 2 && i < 6, o = i == 6 || i == 7;
-      const bool v_ready = i >= 17 + kStages && i < 17 + 2 * kStages;
+      const bool v_ready = i >= 15 + kStages && i < 15 + 2 * kStages;
       mbar_init(&bars[i], p_half ? 8u : o ? 16u : v_ready ? 2u : 1u);
     }
     *abort_flag() = 0;
@@ -101,6 +101,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   cluster_sync();  // the peer's barriers are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *bar.tmem_holder();
+  const uint64_t policy = kv_policy(p);
   const bool no_loads = p.fault && worker == 0;  // test hook: pair 0's consumers wait out and abort
   auto cta0 = [&](uint64_t* b) { return mapa_shared(smem_u32(b), 0); };
 
@@ -115,8 +116,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         if (rank == 0) mbar_arrive_expect_tx(bar.k_full(st), 2 * L::kStage);
         uint8_t* dst = smem + L::kK + st * L::kStage;
         const int g = l.w.u / p.row_groups, key0 = (l.w.first + l.j) * kKvTile + 64 * rank;
-        tma_load_4d_pair(dst, &tmK, cta0(bar.k_full(st)), 0, g, key0, l.w.b);
-        tma_load_4d_pair(dst + L::kStage / 2, &tmK, cta0(bar.k_full(st)), 64, g, key0, l.w.b);
+        tma_load_4d_pair_hint(dst, &tmK, cta0(bar.k_full(st)), 0, g, key0, l.w.b, policy);
+        tma_load_4d_pair_hint(dst + L::kStage / 2, &tmK, cta0(bar.k_full(st)), 64, g, key0, l.w.b, policy);
         ++it;
         return true;
       });
@@ -144,7 +145,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         const int st = it % kStages;
         if (!mbar_wait(bar.v_empty(st), ((it / kStages) & 1) ^ 1u, abort_flag, p.status)) return false;
         mbar_arrive_expect_tx(bar.v_full(st), L::kStage);
-        tma_load_4d(smem + L::kV + st * L::kStage, &tmV, bar.v_full(st), 64 * rank, g, (l.w.first + l.j) * kKvTile, l.w.b);
+        tma_load_4d_hint(smem + L::kV + st * L::kStage, &tmV, bar.v_full(st), 64 * rank, g,
+                         (l.w.first + l.j) * kKvTile, l.w.b, policy);
         ++it;
         return true;
       });
@@ -220,7 +222,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
             }
             if (hf) {
               umma_commit_pair(bar.v_empty(vs), 0x3);
-              umma_commit_pair(bar.pv_done(slot), 0x3);
               if (d.last) umma_commit_pair(bar.o_full(o), 0x3);
             }
           }

@@ -11,7 +11,7 @@
 namespace gqa {
 
 // Unnormalised sum of pieces k0, k0 + step, ... of a block of a cut unit's O, N float4 per lane:
-// with kByRow (scratch [row][128 d], at most kFewPos positions) rows row0 .. row0 + rows - 1 (at
+// with kByRow (scratch [row][128 d], the decode step with weights) rows row0 .. row0 + rows - 1 (at
 // most N), lane = float4 column; else (scratch [float4 column][row]) float4 columns col0 .. col0 +
 // N - 1 of row row0 + lane.  M and l: the rows' maximum and sum; acc is relative to M.
 template <bool kByRow, int N>
@@ -66,8 +66,7 @@ __device__ __forceinline__ uint2 pack4(float4 v, float f) {
   return make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
 }
 
-constexpr int kMergeY = 8;      // blocks per worker
-constexpr int kMergeFewY = 4;   // at most kFewPos positions
+constexpr int kMergeY = 8;  // blocks per worker
 
 // Joins the pieces of the unit that goes on past worker v's range, described by d.  A unit of n
 // pieces goes on past n - 1 workers, whose blocks share it: of theirs, this is block i of `blocks`.
@@ -139,7 +138,6 @@ __device__ __forceinline__ void merge_unit(const CacheAttnParams& p, const int4&
   }
 }
 
-template <bool kByRow>
 __global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttnParams p) {
   griddep_launch_dependents();
   griddep_wait();
@@ -148,7 +146,21 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttnParams 
   const int st = *reinterpret_cast<volatile const int*>(p.status);
   // after a wait that ran out the scratch may be unwritten
   if (d.x < 0 || (st & kDevErrTimeout)) return;
-  merge_unit<kByRow>(p, d, (v - d.z) * gridDim.y + blockIdx.y, (d.w - d.z) * gridDim.y);
+  merge_unit<false>(p, d, (v - d.z) * gridDim.y + blockIdx.y, (d.w - d.z) * gridDim.y);
+}
+
+// (maximum, sum) of four heads from 16-byte aligned memory.
+__device__ __forceinline__ void load_ml(const float2* at, float2 (&m)[4]) {
+  const float4 a = __ldcg(reinterpret_cast<const float4*>(at)), b = __ldcg(reinterpret_cast<const float4*>(at) + 1);
+  m[0] = make_float2(a.x, a.y);
+  m[1] = make_float2(a.z, a.w);
+  m[2] = make_float2(b.x, b.y);
+  m[3] = make_float2(b.z, b.w);
+}
+
+__device__ __forceinline__ float2 join_ml(float2 a, float2 b) {
+  const float top = fmaxf(a.x, b.x), tz = top == -INFINITY ? 0.f : top;
+  return make_float2(top, a.y * fast_exp2(a.x - tz) + b.y * fast_exp2(b.x - tz));
 }
 
 // The decode step with key weights: blocks 0 .. workers - 1 merge, the others add each key's
@@ -169,56 +181,59 @@ __global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnParam
   const int n_warps = (gridDim.x - workers) * 8;
   const int R = p.part_rows;
   if (*reinterpret_cast<volatile const int*>(p.status) & kDevErrTimeout) return;
-  // tiles of a warp are n_warps apart: neighbouring warps read neighbouring scores
+  // neighbouring warps have neighbouring tiles
   for (int i = (blockIdx.x - workers) * 8 + warp; i < total; i += n_warps) {
     const int2 tu = __ldcg(p.tile_unit + i);
-    const float4* s = reinterpret_cast<const float4*>(p.scores) + static_cast<size_t>(i) * kKvTile;
-    float x[4][4];
+    float4 x[4];  // keys 32 k + lane, their four heads' scores
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 v = __ldcg(s + 32 * k + lane);
-      x[0][k] = v.x;
-      x[1][k] = v.y;
-      x[2][k] = v.z;
-      x[3][k] = v.w;
-    }
+    for (int k = 0; k < 4; ++k)
+      x[k] = __ldcg(reinterpret_cast<const float4*>(p.scores) + static_cast<size_t>(i) * kKvTile + 32 * k + lane);
     const int2 cs = __ldcg(p.unit_workers + tu.x);
     float* w = p.weights + static_cast<size_t>(tu.x) * p.S_max + tu.y * kKvTile;
     bool seen[4];
     float a[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {  // -inf in all four heads: past the end (or of no weight)
-      seen[k] = x[0][k] != -INFINITY || x[1][k] != -INFINITY || x[2][k] != -INFINITY || x[3][k] != -INFINITY;
+      seen[k] = x[k].x != -INFINITY || x[k].y != -INFINITY || x[k].z != -INFINITY || x[k].w != -INFINITY;
       a[k] = seen[k] ? __ldcg(w + 32 * k + lane) : 0.f;
     }
-    float add[4] = {0.f, 0.f, 0.f, 0.f};
+    // the heads' maxima and sums: the unit's, or of its pieces joined
+    float2 m[4];
+    if (cs.x == cs.y) {
+      load_ml(p.unit_ml + tu.x * 4, m);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) m[h] = make_float2(-INFINITY, 0.f);
+      const int n = cs.y - cs.x + 1;
+      const bool shared = n > 8;  // many pieces: the lanes share them
+      for (int k = shared ? lane : 0; k < n; k += shared ? 32 : 1) {
+        float2 o[4];
+        load_ml(p.part_ml + static_cast<size_t>(k ? partial_slot(cs.x + k, true) : partial_slot(cs.x, false)) * R, o);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) m[h] = join_ml(m[h], o[h]);
+      }
+      if (shared) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            m[h] = join_ml(m[h], make_float2(__shfl_xor_sync(0xffffffffu, m[h].x, o), __shfl_xor_sync(0xffffffffu, m[h].y, o)));
+      }
+    }
+    float inv[4];
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-      float2 m = make_float2(-INFINITY, 0.f);
-      if (cs.x == cs.y) {
-        m = __ldcg(p.unit_ml + tu.x * 4 + h);
-      } else {  // a cut unit: its pieces' maxima and sums, shared by the lanes
-        for (int k = lane; k <= cs.y - cs.x; k += 32) {
-          const int ps = k ? partial_slot(cs.x + k, true) : partial_slot(cs.x, false);
-          const float2 o = __ldcg(p.part_ml + static_cast<size_t>(ps) * R + h);
-          const float top = fmaxf(m.x, o.x), tz = top == -INFINITY ? 0.f : top;
-          m = make_float2(top, m.y * fast_exp2(m.x - tz) + o.y * fast_exp2(o.x - tz));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const float2 q = make_float2(__shfl_xor_sync(0xffffffffu, m.x, o), __shfl_xor_sync(0xffffffffu, m.y, o));
-          const float top = fmaxf(m.x, q.x), tz = top == -INFINITY ? 0.f : top;
-          m = make_float2(top, m.y * fast_exp2(m.x - tz) + q.y * fast_exp2(q.x - tz));
-        }
-      }
-      const float M = m.x == -INFINITY ? 0.f : m.x;
-      const float inv = 1.f / m.y;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) add[k] += fast_exp2(fmaf(x[h][k], p.scale_log2, -M)) * inv;
+      inv[h] = 1.f / m[h].y;
+      if (m[h].x == -INFINITY) m[h].x = 0.f;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (seen[k]) w[32 * k + lane] = a[k] + add[k];
+    for (int k = 0; k < 4; ++k) {
+      const float add = fast_exp2(fmaf(x[k].x, p.scale_log2, -m[0].x)) * inv[0] +
+                        fast_exp2(fmaf(x[k].y, p.scale_log2, -m[1].x)) * inv[1] +
+                        fast_exp2(fmaf(x[k].z, p.scale_log2, -m[2].x)) * inv[2] +
+                        fast_exp2(fmaf(x[k].w, p.scale_log2, -m[3].x)) * inv[3];
+      if (seen[k]) w[32 * k + lane] = a[k] + add;
+    }
   }
 }
 

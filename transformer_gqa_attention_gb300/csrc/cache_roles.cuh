@@ -13,7 +13,7 @@
 //   warps 4..11 softmax
 // Which products they work on is the kernel's mode:
 //   kTwoWorkers  warps 4..7 and 8..11 are workers of their own (kv_sched.h), each with its own range
-//                of tiles, queries, S and O (cache_attn_few.cuh)
+//                of tiles, queries, S and O (cache_decode.cuh)
 //   kOneTile     one worker: S alternates between two buffers from tile to tile, queries and O from
 //                piece to piece (cache_attn.cuh)
 #pragma once
@@ -45,7 +45,8 @@ constexpr int kKStages = 2;
 constexpr int kVStages = 3;
 
 struct CacheBars {
-  static constexpr int kCount = 30;
+  static constexpr int kV = kVStages;  // V stages
+  static constexpr int kCount = 28;
   static constexpr int kBytes = 256;  // barriers, TMEM address, abort flag
   uint64_t* bars;
   __device__ __forceinline__ explicit CacheBars(uint8_t* at) : bars(reinterpret_cast<uint64_t*>(at)) {}
@@ -58,8 +59,6 @@ struct CacheBars {
   __device__ __forceinline__ uint64_t* s_full(int slot) const { return bars + 14 + slot; }
   __device__ __forceinline__ uint64_t* o_full(int slot) const { return bars + 16 + slot; }
   __device__ __forceinline__ uint64_t* drain() const { return bars + 18; }
-  // kOneTile: the PV that used the S buffer's P is done
-  __device__ __forceinline__ uint64_t* pv_done(int slot) const { return bars + 28 + slot; }
   // 2 arrivals: the PV that used the tile, and warp 2
   __device__ __forceinline__ uint64_t* v_empty(int stage) const { return bars + 19 + stage; }
   // arrivals of its writers: P of the tile's first and second 64 keys (or of all of them: lo)
@@ -70,7 +69,7 @@ struct CacheBars {
   __device__ __forceinline__ uint32_t* tmem_holder() const { return reinterpret_cast<uint32_t*>(bars + kCount); }
   __device__ __forceinline__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(tmem_holder() + 1); }
   __device__ __forceinline__ void init(uint32_t p_writers, uint32_t o_readers) const {
-    for (int i = 0; i < kCount; ++i) mbar_init(&bars[i], i < 19 ? 1u : i < 22 ? 2u : i < 26 ? p_writers : i < 28 ? o_readers : 1u);
+    for (int i = 0; i < kCount; ++i) mbar_init(&bars[i], i < 19 ? 1u : i < 22 ? 2u : i < 26 ? p_writers : o_readers);
     *abort_flag() = 0;
     fence_mbar_init();
   }
@@ -193,12 +192,17 @@ struct CacheTiles {
   }
 };
 
+// K and V are read once, unless a sequence has several groups of rows: they leave L2 first, which
+// keeps the partial results, the scores and the kernel's own code there.
+__device__ __forceinline__ uint64_t kv_policy(const CacheAttnParams& p) { return l2_policy(p.row_groups == 1); }
+
 // Lane 0 of warp 0.
 template <int kWork>
 __device__ __forceinline__ void produce_k(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
                                           const CUtensorMap* tmK, uint8_t* ring) {
   CacheTiles<kWork> tiles(p, ranges);
   volatile int* abort_flag = bar.abort_flag();
+  const uint64_t policy = kv_policy(p);
   int it = 0;
   tiles.each([&](auto, CacheLane& l) {
     const int st = it % kKStages;
@@ -206,8 +210,8 @@ __device__ __forceinline__ void produce_k(const CacheAttnParams& p, const CacheR
     mbar_arrive_expect_tx(bar.k_full(st), kKvTileBytes);
     uint8_t* dst = ring + st * kKvTileBytes;
     const int g = l.w.u / p.row_groups, key0 = (l.w.first + l.j) * kKvTile;
-    tma_load_4d(dst, tmK, bar.k_full(st), 0, g, key0, l.w.b);
-    tma_load_4d(dst + kKvHalfBytes, tmK, bar.k_full(st), 64, g, key0, l.w.b);
+    tma_load_4d_hint(dst, tmK, bar.k_full(st), 0, g, key0, l.w.b, policy);
+    tma_load_4d_hint(dst + kKvHalfBytes, tmK, bar.k_full(st), 64, g, key0, l.w.b, policy);
     ++it;
     return true;
   });
@@ -223,6 +227,7 @@ __device__ __forceinline__ void produce_vq(const CacheAttnParams& p, const Cache
                                            int q_half, uint8_t* ring) {
   CacheTiles<mode_workers(kMode)> tiles(p, ranges);
   volatile int* abort_flag = bar.abort_flag();
+  const uint64_t policy = kv_policy(p);
   int it = 0, asked = 0;  // queries asked for: buffer 0 in the low half, 1 in the high
   tiles.each([&](auto S, CacheLane& l) {
     const int g = l.w.u / p.row_groups;
@@ -241,8 +246,8 @@ __device__ __forceinline__ void produce_vq(const CacheAttnParams& p, const Cache
     mbar_arrive_expect_tx(bar.v_full(st), kKvTileBytes);
     uint8_t* dst = ring + st * kKvTileBytes;
     const int key0 = (l.w.first + l.j) * kKvTile;
-    tma_load_4d(dst, tmV, bar.v_full(st), 0, g, key0, l.w.b);
-    tma_load_4d(dst + kKvHalfBytes, tmV, bar.v_full(st), 64, g, key0, l.w.b);
+    tma_load_4d_hint(dst, tmV, bar.v_full(st), 0, g, key0, l.w.b, policy);
+    tma_load_4d_hint(dst + kKvHalfBytes, tmV, bar.v_full(st), 64, g, key0, l.w.b, policy);
     ++it;
     return true;
   });
@@ -387,7 +392,6 @@ __device__ __forceinline__ void issue_all(const CacheAttnParams& p, const CacheR
         issue_pv_mma(d.slot, d.o, vs, hf, d.first);
         if (hf == kHalves - 1) {
           umma_commit(bar.v_empty(vs));
-          if (kMode == kOneTile) umma_commit(bar.pv_done(d.slot));
           if (d.last) umma_commit(bar.o_full(d.o));
         }
       }

@@ -75,7 +75,6 @@ cudaError_t launch_decode_combine(const DecodeParams& p, int B, cudaStream_t s);
 cudaError_t launch_exp2_compare(const float* a, float* out_fma, float* out_mufu, int n, cudaStream_t s);
 // Attention over caches of per-sequence length, and the cache's own upkeep.
 cudaError_t configure_cache_attn();
-int cache_attn_box(const CacheAttnParams& p);
 cudaError_t launch_cache_attn(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                               const CacheAttnParams& p, int n_ctas, cudaStream_t s);
 cudaError_t launch_cache_merge(const CacheAttnParams& p, int workers, cudaStream_t s);

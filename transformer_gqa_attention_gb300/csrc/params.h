@@ -86,10 +86,8 @@ struct DecodeParams {
   float scale_log2;
 };
 
-// At most this many positions per sequence run with the keys, not the rows, on the tensor core's
-// 128 rows.
-constexpr int kFewPos = 16;
-// At most this many run on one 128-row tile (positions x 4 heads), more on two tiles of a CTA pair.
+// At most this many positions run on one 128-row tile (positions x 4 heads), more on the two tiles of a
+// CTA pair.
 constexpr int kOneTilePos = 32;
 
 // Attention of a few positions per sequence over caches of per-sequence length (tree attention,
@@ -106,8 +104,7 @@ struct CacheAttnParams {
   int* status;
   int fault;               // test hook: CTA 0 issues no loads (its waits run out)
   float scale_log2;        // log2(e) / sqrt(128)
-  // rows: a kv head's T positions in row_groups groups of group_pos (kFewPos, kOneTilePos, or 64
-  // on two row tiles)
+  // rows: a kv head's T positions in row_groups groups of group_pos (kOneTilePos, or 64 on two tiles)
   int row_groups, group_pos;
   // scratch: per worker the unit that goes on past its range (sequence or -1, unit, the unit's first
   // and last worker), the partial results of cut units ([2 workers][32 float4 columns][part_rows], or with at most
