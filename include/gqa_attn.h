@@ -446,7 +446,7 @@ gqa_status attn_decode_attention_noalloc_debug_inject_timeout(void);
  * attn_debug_inject_timeout — test hook for the failure path (no counterpart on the pages).
  * Arms a one-shot flag: on the next launch of kernel kind `kind` (GQA_KERNEL_QKV_GEMM,
  * _QKV_SPLITK, _FLASH_PREFILL, _DECODE_ATTN, _OUT_GEMM, _OUT_SPLITK or _CACHE_ATTN) made through this
- * context, the first work unit's TMA producer issues no loads.  Its consumers' bounded
+ * context, the first work unit's (_CACHE_ATTN: the last worker's) TMA producer issues no loads.  Its consumers' bounded
  * waits then run out (about 2 s), the unit records GQA_ERR_TIMEOUT in the status word,
  * releases its tensor memory and returns; kernels queued after it on the stream may time
  * out too.  Nothing faults or hangs.  The outputs of that call are undefined; the next
@@ -476,8 +476,9 @@ gqa_status attn_debug_pair_schedule(int m_tiles, int n_tiles, int n_pairs, int *
  * 128-key tiles of B sequences among `workers` workers (CTAs or their softmax slots), computed
  * on the host by the code that the kernel runs (for tests, no GPU needed).  lens [B] (host), n_new
  * keys behind each length, units (kv heads x groups of query rows) per sequence.  Writes the
- * pieces in order as septuples (worker, sequence, unit, first tile, tiles, slot of its partial
- * result or -1 for a whole unit, last worker of the unit) into pieces[7 * max_pieces]; *n_pieces gets their count.  Errors:
+ * pieces in order as octuples (worker, sequence, unit, first tile, tiles, slot of its partial
+ * result or -1 for a whole unit, last worker of the unit, number of the first tile among all
+ * tiles) into pieces[8 * max_pieces]; *n_pieces gets their count.  Errors:
  * GQA_ERR_INVALID_ARG, GQA_ERR_SHAPE (more than max_pieces pieces; *n_pieces holds the count).
  */
 gqa_status attn_debug_cache_schedule(const int *lens, int B, int n_new, int S_max, int units, int workers,

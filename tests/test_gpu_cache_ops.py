@@ -449,7 +449,7 @@ def test_evict_refuses_partial_overlaps():
 # ------------------------------------------------------------------------------- failure path
 @pytest.mark.parametrize("weights", [False, True])
 def test_a_wait_that_runs_out_is_reported(weights):
-    # CTA 0 issues no loads: its waits run out, the status says so, and the next call is right
+    # the last worker issues no loads: its waits run out, the status says so, and the next call is right
     ctx = context()
     gen = torch.Generator().manual_seed(11)
     k, v = (t.to(DEV) for t in draw_cache(gen, 2, 900, 8, [800, 800]))

@@ -326,7 +326,7 @@ def attn_cache_evict(ctx, cache_k, cache_v, weights, B, S_max, kv_len, budget, n
 def attn_debug_cache_schedule(lens, n_new, S_max, units, workers):
     """The pieces in which workers share the sequences' key tiles (host computation, no GPU
     needed): a list of (worker, sequence, unit, first tile, tiles, partial slot or -1, the unit's
-    last worker)."""
+    last worker, the first tile's number among all tiles)."""
     i32 = ctypes.c_int
     B = len(lens)
     arr, n = (i32 * B)(*lens), i32()
@@ -334,10 +334,10 @@ def attn_debug_cache_schedule(lens, n_new, S_max, units, workers):
     st = L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, workers, None, 0, ctypes.byref(n))
     if st not in (0, 2):  # GQA_ERR_SHAPE: the count is in n
         _check("attn_debug_cache_schedule", st)
-    buf = (i32 * (7 * max(n.value, 1)))()
+    buf = (i32 * (8 * max(n.value, 1)))()
     _check("attn_debug_cache_schedule",
            L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, workers, buf, n.value, ctypes.byref(n)))
-    return [tuple(buf[7 * i:7 * i + 7]) for i in range(n.value)]
+    return [tuple(buf[8 * i:8 * i + 8]) for i in range(n.value)]
 
 
 def attn_destroy(ctx):

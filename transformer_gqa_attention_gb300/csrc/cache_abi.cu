@@ -49,14 +49,13 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   const size_t merge = take(workers * sizeof(int4));
   const size_t part_ml = take(slots * p.part_rows * sizeof(float2));
   const size_t part_o = take(slots * p.part_rows * 128 * sizeof(float));
-  size_t total = 0, scores = 0, tile_unit = 0, unit_workers = 0, unit_ml = 0;
+  size_t total = 0, scores = 0, tile_unit = 0, unit_ml = 0;
   if (a.weights) {
     const size_t units = static_cast<size_t>(a.B) * G;
     const size_t tiles = units * ((a.S_max + kKvTile - 1) / kKvTile);
     total = take(sizeof(int));
     scores = take(tiles * 4 * kKvTile * sizeof(float));
-    tile_unit = take(tiles * sizeof(int2));
-    unit_workers = take(units * sizeof(int2));
+    tile_unit = take(tiles * sizeof(int4));
     unit_ml = take(units * 4 * sizeof(float2));
   }
   gqa_status st = ensure_buffer(c, c->cache_ws, off, s);
@@ -68,8 +67,7 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   if (a.weights) {
     p.total_tiles = reinterpret_cast<int*>(ws + total);
     p.scores = reinterpret_cast<float*>(ws + scores);
-    p.tile_unit = reinterpret_cast<int2*>(ws + tile_unit);
-    p.unit_workers = reinterpret_cast<int2*>(ws + unit_workers);
+    p.tile_unit = reinterpret_cast<int4*>(ws + tile_unit);
     p.unit_ml = reinterpret_cast<float2*>(ws + unit_ml);
   }
 
@@ -259,30 +257,29 @@ gqa_status attn_debug_cache_schedule(const int* lens, int B, int n_new, int S_ma
       workers < 1 || max_pieces < 0)
     return GQA_ERR_INVALID_ARG;
   auto len_of = [&](int b) { return b < B ? lens[b] : 0; };
-  auto tiles_of = [&](int b) { return kv_tiles(kv_end(len_of(b), n_new, S_max)); };
+  auto places_of = [&](int b) { return (kv_tiles(kv_end(len_of(b), n_new, S_max)) + kUnitCost) * units; };
   long long all = 0;
-  for (int b = 0; b < B; ++b) all += static_cast<long long>(tiles_of(b)) * units;
+  for (int b = 0; b < B; ++b) all += (static_cast<long long>(kv_tiles(kv_end(lens[b], n_new, S_max))) + kUnitCost) * units;
   if (all > 0x7FFFFFFF) return GQA_ERR_SHAPE;
   const int total = static_cast<int>(all), n_work = range_workers(total, workers);
   int n = 0;
   for (int c = 0; c < n_work; ++c) {
     const int lo = range_start(total, n_work, c), hi = range_start(total, n_work, c + 1);
     int b = 0, at = 0;
-    while (at + tiles_of(b) * units <= lo) at += tiles_of(b++) * units;
+    while (at + places_of(b) <= lo) at += places_of(b++);
     KvWalk w;
-    int flat = lo;
-    for (w.start(b, lo - at, len_of(b), n_new, S_max, hi - lo); !w.done(); w.next(units, n_new, S_max, len_of), ++n) {
+    for (w.start(b, lo - at, len_of(b), n_new, S_max, lo, hi - lo); !w.done(); w.next(units, n_new, S_max, len_of), ++n) {
       if (n < max_pieces) {
-        int* o = pieces + 7 * n;
+        int* o = pieces + 8 * n;
         o[0] = c;
         o[1] = w.b;
         o[2] = w.u;
         o[3] = w.first;
         o[4] = w.n;
         o[5] = w.whole() ? -1 : partial_slot(c, w.first > 0);
-        o[6] = range_owner(total, n_work, flat - w.first + w.tiles - 1);
+        o[6] = range_owner(total, n_work, w.place(w.tiles - 1));
+        o[7] = w.tile(w.first, units);
       }
-      flat += w.n;
     }
   }
   *n_pieces = n;

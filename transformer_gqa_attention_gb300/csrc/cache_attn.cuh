@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(384, 1)
   ranges.find<1>(p, blockIdx.x, gridDim.x);
   tc_fence_after();
   const uint32_t tmem_base = *bar.tmem_holder();
-  const bool no_loads = p.fault && blockIdx.x == 0;  // test hook: CTA 0's consumers wait out and abort
+  // test hook: the last worker loads nothing, its consumers wait out and abort
+  const bool no_loads = p.fault && static_cast<int>(blockIdx.x) == ranges.workers() - 1;
 
   if (warp == 0) {
     if (lane == 0 && !no_loads) produce_k<1>(p, ranges, bar, &tmK, smem + L::kK);

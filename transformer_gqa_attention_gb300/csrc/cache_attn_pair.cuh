@@ -102,7 +102,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem_base = *bar.tmem_holder();
   const uint64_t policy = kv_policy(p);
-  const bool no_loads = p.fault && worker == 0;  // test hook: pair 0's consumers wait out and abort
+  // test hook: the last pair loads nothing, its consumers wait out and abort
+  const bool no_loads = p.fault && worker == ranges.workers() - 1;
   auto cta0 = [&](uint64_t* b) { return mapa_shared(smem_u32(b), 0); };
 
   if (warp == 0) {
@@ -161,9 +162,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     CacheTiles<1> tiles(p, ranges);
     ClearRows clear;
     int it = 0;
-    if (rank == 0 && lane == 0 && ranges.tiles(0) == 0) p.merge[worker] = make_int4(-1, 0, 0, 0);
+    if (rank == 0 && lane == 0 && tiles.l0.w.done()) p.merge[worker] = make_int4(-1, 0, 0, 0);
     tiles.each([&](auto, CacheLane& l) {
-      if (rank == 0 && lane == 0 && l.j == 0 && l.w.left == l.w.n) p.merge[worker] = goes_on(ranges, l.w, 0, worker);
+      if (rank == 0 && lane == 0 && l.j == 0 && l.w.after == 0) p.merge[worker] = goes_on(ranges, l.w, worker);
       const bool fix = clear.prepare(p, l);
       const int st = it % kStages;
       if (!__all_sync(0xffffffffu, mbar_wait(bar.v_full(st), (it / kStages) & 1, abort_flag, p.status))) return false;

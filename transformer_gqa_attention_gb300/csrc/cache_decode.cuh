@@ -64,7 +64,8 @@ __global__ void __launch_bounds__(384, 1)
   ranges.find<kWork>(p, kWork * blockIdx.x, kWork * gridDim.x);
   tc_fence_after();
   const uint32_t tmem_base = *bar.tmem_holder();
-  const bool no_loads = p.fault && blockIdx.x == 0;  // test hook: CTA 0's consumers wait out and abort
+  // test hook: the last worker's CTA loads nothing, its consumers wait out and abort
+  const bool no_loads = p.fault && static_cast<int>(blockIdx.x) == (ranges.workers() - 1) / kWork;
 
   if (warp == 0) {
     if (lane == 0 && !no_loads) produce_k<kWork>(p, ranges, bar, &tmK, smem + L::kK);
@@ -130,11 +131,15 @@ __global__ void __launch_bounds__(384, 1)
       if (lane == 0) *reinterpret_cast<float4*>(red + 4 * quarter) = make_float4(x[0], x[1], x[2], x[3]);
     };
     KvWalk w = ranges.walk(slot, p);
-    int flat = ranges.first_tile(slot);
     int items = 0, piece = 0;
     bool ok = true;
     for (; ok && !w.done(); w.next(units, p.n_new, p.S_max, [&](int b) { return __ldcg(p.kv_len + b); }), ++piece) {
       const int end = kv_end(w.len, p.n_new, p.S_max);  // (out of range: -1, no key is visible)
+      const int flat = w.tile(w.first, units);
+      int4 unit;  // of the weights kernel's tile records
+      if (r == 0)
+        unit = make_int4(w.b * units + w.u, w.first, range_owner(ranges.total(), ranges.workers(), w.place(0)),
+                         range_owner(ranges.total(), ranges.workers(), w.place(w.tiles - 1)));
       float l[4] = {0.f, 0.f, 0.f, 0.f};
       for (int j = 0; j < w.n; ++j, ++items) {
         ok = __all_sync(0xffffffffu, mbar_wait(bar.s_full(slot), items & 1, abort_flag, p.status));
@@ -143,7 +148,7 @@ __global__ void __launch_bounds__(384, 1)
         load(t_s, s);
         if ((w.first + j) * kKvTile + r >= end) s[0] = s[1] = s[2] = s[3] = -INFINITY;
         reinterpret_cast<float4*>(p.scores)[static_cast<size_t>(flat + j) * kKvTile + r] = make_float4(s[0], s[1], s[2], s[3]);
-        if (r == 0) p.tile_unit[flat + j] = make_int2(w.b * units + w.u, w.first + j);
+        if (r == 0) p.tile_unit[flat + j] = make_int4(unit.x, unit.y + j, unit.z, unit.w);
         bool over = j == 0;
         if (j > 0) {
           const float4 lim = *reinterpret_cast<const float4*>(limit);
@@ -210,11 +215,7 @@ __global__ void __launch_bounds__(384, 1)
           p.unit_ml[(w.b * units + w.u) * 4 + r] = make_float2(m, sum);
         else
           p.part_ml[ps * p.part_rows + r] = make_float2(m, sum);
-        if (r == 0 && w.first == 0) {
-          p.unit_workers[w.b * units + w.u] =
-              make_int2(worker, whole ? worker : range_owner(ranges.total(), ranges.workers(), flat + w.tiles - 1));
-          if (end < 0) atomicOr(p.status, kDevErrRange);
-        }
+        if (r == 0 && w.first == 0 && end < 0) atomicOr(p.status, kDevErrRange);
       }
       named_bar_sync(bar_id, 128);
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.h) + static_cast<size_t>(w.b) * (p.n_kv * 512) + w.u * 512 + r;
@@ -226,7 +227,6 @@ __global__ void __launch_bounds__(384, 1)
         else
           part[i * 128] = o[i];
       }
-      flat += w.n;
     }
   }
 

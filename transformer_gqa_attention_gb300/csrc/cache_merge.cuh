@@ -166,7 +166,7 @@ __device__ __forceinline__ float2 join_ml(float2 a, float2 b) {
 // The decode step with key weights: blocks 0 .. workers - 1 merge, the others add each key's
 // weight, the sum over the four heads of 2^(c s - M) / l, to the running sums, one key tile per warp
 // at a time.
-__global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnParams p, int workers) {
+__global__ void __launch_bounds__(256, 4) cache_weights_kernel(const CacheAttnParams p, int workers) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_launch_dependents();
   griddep_wait();
@@ -183,12 +183,11 @@ __global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnParam
   if (*reinterpret_cast<volatile const int*>(p.status) & kDevErrTimeout) return;
   // neighbouring warps have neighbouring tiles
   for (int i = (blockIdx.x - workers) * 8 + warp; i < total; i += n_warps) {
-    const int2 tu = __ldcg(p.tile_unit + i);
+    const int4 tu = __ldcg(p.tile_unit + i);
     float4 x[4];  // keys 32 k + lane, their four heads' scores
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       x[k] = __ldcg(reinterpret_cast<const float4*>(p.scores) + static_cast<size_t>(i) * kKvTile + 32 * k + lane);
-    const int2 cs = __ldcg(p.unit_workers + tu.x);
     float* w = p.weights + static_cast<size_t>(tu.x) * p.S_max + tu.y * kKvTile;
     bool seen[4];
     float a[4];
@@ -199,16 +198,16 @@ __global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnParam
     }
     // the heads' maxima and sums: the unit's, or of its pieces joined
     float2 m[4];
-    if (cs.x == cs.y) {
+    if (tu.z == tu.w) {
       load_ml(p.unit_ml + tu.x * 4, m);
     } else {
 #pragma unroll
       for (int h = 0; h < 4; ++h) m[h] = make_float2(-INFINITY, 0.f);
-      const int n = cs.y - cs.x + 1;
+      const int n = tu.w - tu.z + 1;
       const bool shared = n > 8;  // many pieces: the lanes share them
       for (int k = shared ? lane : 0; k < n; k += shared ? 32 : 1) {
         float2 o[4];
-        load_ml(p.part_ml + static_cast<size_t>(k ? partial_slot(cs.x + k, true) : partial_slot(cs.x, false)) * R, o);
+        load_ml(p.part_ml + static_cast<size_t>(k ? partial_slot(tu.z + k, true) : partial_slot(tu.z, false)) * R, o);
 #pragma unroll
         for (int h = 0; h < 4; ++h) m[h] = join_ml(m[h], o[h]);
       }

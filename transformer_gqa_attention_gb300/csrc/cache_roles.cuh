@@ -75,23 +75,22 @@ struct CacheBars {
   }
 };
 
-// The CTA's ranges of key tiles, in shared memory: thread i sums the tiles of sequences i per ..
-// i per + per - 1 (B <= 1024: per <= 3); a scan over the CTA gives the total and finds where the
+// The CTA's ranges of places (kv_sched.h), in shared memory: thread i sums the places of sequences i
+// per .. i per + per - 1 (B <= 1024: per <= 3); a scan over the CTA gives the total and finds where the
 // ranges start.  Called by all 384 threads.
 struct CacheRanges {
   static constexpr int kBytes = 128;
   int* scan;   // [12] per-warp sums
-  int* where;  // total, workers, then per worker: first tile, tiles, sequence, offset in it, its length
+  int* where;  // total, workers, then per worker: first place, places, sequence, offset in it, its length
 
   __device__ __forceinline__ explicit CacheRanges(uint8_t* at) : scan(reinterpret_cast<int*>(at)), where(scan + 16) {}
   __device__ __forceinline__ int total() const { return where[0]; }
   __device__ __forceinline__ int workers() const { return where[1]; }
-  __device__ __forceinline__ int first_tile(int s) const { return where[2 + 5 * s]; }
-  __device__ __forceinline__ int tiles(int s) const { return where[3 + 5 * s]; }
   __device__ __forceinline__ KvWalk walk(int s, const CacheAttnParams& p) const {
     KvWalk w;
-    w.left = where[3 + 5 * s];
-    if (w.left > 0) w.start(where[4 + 5 * s], where[5 + 5 * s], where[6 + 5 * s], p.n_new, p.S_max, w.left);
+    w.n = 0;
+    if (where[3 + 5 * s] > 0)
+      w.start(where[4 + 5 * s], where[5 + 5 * s], where[6 + 5 * s], p.n_new, p.S_max, where[2 + 5 * s], where[3 + 5 * s]);
     return w;
   }
 
@@ -102,13 +101,13 @@ struct CacheRanges {
     const int units = p.n_kv * p.row_groups;
     const int per = (p.B + 383) / 384;
     const int b0 = threadIdx.x * per;
-    int lens[3], tiles[3], mine = 0;
+    int lens[3], places[3], mine = 0;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       const bool in = i < per && b0 + i < p.B;
       lens[i] = in ? __ldcg(p.kv_len + b0 + i) : 0;
-      tiles[i] = in ? kv_tiles(kv_end(lens[i], p.n_new, p.S_max)) : 0;
-      mine += tiles[i] * units;
+      places[i] = in ? (kv_tiles(kv_end(lens[i], p.n_new, p.S_max)) + kUnitCost) * units : 0;
+      mine += places[i];
     }
     int x = mine;
 #pragma unroll
@@ -128,7 +127,7 @@ struct CacheRanges {
     if (threadIdx.x == 0) {
       where[0] = total;
       where[1] = n_work;
-      if (p.total_tiles && blockIdx.x == 0) *p.total_tiles = total;
+      if (p.total_tiles && blockIdx.x == 0) *p.total_tiles = total - kUnitCost * units * p.B;
     }
 #pragma unroll
     for (int s = 0; s < kWork; ++s) {
@@ -142,12 +141,12 @@ struct CacheRanges {
       int at = before;
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
-        if (lo >= at && lo < at + tiles[i] * units) {
+        if (lo >= at && lo < at + places[i]) {
           where[4 + 5 * s] = b0 + i;
           where[5 + 5 * s] = lo - at;
           where[6 + 5 * s] = lens[i];
         }
-        at += tiles[i] * units;
+        at += places[i];
       }
     }
     __syncthreads();
@@ -265,11 +264,10 @@ __device__ __forceinline__ int keys_all_see(const CacheAttnParams& p, int len) {
 
 // The unit of a worker's last piece as the merge wants it (CacheAttnParams::merge): whether it goes
 // on past the worker's range.
-__device__ __forceinline__ int4 goes_on(const CacheRanges& ranges, const KvWalk& w, int s, int worker) {
+__device__ __forceinline__ int4 goes_on(const CacheRanges& ranges, const KvWalk& w, int worker) {
   if (w.first + w.n == w.tiles) return make_int4(-1, 0, 0, 0);
-  const int lo = ranges.first_tile(s) + ranges.tiles(s) - w.left - w.first;  // the unit's first tile
-  return make_int4(w.b, w.u, w.first > 0 ? range_owner(ranges.total(), ranges.workers(), lo) : worker,
-                   range_owner(ranges.total(), ranges.workers(), lo + w.tiles - 1));
+  return make_int4(w.b, w.u, w.first > 0 ? range_owner(ranges.total(), ranges.workers(), w.place(0)) : worker,
+                   range_owner(ranges.total(), ranges.workers(), w.place(w.tiles - 1)));
 }
 
 // Which rows of a V tile no row of the product sees; used by a whole warp.
@@ -329,10 +327,13 @@ __device__ __forceinline__ void clear_v(const CacheAttnParams& p, const CacheRan
   const int lane = threadIdx.x & 31;
   ClearRows clear;
   int it = 0;
-  if (lane < kWork && ranges.tiles(lane) == 0) p.merge[kWork * blockIdx.x + lane] = make_int4(-1, 0, 0, 0);
+  if (lane == 0) {  // workers without a tile
+    if (tiles.l0.w.done()) p.merge[kWork * blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (kWork == 2 && tiles.l1.w.done()) p.merge[kWork * blockIdx.x + 1] = make_int4(-1, 0, 0, 0);
+  }
   tiles.each([&](auto S, CacheLane& l) {
     const int worker = kWork * blockIdx.x + S.value;
-    if (lane == 0 && l.j == 0 && l.w.left == l.w.n) p.merge[worker] = goes_on(ranges, l.w, S.value, worker);
+    if (lane == 0 && l.j == 0 && l.w.after == 0) p.merge[worker] = goes_on(ranges, l.w, worker);
     const bool fix = clear.prepare(p, l);
     // every tile is waited for and released, so that this warp stays in step with the ring
     const int st = it % kVStages;

@@ -1,13 +1,14 @@
 // kv_sched.h — how the attention over caches of per-sequence length shares its key tiles among
-// CTAs.  Host and device use the same code (the host's for tests).
+// workers.  Host and device use the same code (the host's for tests).
 //
 // A unit is (sequence b, kv head, group of query rows); it reads the ceil(end_b / 128) key tiles
-// of its sequence (at least one, so that every unit writes its rows).  The units' tiles, unit
-// after unit and sequence after sequence, form one row of `total` tiles, of which worker c of n
-// takes tiles c total / n .. (c + 1) total / n - 1: equal work whatever the lengths are, without
-// the host knowing them.  What a worker takes of one unit is a piece; a unit cut over several
-// workers is merged from its pieces' partial results.  A worker is a CTA, or one of a CTA's two
-// softmax slots.
+// of its sequence (at least one, so that every unit writes its rows).  Beginning and ending a unit
+// costs about as much as kUnitCost tiles, so each unit has that many empty places before its tiles.
+// The units' places, unit after unit and sequence after sequence, form one row of `total` places, of
+// which worker c of n takes places c total / n .. (c + 1) total / n - 1: equal work whatever the
+// lengths are, without the host knowing them.  What a worker takes of one unit's tiles is a piece; a
+// unit cut over several workers is merged from its pieces' partial results.  A worker is a CTA, a CTA
+// pair, or one of a CTA's two softmax slots.
 #pragma once
 
 #ifdef __CUDACC__
@@ -19,14 +20,19 @@
 namespace gqa {
 
 constexpr int kKvTile = 128;
+// A tile takes 0.9 to 1.5 us, the end of a unit and the start of the next about 3.  Measured with 0, 2
+// and 4: 29.7, 27.1, 26.7 us for 8 ragged sequences of up to 4000 keys and 26 drafted tokens; 29.0,
+// 25.5, 23.4 for 6 of up to 2000 and 150 tokens; 34.2, 33.9, 35.0 for the decode step of 16 of up to
+// 4096 with key weights.
+constexpr int kUnitCost = 2;
 
 // Keys that sequence b reads: its length and the n_new positions behind it; -1: out of range.
 GQA_HD int kv_end(int len, int n_new, int S_max) { return len < 0 || len > S_max - n_new ? -1 : len + n_new; }
 
 GQA_HD int kv_tiles(int end) { return end <= kKvTile ? 1 : (end + kKvTile - 1) / kKvTile; }
 
-// Workers that share the row: no more than tiles, so that every one of them has a range and a
-// unit's pieces lie with consecutive workers.
+// Workers that share the row: no more than places, so that a unit's pieces lie with consecutive
+// workers.
 GQA_HD int range_workers(int total, int most) { return total < most ? total : most; }
 
 // floor(c total / n) in 32-bit arithmetic (n <= 32768)
@@ -36,7 +42,7 @@ GQA_HD int range_start(int total, int n, int c) {
   return static_cast<int>(c * q + c * rem / static_cast<unsigned>(n));
 }
 
-// The worker whose range holds tile x: the last c with range_start(c) <= x.
+// The worker whose range holds place x: the last c with range_start(c) <= x.
 GQA_HD int range_owner(int total, int n, int x) {
   int c = static_cast<int>(static_cast<float>(x) * static_cast<float>(n) / static_cast<float>(total));  // off by 1 or so
   c = c < n - 1 ? c : n - 1;
@@ -51,34 +57,52 @@ struct KvWalk {
   int len;        // the sequence's length
   int tiles;      // key tiles of each of the sequence's units
   int first;      // the piece's first tile
-  int n;          // its tiles
-  int left;       // tiles of the range from the piece on (0: done)
+  int n;          // its tiles (0: the range has no more)
+  int after;      // places of the range behind the piece (0: this is the last piece)
+  int lo;         // the unit's first place
 
-  // offset: tiles of sequence b before the range's start
-  GQA_HD void start(int b_, int offset, int len_, int n_new, int S_max, int range) {
+  // A range of `count` places from place `begin` on, which is `offset` places into sequence b.
+  GQA_HD void start(int b_, int offset, int len_, int n_new, int S_max, int begin, int count) {
     b = b_;
     len = len_;
     tiles = kv_tiles(kv_end(len, n_new, S_max));
-    u = offset / tiles;
-    first = offset - u * tiles;
-    left = range;
-    n = tiles - first < left ? tiles - first : left;
+    u = offset / (tiles + kUnitCost);
+    const int pos = offset - u * (tiles + kUnitCost);
+    lo = begin - pos;
+    first = pos > kUnitCost ? pos - kUnitCost : 0;
+    const int mine = min_(tiles + kUnitCost - pos, count);
+    n = pos + mine - kUnitCost - first;
+    if (n < 0) n = 0;
+    after = rest_(count - mine);
+    // (a range that ends inside the empty places has no tile of this unit, and none behind it)
   }
-  GQA_HD bool done() const { return left <= 0; }
+  GQA_HD bool done() const { return n == 0; }
   GQA_HD bool whole() const { return n == tiles; }
   // units of a sequence; len_of(b): its length
   template <typename F>
   GQA_HD void next(int units, int n_new, int S_max, F len_of) {
-    left -= n;
-    if (left <= 0) return;
+    n = 0;
+    if (after == 0) return;
     first = 0;
+    lo += tiles + kUnitCost;
     if (++u == units) {
       u = 0;
       len = len_of(++b);
       tiles = kv_tiles(kv_end(len, n_new, S_max));
     }
-    n = tiles < left ? tiles : left;
+    const int mine = min_(tiles + kUnitCost, after);
+    n = mine - kUnitCost;
+    after = rest_(after - mine);
   }
+  // place of the unit's tile t
+  GQA_HD int place(int t) const { return lo + kUnitCost + t; }
+  // number of the unit's tile t among all tiles
+  GQA_HD int tile(int t, int units) const { return lo - kUnitCost * (b * units + u) + t; }
+
+ private:
+  GQA_HD static int min_(int x, int y) { return x < y ? x : y; }
+  // what is left of a range, if it reaches a tile of the next unit
+  GQA_HD static int rest_(int x) { return x > kUnitCost ? x : 0; }
 };
 
 // Slots of partial results: a worker has at most two pieces that are not whole units, the one its

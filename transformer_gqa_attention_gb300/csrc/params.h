@@ -102,7 +102,7 @@ struct CacheAttnParams {
   void* h;                 // [B, T, 512 n_kv] bf16
   float* weights;          // [B, n_kv, S_max] accumulated key weights (T = 1), or null
   int* status;
-  int fault;               // test hook: CTA 0 issues no loads (its waits run out)
+  int fault;               // test hook: the last worker issues no loads (its waits run out)
   float scale_log2;        // log2(e) / sqrt(128)
   // rows: a kv head's T positions in row_groups groups of group_pos (kOneTilePos, or 64 on two tiles)
   int row_groups, group_pos;
@@ -113,11 +113,10 @@ struct CacheAttnParams {
   float* part_o;
   float2* part_ml;
   int part_rows;
-  // with weights: scores [tile][128 keys][4 heads], each tile's (unit, index in it), each unit's
-  // (first, last worker) and, for whole units, each head's (maximum, sum)
+  // with weights: scores [tile][128 keys][4 heads], each tile's (unit, index in it, the unit's first
+  // and last worker) and, for whole units, each head's (maximum, sum)
   float* scores;
-  int2* tile_unit;
-  int2* unit_workers;
+  int4* tile_unit;
   float2* unit_ml;
   int* total_tiles;
 };
