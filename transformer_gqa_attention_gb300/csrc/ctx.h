@@ -135,6 +135,7 @@ inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // uses is kept until the context is destroyed, not freed, when the buffer outgrows it: the graph
 // holds its address.
 inline gqa_status ensure_buffer(gqa_ctx* c, DeviceBuffer& buf, size_t bytes, cudaStream_t s) {
+  if (bytes <= buf.bytes && buf.captured) return GQA_OK;
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) {  // the legacy stream beside another capture
     cudaGetLastError();

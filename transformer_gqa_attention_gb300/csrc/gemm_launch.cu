@@ -22,6 +22,15 @@ cudaError_t configure_gemm_kernels() {
   e = cudaFuncSetAttribute(gemm_tc_pair_kernel<6, kQkvRope>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            PairSmem::kBytes);
   if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(gemm_tc_pair_kernel<6, kQkvRopeSeq>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           PairSmem::kBytes);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(gemm_splitk_cluster_kernel<kSplitKQkvSeq, kSkinnyStages, 64>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, SkinnySmem::kBytes);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(gemm_splitk_cluster_kernel<kSplitKQkvSeq, kNarrowStages, 32>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, NarrowSmem::kBytes);
+  if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(gemm_tc_pair_kernel<6, kStoreF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            PairSmem::kBytes);
   if (e != cudaSuccess) return e;
@@ -53,6 +62,8 @@ int gemm_pair_max_clusters() {
 
 cudaError_t launch_gemm_qkv_rope(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& bt,
                                  const GemmParams& p, int grid, cudaStream_t s) {
+  if (p.seq_start)
+    return launch_pdl(gemm_tc_pair_kernel<6, kQkvRopeSeq>, dim3(grid), dim3(192), PairSmem::kBytes, s, 0, a, b, bt, p);
   return launch_pdl(gemm_tc_pair_kernel<6, kQkvRope>, dim3(grid), dim3(192), PairSmem::kBytes, s, 0, a, b, bt, p);
 }
 
@@ -75,7 +86,7 @@ static cudaError_t launch_splitk(const CUtensorMap& a, const CUtensorMap& b, con
     return launch_pdl(gemm_splitk_cluster_kernel<EPI, kNarrowStages, 32>, grid, dim3(192), NarrowSmem::kBytes, s,
                       p.splits, a, b, p);
   }
-  if constexpr (EPI == kSplitKQkv) {
+  if constexpr (EPI != kSplitKOut) {
     if (!splitk_fits<64, kSkinnyStages>(p.splits)) return cudaErrorInvalidValue;
     return launch_pdl(gemm_splitk_cluster_kernel<EPI, kSkinnyStages, 64>, grid, dim3(192), SkinnySmem::kBytes, s,
                       p.splits, a, b, p);
@@ -90,7 +101,7 @@ int splitk_token_tile(int n_tok) { return n_tok <= 32 ? 32 : 64; }
 
 cudaError_t launch_gemm_splitk_qkv(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
                                    cudaStream_t s) {
-  return launch_splitk<kSplitKQkv>(a, b, p, s);
+  return p.seq_start ? launch_splitk<kSplitKQkvSeq>(a, b, p, s) : launch_splitk<kSplitKQkv>(a, b, p, s);
 }
 
 cudaError_t launch_gemm_splitk_out(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,

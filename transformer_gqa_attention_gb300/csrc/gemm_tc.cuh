@@ -27,6 +27,8 @@
 //               position start_pos + t.
 //   kStoreF32 — Delta = H W_O^T (step 14) stored fp32 row-major.
 //   kSplitKQkv / kSplitKOut — the same two epilogues for the few-token kernel.
+//   kQkvRopeSeq / kSplitKQkvSeq — kQkvRope / kSplitKQkv where every sequence has its own start in the
+//               cache (GemmParams::seq_start) and R has a row per token.
 #pragma once
 
 #include "pair_sched.h"
@@ -70,7 +72,6 @@ __device__ __forceinline__ void stage_chunk(float* stage, int lane, const uint32
 // 8k + lane/4 of the warp's 32 rows, columns 8 (lane & 3) .. +7 of the chunk.
 struct QkvRows {
   int m[4], b[4], t[4];
-  int pos[4];   // cache position of the row (-1: not written)
   float rs[4];  // row scale (1 / rms of the token row under attention_norm; 1 for the block alone)
 };
 
@@ -82,11 +83,6 @@ __device__ __forceinline__ QkvRows qkv_rows(const GemmParams& p, int lane, int m
     const int mc = min(q.m[k], p.M - 1);
     q.b[k] = mc / p.T;
     q.t[k] = mc - q.b[k] * p.T;
-    q.pos[k] = p.start_pos + q.t[k];
-    if (p.seq_start) {
-      q.pos[k] = q.t[k];  // offset from the sequence's start, added by qkv_row_starts
-      q.t[k] = mc;        // R has a row per token
-    }
     q.rs[k] = 1.f;
   }
   return q;
@@ -100,34 +96,34 @@ __device__ __forceinline__ void qkv_row_scales(const GemmParams& p, QkvRows& q) 
   for (int k = 0; k < 4; ++k) q.rs[k] = __ldg(p.row_scale + min(q.m[k], p.M - 1));
 }
 
-// The rows' cache positions where every sequence has its own start.  The starts may come from the
-// previous kernel: read, like the row scales, after the accumulator wait.
-__device__ __forceinline__ void qkv_row_starts(const GemmParams& p, QkvRows& q) {
-  if (!p.seq_start) return;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int start = __ldcg(p.seq_start + q.b[k]);
-    q.pos[k] = start >= 0 && start <= p.S_max - p.T ? start + q.pos[k] : -1;
-  }
+// Cache position of position t of sequence b, or -1: a sequence whose p.T positions do not fit the
+// cache is not written.  The starts may come from the previous kernel: read, like the row scales,
+// after the accumulator wait (or behind the reduction, which follows it).
+__device__ __forceinline__ int seq_position(const GemmParams& p, int b, int t) {
+  const int start = __ldcg(p.seq_start + b);
+  return start >= 0 && start <= p.S_max - p.T ? start + t : -1;
 }
 
 // (cos, sin) of the 4 RoPE pairs a lane rotates in chunk-column block cc (0..3) of a head
 // slice: pairs 16 cc + 4 (lane & 3) .. +3 of each of its 4 rows.
+template <bool kSeq>
 __device__ __forceinline__ void load_rope(const GemmParams& p, const QkvRows& q, int lane, int cc,
                                           float4 (&cs)[4][2]) {
   const int j0 = 16 * cc + 4 * (lane & 3);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float4* rp = reinterpret_cast<const float4*>(p.R + (static_cast<size_t>(q.t[k]) * 64 + j0) * 2);
+    const float4* rp = reinterpret_cast<const float4*>(
+        p.R + (static_cast<size_t>(kSeq ? min(q.m[k], p.M - 1) : q.t[k]) * 64 + j0) * 2);
     cs[k][0] = __ldg(rp);
     cs[k][1] = __ldg(rp + 1);
   }
 }
 
 // Q/K/V epilogue of one staged chunk (columns col0 .. col0+31, all of one of Q, K, V: the
-// boundaries are multiples of 128).
+// boundaries are multiples of 128).  kSeq: pos[k] is the row's cache position, -1 where it is not written.
+template <bool kSeq>
 __device__ __forceinline__ void store_qkv_chunk(const GemmParams& p, const float* stage, int lane, const QkvRows& q,
-                                                int col0, const float4 (&cs)[4][2]) {
+                                                int col0, const float4 (&cs)[4][2], const int (&pos)[4]) {
   const int cq = lane & 3;
   const int col = col0 + 8 * cq;
   const int k_col0 = p.q_cols;              // first key column
@@ -157,8 +153,8 @@ __device__ __forceinline__ void store_qkv_chunk(const GemmParams& p, const float
     if (col0 < k_col0) {
       dst = static_cast<__nv_bfloat16*>(p.out0) + static_cast<size_t>(q.m[k]) * p.q_cols + col;
     } else {
-      if (q.pos[k] < 0) continue;
-      const size_t cache_row = static_cast<size_t>(q.b[k]) * p.S_max + q.pos[k];
+      if (kSeq && pos[k] < 0) continue;
+      const size_t cache_row = static_cast<size_t>(q.b[k]) * p.S_max + (kSeq ? pos[k] : p.start_pos + q.t[k]);
       dst = static_cast<__nv_bfloat16*>(is_v ? p.out2 : p.out1) + cache_row * p.kv_cols + (col - (is_v ? v_col0 : k_col0));
     }
     *reinterpret_cast<uint4*>(dst) = w;
@@ -386,17 +382,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       // ((n0 / 32) + cp) mod 4 of a head slice.  Q/K items read all their rotation
       // coefficients before waiting for the accumulator, so the latency hides under the main
       // loop (an item may mix key and value chunks: each chunk picks its own store).
-      const bool rope = EPI == kQkvRope && n0 < p.q_cols + p.kv_cols;
+      constexpr bool kQkv = EPI == kQkvRope || EPI == kQkvRopeSeq, kSeq = EPI == kQkvRopeSeq;
+      const bool rope = kQkv && n0 < p.q_cols + p.kv_cols;
       QkvRows qr{};
+      int pos[4] = {0, 0, 0, 0};
       float4 cs[4][4][2];
       // Delta items with a residual: the residual of chunk pair cp + 1 is read while pair cp
       // is stored (pair 0 before the accumulator wait)
       uint2 rva[8], rvb[8], rva_n[8], rvb_n[8];
-      if constexpr (EPI == kQkvRope) {
+      if constexpr (kQkv) {
         qr = qkv_rows(p, lane, m_base);
         if (rope) {
 #pragma unroll
-          for (int cp = 0; cp < 4; ++cp) load_rope(p, qr, lane, ((n0 >> 5) + cp) & 3, cs[cp]);
+          for (int cp = 0; cp < 4; ++cp) load_rope<kSeq>(p, qr, lane, ((n0 >> 5) + cp) & 3, cs[cp]);
         }
       } else {
         if (p.residual) {
@@ -407,9 +405,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[ab], (lt >> 1) & 1, abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
-      if constexpr (EPI == kQkvRope) {
-        qkv_row_scales(p, qr);
-        qkv_row_starts(p, qr);
+      if constexpr (kQkv) qkv_row_scales(p, qr);
+      if constexpr (kSeq) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) pos[k] = seq_position(p, qr.b[k], qr.t[k]);
       }
       const uint32_t t_row = tmem_base + lane_off + ab * 256;
 #pragma unroll
@@ -428,8 +427,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
         tmem_ld_wait();
         stage_chunk(stage, lane, va);
         __syncwarp();
-        if constexpr (EPI == kQkvRope) {
-          store_qkv_chunk(p, stage, lane, qr, n0 + cp * 32, cs[cp]);
+        if constexpr (kQkv) {
+          store_qkv_chunk<kSeq>(p, stage, lane, qr, n0 + cp * 32, cs[cp], pos);
         } else {
           store_f32_chunk(p, stage, lane, m_base, n0 + cp * 32, rva);
         }
@@ -437,8 +436,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
         if (has_b) {
           stage_chunk(stage, lane, vb);
           __syncwarp();
-          if constexpr (EPI == kQkvRope) {
-            store_qkv_chunk(p, stage, lane, qr, n0 + (cp + 4) * 32, cs[cp]);
+          if constexpr (kQkv) {
+            store_qkv_chunk<kSeq>(p, stage, lane, qr, n0 + (cp + 4) * 32, cs[cp], pos);
           } else {
             store_f32_chunk(p, stage, lane, m_base, n0 + (cp + 4) * 32, rvb);
           }
@@ -608,7 +607,7 @@ __global__ void __launch_bounds__(192, (STAGES <= 5 ? 2 : 1))
   } else {
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    if constexpr (EPI == kSplitKQkv) {
+    if constexpr (EPI == kSplitKQkv || EPI == kSplitKQkvSeq) {
       const int m = m0 + 4 * lane;  // pairs (m & 127) / 2 and the next one
       const bool rope = m < p.q_cols + p.kv_cols;
 #pragma unroll
@@ -616,7 +615,7 @@ __global__ void __launch_bounds__(192, (STAGES <= 5 ? 2 : 1))
         const int tok = t_lo + (warp - 2) + 4 * j;
         cs[j] = make_float4(1.f, 0.f, 1.f, 0.f);  // value features: not rotated
         if (rope && tok < t_hi) {
-          const int t = p.seq_start ? tok : tok - (tok / p.T) * p.T;
+          const int t = EPI == kSplitKQkvSeq ? tok : tok - (tok / p.T) * p.T;
           cs[j] = __ldg(reinterpret_cast<const float4*>(p.R + (static_cast<size_t>(t) * 64 + ((m & 127) >> 1)) * 2));
         }
       }
@@ -712,9 +711,12 @@ __global__ void __launch_bounds__(192, (STAGES <= 5 ? 2 : 1))
         } else {
           const int v_col0 = p.q_cols + p.kv_cols;
           const bool is_v = m >= v_col0;
-          const int start = p.seq_start ? __ldcg(p.seq_start + b) : p.start_pos;
-          if (start < 0 || start > p.S_max - p.T) continue;  // only a sequence's own start can be
-          const size_t crow = static_cast<size_t>(b) * p.S_max + start + t;
+          int pos = p.start_pos + t;
+          if constexpr (EPI == kSplitKQkvSeq) {
+            pos = seq_position(p, b, t);
+            if (pos < 0) continue;
+          }
+          const size_t crow = static_cast<size_t>(b) * p.S_max + pos;
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(is_v ? p.fin2 : p.fin1) + crow * p.kv_cols +
                                     (m - (is_v ? v_col0 : p.q_cols))) = o;
         }

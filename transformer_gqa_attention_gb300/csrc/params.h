@@ -17,8 +17,9 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr uint64_t kDrainLimitNs = 200000000ull;  // 0.2 s while draining after an abort
 
 // kQkvRope / kStoreF32: many-token epilogues.  kSplitKQkv / kSplitKOut: the same two
-// epilogues after the cluster-wide split-K reduction of the few-token kernel.
-enum EpiMode : int { kQkvRope = 0, kStoreF32 = 1, kSplitKQkv = 3, kSplitKOut = 4 };
+// epilogues after the cluster-wide split-K reduction of the few-token kernel.  kQkvRopeSeq /
+// kSplitKQkvSeq: the Q/K/V ones with a start of its own for every sequence.
+enum EpiMode : int { kQkvRope = 0, kStoreF32 = 1, kSplitKQkv = 3, kSplitKOut = 4, kQkvRopeSeq = 5, kSplitKQkvSeq = 6 };
 
 struct GemmParams {
   int M, N;          // rows of A, rows of B
