@@ -64,7 +64,7 @@ cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t s) {
 
 // ------------------------------------------------------------------------------ eviction
 constexpr int kSelThreads = 512;
-constexpr int kSelEach = 8;                          // positions per thread of a staged chunk
+constexpr int kSelEach = 12;                         // positions per thread of a staged chunk (a multiple of 4)
 constexpr int kSelChunk = kSelThreads * kSelEach;
 constexpr int kSelBins = 2048;
 constexpr int kSelMaxCluster = 8;
@@ -191,27 +191,29 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     }
   }
   const uint32_t above = prefix | ~mask;
-  // flags of the thread's positions of a staged chunk: bits 0..7 kept for sure, 8..15 equal
+  // flags of the thread's positions of a staged chunk: bits 0..15 kept for sure, 16..31 equal
   auto flags = [&](int s0) {
     uint32_t f = 0;
-    const float4 x0 = *reinterpret_cast<const float4*>(stage + tid * kSelEach);
-    const float4 x1 = *reinterpret_cast<const float4*>(stage + tid * kSelEach + 4);
-    const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-    for (int k = 0; k < kSelEach; ++k) {
-      const int s = s0 + tid * kSelEach + k;
-      if (s < hi) {
-        const uint32_t u = weight_rank(x[k]);
-        const bool edge = s < mid0 || s >= mid1;
-        if (edge || u > above)
-          f |= 1u << k;
-        else if ((u & mask) == prefix)
-          f |= 256u << k;
+    for (int q = 0; q < kSelEach; q += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(stage + tid * kSelEach + q);
+      const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int s = s0 + tid * kSelEach + q + k;
+        if (s < hi) {
+          const uint32_t u = weight_rank(x[k]);
+          const bool edge = s < mid0 || s >= mid1;
+          if (edge || u > above)
+            f |= 1u << (q + k);
+          else if ((u & mask) == prefix)
+            f |= 0x10000u << (q + k);
+        }
       }
     }
     return f;
   };
-  auto packed = [](uint32_t f) { return (__popc(f & 255u) << 16) | __popc(f >> 8); };  // at most 4096 each
+  auto packed = [](uint32_t f) { return (__popc(f & 0xFFFFu) << 16) | __popc(f >> 16); };  // at most kSelChunk each
   // this slice's totals, then those of the CTAs before it
   int sure = 0, equal = 0;
   uint32_t f = 0;
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     int gt = base_sure + (before >> 16), eq = base_equal + (before & 0xFFFF);
 #pragma unroll
     for (int k = 0; k < kSelEach; ++k) {
-      const bool is_gt = (f >> k) & 1u, is_eq = (f >> (8 + k)) & 1u;
+      const bool is_gt = (f >> k) & 1u, is_eq = (f >> (16 + k)) & 1u;
       if (is_gt || (is_eq && eq < rem)) kept[gt + min(eq, rem)] = s0 + tid * kSelEach + k;
       gt += is_gt;
       eq += is_eq;
@@ -337,9 +339,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 }
 
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s) {
-  // CTAs per (sequence, kv head): about 512 in all
-  const long long units = static_cast<long long>(p.B) * p.n_kv;
-  const int c = units <= 64 ? 8 : units <= 128 ? 4 : units <= 256 ? 2 : 1;
+  // As few CTAs per (sequence, kv head) as hold its positions in their shared memory (up to eight),
+  // since every exchange between them costs more than it saves below that.  Measured with 1, 2, 4, 8
+  // CTAs (whole eviction, us): one sequence of 4100 positions 8.8, 10.8, 12.0, 15.3; of 16384 33.4, 25.9,
+  // 16.2, 18.7; of 32768 83, 53, 40, 28; 16 sequences of 4096 49, 53, 67, 118.
+  int c = 1;
+  while (c < kSelMaxCluster && (p.S_max + c - 1) / c > kSelChunk) c *= 2;
   return launch_pdl(evict_select_kernel, dim3(c, p.n_kv, p.B), dim3(kSelThreads), 0, s, c > 1 ? c : 0, p);
 }
 

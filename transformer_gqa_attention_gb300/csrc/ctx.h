@@ -211,9 +211,16 @@ struct ProfScope {
         cudaEvent_t a, b;
         if (cudaEventCreate(&a) != cudaSuccess) return;
         if (cudaEventCreate(&b) != cudaSuccess) { cudaEventDestroy(a); return; }
+        try {
+          c->ev.reserve(c->ev.size() + 2);
+          c->ev_kind.push_back(kind);
+        } catch (...) {  // this launch goes unrecorded
+          cudaEventDestroy(a);
+          cudaEventDestroy(b);
+          return;
+        }
         c->ev.push_back(a);
         c->ev.push_back(b);
-        c->ev_kind.push_back(kind);
       }
       c->ev_kind[c->ev_used] = kind;
       on = cudaEventRecord(c->ev[2 * c->ev_used], s) == cudaSuccess;

@@ -244,7 +244,7 @@ const char* attn_strerror(gqa_status st) {
   switch (st) {
     case GQA_OK: return "ok";
     case GQA_ERR_INVALID_ARG: return "invalid argument (null pointer, null context or bad flag)";
-    case GQA_ERR_SHAPE: return "shape out of range (B, T, S_max or start_pos)";
+    case GQA_ERR_SHAPE: return "shape out of range (B, T, S_max, start_pos or a length read on the device)";
     case GQA_ERR_ALIGN: return "device pointer not 16-byte aligned";
     case GQA_ERR_CUDA: return "CUDA runtime error (see attn_last_cuda_error)";
     case GQA_ERR_TIMEOUT: return "a bounded device-side wait timed out";
