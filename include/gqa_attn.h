@@ -332,7 +332,7 @@ gqa_status attn_decode_weights_residual(gqa_ctx *ctx, const void *x, int B, cons
  * kept    [B,n_kv,budget] int32 output: the position that each kept one had; -1 past the new
  *         length.
  * new_len [B] int32 output: min(kv_len[b], budget); may be the array kv_len itself, but not
- *         overlap it otherwise.
+ *         overlap it otherwise.  No output may overlap another.
  * Requires 1 <= budget <= S_out, n_first, n_recent >= 0, n_first + n_recent <= budget, and the
  * limits of attn_decode_attention_weights.  A kv_len outside 0 .. S_max: the sequence's caches
  * and weights stay as they are, its kept is -1, its new_len 0, and attn_sync_status reports

@@ -446,6 +446,34 @@ def test_evict_refuses_partial_overlaps():
     abi.attn_sync_status(ctx)
 
 
+def test_outputs_that_overlap_each_other_are_refused():
+    ctx = context()
+    part = 64 * 8 * 128
+    pool = torch.zeros(6 * part, dtype=torch.bfloat16, device=DEV)
+    k, v, a, c = (pool[i * part:(i + 1) * part] for i in range(4))
+    w, ow = torch.zeros(8, 64, device=DEV), torch.zeros(8, 64, device=DEV)
+    lens, kept, new = ints([64]), torch.zeros(8 * 16, dtype=torch.int32, device=DEV), ints([0])
+    good = dict(ck=k, cv=v, ok=a, ov=c, ow=ow, kept=kept, new=new, S_out=64)
+
+    def evict(**kw):
+        d = {**good, **kw}
+        abi.attn_cache_evict(ctx, d["ck"], d["cv"], w, 1, 64, lens, 16, 0, 0, d["ok"], d["ov"], d["ow"], d["S_out"],
+                             d["kept"], d["new"])
+
+    for bad in (dict(ov=a), dict(ov=pool[2 * part + 128:]), dict(new=kept), dict(kept=ow), dict(kept=w.view(torch.int32)),
+                dict(new=ow.view(torch.int32)), dict(ck=k, cv=k, ok=k, ov=k, ow=w), dict(kept=a.view(torch.int32)),
+                dict(ok=k, ov=v, ow=w, kept=lens)):
+        with pytest.raises(abi.GQAError) as err:
+            evict(**bad)
+        assert err.value.status == 1, bad.keys()
+    evict()
+    evict(new=lens)
+    with pytest.raises(abi.GQAError) as err:  # K and V of a commit lie apart
+        abi.attn_cache_commit(ctx, k, k, 1, 64, 4, ints([8]), ints([0, 1, 2, 3]), ints([4]), new)
+    assert err.value.status == 1
+    abi.attn_sync_status(ctx)
+
+
 # ------------------------------------------------------------------------------- failure path
 @pytest.mark.parametrize("weights", [False, True])
 def test_a_wait_that_runs_out_is_reported(weights):

@@ -171,6 +171,8 @@ gqa_status attn_cache_commit(gqa_ctx* c, void* cache_k, void* cache_v, int B, in
     return GQA_ERR_INVALID_ARG;
   gqa_status st = check_device(c);
   if (st != GQA_OK) return st;
+  const size_t bytes = static_cast<size_t>(B) * S_max * c->n_kv * 256;
+  if (overlap(cache_k, bytes, cache_v, bytes)) return GQA_ERR_INVALID_ARG;
   CallRange range("gqa.attn_cache_commit");
   CommitParams p{};
   p.B = B;
@@ -213,11 +215,20 @@ gqa_status attn_cache_evict(gqa_ctx* c, const void* cache_k, const void* cache_v
   if (new_len != kv_len && overlap(new_len, lens, kv_len, lens)) return GQA_ERR_INVALID_ARG;
   gqa_status st = check_device(c);
   if (st != GQA_OK) return st;
-  const size_t unit = static_cast<size_t>(B) * c->n_kv;  // (sequence, kv head) pairs
-  const size_t per_pos[3] = {256, 256, 4};               // bytes of one of their positions
-  for (int i = 0; i < 3 && !in_place; ++i)
-    for (int j = 0; j < 3; ++j)
-      if (overlap(ins[i], unit * S_max * per_pos[i], outs[j], unit * S_out * per_pos[j])) return GQA_ERR_INVALID_ARG;
+  // no output overlaps another, nor an input other than its own (in place; new_len: kv_len)
+  const size_t unit = static_cast<size_t>(B) * c->n_kv;  // (sequence, kv head) pairs; 256 bytes of K per position
+  const size_t in_bytes[4] = {unit * S_max * 256, unit * S_max * 256, unit * S_max * 4, lens};
+  const size_t out_bytes[5] = {unit * S_out * 256, unit * S_out * 256, unit * S_out * 4, lens, unit * budget * 4};
+  const void* all_ins[4] = {cache_k, cache_v, weights, kv_len};
+  const void* all_outs[5] = {out_k, out_v, out_weights, new_len, kept};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(all_outs[i], out_bytes[i], all_outs[j], out_bytes[j])) return GQA_ERR_INVALID_ARG;
+    for (int j = 0; j < 4; ++j) {
+      const bool own = i == j && all_outs[i] == all_ins[j] && (i == 3 || in_place);
+      if (!own && overlap(all_outs[i], out_bytes[i], all_ins[j], in_bytes[j])) return GQA_ERR_INVALID_ARG;
+    }
+  }
   CallRange range("gqa.attn_cache_evict");
   EvictParams p{};
   p.B = B;

@@ -108,8 +108,8 @@ struct CacheAttnParams {
   // rows: a kv head's T positions in row_groups groups of group_pos (kOneTilePos, or 64 on two tiles)
   int row_groups, group_pos;
   // scratch: per worker the unit that goes on past its range (sequence or -1, unit, the unit's first
-  // and last worker), the partial results of cut units ([2 workers][32 float4 columns][part_rows], or with at most
-  // kFewPos positions [2 workers][part_rows][128]) and their (maximum, sum)
+  // and last worker), the partial results of cut units ([2 workers][32 float4 columns][part_rows], with
+  // weights [2 workers][part_rows][128]) and their (maximum, sum)
   int4* merge;
   float* part_o;
   float2* part_ml;
