@@ -3,7 +3,12 @@
 //
 // The four query heads of a kv head read the same keys and values, so the tensor core's 128 rows
 // are 32 positions x 4 heads: row 4t + h.  Every K/V byte then serves all rows of up to 32
-// positions: 4 T rows do 4 T x 128 x 4 FLOP per key of 512 bytes.
+// positions: 4 T rows do 4 T x 128 x 4 FLOP per key of 512 bytes, far below what the tensor cores could
+// do, so reading the keys and values bounds it: 32 sequences of 4000 keys (528 MB) take 88 us with 8
+// tokens (6.0 TB/s) and 95 with 32, with the merge; 8 ragged ones of up to 4000 keys and 26 tokens (73 MB)
+// 26, of which the merge is 4 and a CTA's first tile 5; one of 300 keys and 8 tokens 10.8, all latency.
+// Keys on the tensor core's rows, as the decode step has them (cache_decode.cuh): 106 us for 8 tokens
+// where this takes 87.
 //   S = Q K^T into TMEM, softmax, P over S in TMEM, O += P V.
 // S alternates between two buffers from tile to tile, queries and O from unit to unit, so that the end
 // of one unit (last PV, normalisation, stores) passes under the next one's first tiles.
@@ -25,6 +30,24 @@ struct CacheAttnSmem {
   static constexpr int kExchange = kRanges + CacheRanges::kBytes;  // [2 halves][128 rows] floats
   static constexpr int kBytes = kExchange + 2 * 128 * 4 + 1024;
 };
+
+// Groups of eight lanes with eight pieces each: lane j gets piece j of every lane, x[k] from lane k.
+__device__ __forceinline__ void transpose8(uint4 (&x)[8]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k & d) continue;
+      const uint4 give = up ? x[k] : x[k + d];
+      const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, d), __shfl_xor_sync(0xffffffffu, give.y, d),
+                                   __shfl_xor_sync(0xffffffffu, give.z, d), __shfl_xor_sync(0xffffffffu, give.w, d));
+      x[k] = up ? got : x[k];
+      x[k + d] = up ? x[k + d] : got;
+    }
+  }
+}
 
 // The softmax warps of a row tile (warps 4..11), whose rows are positions t0 + 32 tile .. + 31 of a
 // unit.  Two threads share a row: warps 4..7 take keys 0..63 of a key tile, warps 8..11 keys 64..127
@@ -56,21 +79,26 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
     const int g = w.u / p.row_groups;
     const int t0 = (w.u - g * p.row_groups) * p.group_pos + 32 * tile;
     const bool warp_live = t0 + quarter * 8 < p.T;
-    const uint32_t t_o = t_row + 256 + 128 * (piece & 1) + 64 * half;  // this half's columns of O
+    const uint32_t t_o = t_row + 128 * (Bars::kS + piece % Bars::kO) + 64 * half;  // this half's columns of O
     float m_used = -INFINITY, l_sum = 0.f;
+    uint32_t sv[64];
+    bool loading = false;  // the tile's S is on its way
+    auto load_s = [&](int slot) {
+      tc_fence_after();
+      const uint32_t at = t_row + slot * 128 + 64 * half;
+      tmem_ld32(at, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+      tmem_ld32(at + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+    };
     for (int j = 0; j < w.n; ++j, ++it) {
-      const int slot = it & 1;
+      const int slot = it % Bars::kS;
       const uint32_t t_s = t_row + slot * 128;
-      ok = __all_sync(0xffffffffu, wait(bar.s_full(slot), (it >> 1) & 1));
+      if (!loading) ok = __all_sync(0xffffffffu, wait(bar.s_full(slot), (it / Bars::kS) & 1));
       if (!warp_live) {  // rows past the last position: whatever their P is, their O is not used
         if (!ok) break;
         if (lane == 0) arrive_p(slot, half);
         continue;
       }
-      tc_fence_after();
-      uint32_t sv[64];
-      tmem_ld32(t_s + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-      tmem_ld32(t_s + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+      if (!loading) load_s(slot);
       tmem_ld_wait();
       const int key0 = (w.first + j) * kKvTile + 64 * half;
       if (key0 + 64 > safe) {
@@ -143,6 +171,11 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
         }
         tmem_st16(t_s + 32 * half + c * 16, pw);
       }
+      // the next tile's S, if it is there, comes in under the rest of this one
+      const int s_next = (it + 1) % Bars::kS;
+      loading = j + 1 < w.n &&
+                __all_sync(0xffffffffu, mbar_test_wait(bar.s_full(s_next), ((it + 1) / Bars::kS) & 1));
+      if (loading) load_s(s_next);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -151,15 +184,14 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
       l_sum += l2.x + l2.y;
     }
     // ---------------------------------------------------------------- end of a piece
-    const int at = piece & 1;
-    if (ok) ok = __all_sync(0xffffffffu, wait(bar.o_full(at), (piece >> 1) & 1));
-    else break;  // both warps of the row group left the tiles at the same place
+    const int at = piece % Bars::kO;
+    // one decision of the row group's warps, with or without live rows, whether a wait was given up
+    ok = ok && __all_sync(0xffffffffu, wait(bar.o_full(at), (piece / Bars::kO) & 1));
+    if (!(ok = named_bar_and(bar_id, 64, ok))) break;
     if (!warp_live) {
-      if (!ok) break;
       if (lane == 0) arrive_o(at);
       continue;
     }
-    if (!(ok = named_bar_and(bar_id, 64, ok))) break;
     tc_fence_after();
     uint32_t v[64];
     tmem_ld32(t_o, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
@@ -173,32 +205,38 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
     const float l_other = *other;
     const float l = half ? l_other + l_sum : l_sum + l_other;
     named_bar_sync(bar_id, 64);  // read before the next exchange
-    const int t = t0 + (r >> 2);
-    if (t < p.T) {
-      if (w.whole()) {
-        // no visible key: zeros; a length out of range: NaN
-        const float inv = end < 0 ? __int_as_float(0x7FC00000) : (l == 0.f ? 0.f : 1.f / l);
-        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.h) +
-                                              (static_cast<size_t>(w.b) * p.T + t) * (p.n_kv * 512) +
-                                              (g * 4 + (r & 3)) * 128 + 64 * half);
+    if (w.whole()) {
+      // no visible key: zeros; a length out of range: NaN
+      const float inv = end < 0 ? __int_as_float(0x7FC00000) : (l == 0.f ? 0.f : 1.f / l);
+      uint4 o[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          out[k] = make_uint4(pack_bf16x2(__uint_as_float(v[8 * k + 0]) * inv, __uint_as_float(v[8 * k + 1]) * inv),
-                              pack_bf16x2(__uint_as_float(v[8 * k + 2]) * inv, __uint_as_float(v[8 * k + 3]) * inv),
-                              pack_bf16x2(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv),
-                              pack_bf16x2(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv));
-      } else {
-        const int row = 128 * tile + r;
-        const size_t ps = partial_slot(worker, w.first > 0);
-        float4* part = reinterpret_cast<float4*>(p.part_o) + (ps * 32 + 16 * half) * p.part_rows + row;
+      for (int k = 0; k < 8; ++k)
+        o[k] = make_uint4(pack_bf16x2(__uint_as_float(v[8 * k + 0]) * inv, __uint_as_float(v[8 * k + 1]) * inv),
+                          pack_bf16x2(__uint_as_float(v[8 * k + 2]) * inv, __uint_as_float(v[8 * k + 3]) * inv),
+                          pack_bf16x2(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv),
+                          pack_bf16x2(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv));
+      // A lane has 128 bytes of its row; eight lanes exchange theirs, so that they store one row at a time
+      // (each lane its own row: 32 pieces of 16 bytes an instruction, 2 us a unit).
+      transpose8(o);
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          part[k * p.part_rows] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
-                                              __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
-        if (half == 0) p.part_ml[ps * p.part_rows + row] = make_float2(m_used, l);
+      for (int k = 0; k < 8; ++k) {
+        const int row = quarter * 32 + (lane & 24) + k, t = t0 + (row >> 2);
+        if (t < p.T)
+          reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.h) +
+                                   (static_cast<size_t>(w.b) * p.T + t) * (p.n_kv * 512) + (g * 4 + (row & 3)) * 128 +
+                                   64 * half)[lane & 7] = o[k];
       }
-      if (tile == 0 && r == 0 && half == 0 && w.first == 0 && end < 0) atomicOr(p.status, kDevErrRange);
+    } else if (t0 + (r >> 2) < p.T) {
+      const int row = 128 * tile + r;
+      const size_t ps = partial_slot(worker, w.first > 0);
+      float4* part = reinterpret_cast<float4*>(p.part_o) + (ps * 32 + 16 * half) * p.part_rows + row;
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        part[k * p.part_rows] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                            __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+      if (half == 0) p.part_ml[ps * p.part_rows + row] = make_float2(m_used, l);
     }
+    if (tile == 0 && r == 0 && half == 0 && w.first == 0 && end < 0) atomicOr(p.status, kDevErrRange);
   }
 }
 

@@ -3,17 +3,27 @@
 //
 // A pair is one worker (kv_sched.h) and its units are 64 positions x 4 heads = 256 rows, of which
 // CTA r has the 128 of positions 32 r .. 32 r + 31.  The pair's UMMAs read both CTAs' shared memory,
-// so each CTA stages half of every key tile (keys 64 r .. + 63 of K, d 64 r .. + 63 of V) and a key
-// tile costs one SM 32 KB instead of 64: ten 16 KB stages are 160 KB in flight, and the softmax of a
-// CTA has one row tile per key tile, whose S alternates between two buffers.  With two row tiles in
-// one CTA and the same shared memory the ring held two and a half key tiles, and S could not be
-// buffered: 2.0 us per key tile and SM, against 1.47 us to read it.
-// Roles per CTA as in cache_roles.cuh, but
-//   warp 1      of CTA 0 issues the pair's UMMAs (M = 256), of CTA 1 only keeps its TMEM
-//   warp 2      waits for every V half, clears rows if need be, and tells CTA 0
-// Barriers that the issuer waits on are CTA 0's, and its commits arrive on both CTAs' barriers.
+// so each CTA stages half of every key tile (keys 64 r .. + 63 of K, d 64 r .. + 63 of V): a key tile
+// costs one SM 32 KB instead of 64.
+// A tile's chain is long (K lands, S, softmax, P's word to CTA 0, PV, V's stage and S's buffer free
+// again), so its steps are kept apart: S has three buffers and a warp of its own issues it, up to
+// three tiles ahead of PV, and the next unit's first S wait for nothing but their queries.
+// Warps of a CTA (384 threads):
+//   warp 0      TMA producer of K and V
+//   warp 1      TMEM owner; a unit's queries; in CTA 0 issues the pair's S (M = 256)
+//   warp 2      the rows of its half of V that no row sees, in the tiles that have such rows
+//   warp 3      in CTA 0 issues the pair's PV
+//   warps 4..11 softmax (softmax_halves)
+// Barriers that the issuers wait on are CTA 0's, and their commits arrive on both CTAs' barriers.
 //
-// TMEM columns (each CTA, its own rows): S_0/P_0 at 0, S_1/P_1 at 128, O_0 at 256, O_1 at 384.
+// What it does per key tile is 4 x 256 x 128 x 128 FLOP in 1040 cycles of UMMAs; it takes about 1500,
+// the softmax of 64 keys a thread with its waits (0.8 us, where reading the tile takes 0.73).  32
+// sequences of 8128 keys and 64 tokens (1.1 GB, 275 GFLOP): 202 to 210 us, 5.4 TB/s; one of 32000 keys
+// and 60 tokens 38; 32 of 4000 keys 116, where one CTA with two row tiles (no room for a second S
+// buffer, a ring of two and a half tiles) took 2.0 us per tile.  One issuing warp for S and PV and two
+// buffers of S: 212, 40 and 122 us; alternate tiles for the two softmax warpgroups: 10 % slower.
+//
+// TMEM columns (each CTA, its own rows): S_0/P_0, S_1/P_1, S_2/P_2 at 0, 128, 256, O at 384.
 #pragma once
 
 #include "cache_attn.cuh"
@@ -22,44 +32,59 @@
 namespace gqa {
 
 struct CachePairBars {
-  static constexpr int kStages = 5;  // each of K and V
+  static constexpr int kStages = 5;     // each of K and V
   static constexpr int kV = kStages;
-  static constexpr int kCount = 15 + 5 * kStages;
+  static constexpr int kS = 3, kO = 1;  // buffers of S and O
+  static constexpr int kRing = 6 + 2 * kS;
+  static constexpr int kCount = kRing + 5 * kStages;
   static constexpr int kBytes = 384;
   uint64_t* bars;
   __device__ __forceinline__ explicit CachePairBars(uint8_t* at) : bars(reinterpret_cast<uint64_t*>(at)) {}
-  // CTA 0's: both CTAs' bytes of the queries and of K, and both CTAs' word that V is there and clear
-  __device__ __forceinline__ uint64_t* q_full(int i) const { return bars + i; }
-  __device__ __forceinline__ uint64_t* k_full(int i) const { return bars + 15 + i; }
-  __device__ __forceinline__ uint64_t* v_ready(int i) const { return bars + 15 + kStages + i; }
-  // CTA 0's: an arrival of every softmax warp of both CTAs that writes P's half, or reads O
-  __device__ __forceinline__ uint64_t* p_lo(int i) const { return bars + 2 + i; }
-  __device__ __forceinline__ uint64_t* p_hi(int i) const { return bars + 4 + i; }
-  __device__ __forceinline__ uint64_t* o_empty(int i) const { return bars + 6 + i; }
+  // CTA 0's: both CTAs' bytes of the queries, of K and of V (or, if rows of V are cleared, both CTAs' word
+  // that they are)
+  __device__ __forceinline__ uint64_t* q_full() const { return bars; }
+  __device__ __forceinline__ uint64_t* k_full(int i) const { return bars + kRing + i; }
+  __device__ __forceinline__ uint64_t* v_ready(int i) const { return bars + kRing + kStages + i; }
+  // CTA 0's: an arrival of every softmax warp of both CTAs that has written its part of P, or read O
+  __device__ __forceinline__ uint64_t* p_full(int i) const { return bars + 6 + i; }
+  __device__ __forceinline__ uint64_t* o_empty(int) const { return bars + 1; }
   // each CTA's own
-  __device__ __forceinline__ uint64_t* q_empty(int i) const { return bars + 8 + i; }
-  __device__ __forceinline__ uint64_t* s_full(int i) const { return bars + 10 + i; }
-  __device__ __forceinline__ uint64_t* o_full(int i) const { return bars + 12 + i; }
-  __device__ __forceinline__ uint64_t* drain() const { return bars + 14; }
-  __device__ __forceinline__ uint64_t* k_empty(int i) const { return bars + 15 + 2 * kStages + i; }
-  __device__ __forceinline__ uint64_t* v_full(int i) const { return bars + 15 + 3 * kStages + i; }
-  __device__ __forceinline__ uint64_t* v_empty(int i) const { return bars + 15 + 4 * kStages + i; }
+  __device__ __forceinline__ uint64_t* q_empty() const { return bars + 2; }
+  __device__ __forceinline__ uint64_t* o_full(int) const { return bars + 3; }
+  __device__ __forceinline__ uint64_t* drain(int i) const { return bars + 4 + i; }
+  __device__ __forceinline__ uint64_t* s_full(int i) const { return bars + 6 + kS + i; }
+  __device__ __forceinline__ uint64_t* k_empty(int i) const { return bars + kRing + 2 * kStages + i; }
+  __device__ __forceinline__ uint64_t* v_empty(int i) const { return bars + kRing + 3 * kStages + i; }
+  // the bytes of a half of V of which rows are to be cleared
+  __device__ __forceinline__ uint64_t* v_full(int i) const { return bars + kRing + 4 * kStages + i; }
   __device__ __forceinline__ uint32_t* tmem_holder() const { return reinterpret_cast<uint32_t*>(bars + kCount); }
   __device__ __forceinline__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(tmem_holder() + 1); }
   __device__ __forceinline__ void init() const {
     for (int i = 0; i < kCount; ++i) {
-      const bool p_half = i >= 2 && i < 6, o = i == 6 || i == 7;
-      const bool v_ready = i >= 15 + kStages && i < 15 + 2 * kStages;
-      mbar_init(&bars[i], p_half ? 8u : o ? 16u : v_ready ? 2u : 1u);
+      const bool p_or_o = (i >= 6 && i < 6 + kS) || i == 1, v_ready = i >= kRing + kStages && i < kRing + 2 * kStages;
+      mbar_init(&bars[i], p_or_o ? 16u : v_ready ? 2u : 1u);
     }
     *abort_flag() = 0;
     fence_mbar_init();
   }
 };
 
+// A place in a ring of N and the parity of its phase.
+template <int N>
+struct RingPlace {
+  int i = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
 struct CachePairSmem {
   static constexpr int kStage = kKvTileBytes / 2;  // half a key tile of K or V
-  static constexpr int kK = 2 * kKvTileBytes;      // behind two query tiles
+  static constexpr int kK = kKvTileBytes;          // behind the query tile
   static constexpr int kV = kK + CachePairBars::kStages * kStage;
   static constexpr int kBar = kV + CachePairBars::kStages * kStage;
   static constexpr int kRanges = kBar + CachePairBars::kBytes;
@@ -72,7 +97,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     cache_attn_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const CacheAttnParams p) {
   using L = CachePairSmem;
-  constexpr int kStages = CachePairBars::kStages;
+  constexpr int kStages = CachePairBars::kStages, kS = CachePairBars::kS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -105,168 +130,213 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   // test hook: the last pair loads nothing, its consumers wait out and abort
   const bool no_loads = p.fault && worker == ranges.workers() - 1;
   auto cta0 = [&](uint64_t* b) { return mapa_shared(smem_u32(b), 0); };
+  // a whole warp's waits
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.status));
+  };
+  auto wait_cluster = [&](uint64_t* b, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_cluster(b, parity, abort_flag, p.status));
+  };
+  // a warp that issued UMMAs, after a wait that was given up: they finish before TMEM is released
+  auto drain = [&](uint64_t* b) {
+    if (!__any_sync(0xffffffffu, *abort_flag != 0)) return;
+    if (elect_one_sync()) umma_commit_pair(b, 0x1);
+    __syncwarp();
+    mbar_wait_drain(b, 0);
+  };
+
+  const int units = p.n_kv * p.row_groups;
+  auto next = [&](KvWalk& w) {
+    w.next(units, p.n_new, p.S_max, [&](int b) { return __ldcg(p.kv_len + b); });
+  };
+  // tile t of a piece has rows of V that no row of the product sees
+  auto cleared = [&](const KvWalk& w, int t) { return (t + 1) * kKvTile > keys_all_see(p, w.len); };
 
   if (warp == 0) {
     if (lane == 0 && !no_loads) {
-      // ---------------------------------------------------------------- K producer
-      CacheTiles<1> tiles(p, ranges);
-      int it = 0;
-      tiles.each([&](auto, CacheLane& l) {
-        const int st = it % kStages;
-        if (!mbar_wait(bar.k_empty(st), ((it / kStages) & 1) ^ 1u, abort_flag, p.status)) return false;
-        if (rank == 0) mbar_arrive_expect_tx(bar.k_full(st), 2 * L::kStage);
-        uint8_t* dst = smem + L::kK + st * L::kStage;
-        const int g = l.w.u / p.row_groups, key0 = (l.w.first + l.j) * kKvTile + 64 * rank;
-        tma_load_4d_pair_hint(dst, &tmK, cta0(bar.k_full(st)), 0, g, key0, l.w.b, policy);
-        tma_load_4d_pair_hint(dst + L::kStage / 2, &tmK, cta0(bar.k_full(st)), 64, g, key0, l.w.b, policy);
-        ++it;
-        return true;
-      });
-      // let copies still in flight land before the pair leaves (CTA 0's barriers count both CTAs' bytes)
-      if (*abort_flag && rank == 0)
-        for (int i = max(0, it - kStages); i < it; ++i) mbar_wait_drain(bar.k_full(i % kStages), (i / kStages) & 1);
-    }
-  } else if (warp == 3) {
-    if (lane == 0 && !no_loads) {
-      // ---------------------------------------------------------------- V and query producer
-      CacheTiles<1> tiles(p, ranges);
-      int it = 0, asked = 0;
-      tiles.each([&](auto, CacheLane& l) {
-        const int g = l.w.u / p.row_groups;
-        if (l.j == 0) {
-          const int t0 = (l.w.u - g * p.row_groups) * 64 + 32 * rank;
-          const int at = l.piece & 1, turn = l.piece >> 1;
-          if (turn > 0 && !mbar_wait(bar.q_empty(at), (turn - 1) & 1, abort_flag, p.status)) return false;
-          if (rank == 0) mbar_arrive_expect_tx(bar.q_full(at), 2 * kKvTileBytes);
-          uint8_t* dst = smem + at * kKvTileBytes;
-          tma_load_4d_pair(dst, &tmQ, cta0(bar.q_full(at)), 0, 4 * g, t0, l.w.b);
-          tma_load_4d_pair(dst + kKvHalfBytes, &tmQ, cta0(bar.q_full(at)), 64, 4 * g, t0, l.w.b);
-          ++asked;
+      // ---------------------------------------------------------------- K and V producer
+      // K runs a tile ahead of V (one to four: within 2 %).
+      constexpr int kAhead = 1;
+      KvWalk kw = ranges.walk(0, p), vw = kw;
+      RingPlace<kStages> k, v;
+      int kj = 0, k_asked = 0, v_asked = 0;
+      uint32_t v_own = 0, own_parity = 0;  // of V's places: rows are cleared; parity of v_full's last phase
+      auto ask_k = [&] {
+        if (kw.done()) return true;
+        if (!mbar_wait(bar.k_empty(k.i), k.parity ^ 1u, abort_flag, p.status)) return false;
+        if (rank == 0) mbar_arrive_expect_tx(bar.k_full(k.i), 2 * L::kStage);
+        uint8_t* dst = smem + L::kK + k.i * L::kStage;
+        const int g = kw.u / p.row_groups, key0 = (kw.first + kj) * kKvTile + 64 * rank;
+        tma_load_4d_pair_hint(dst, &tmK, cta0(bar.k_full(k.i)), 0, g, key0, kw.b, policy);
+        tma_load_4d_pair_hint(dst + L::kStage / 2, &tmK, cta0(bar.k_full(k.i)), 64, g, key0, kw.b, policy);
+        ++k_asked;
+        k.next();
+        if (++kj == kw.n) {
+          kj = 0;
+          next(kw);
         }
-        const int st = it % kStages;
-        if (!mbar_wait(bar.v_empty(st), ((it / kStages) & 1) ^ 1u, abort_flag, p.status)) return false;
-        mbar_arrive_expect_tx(bar.v_full(st), L::kStage);
-        tma_load_4d_hint(smem + L::kV + st * L::kStage, &tmV, bar.v_full(st), 64 * rank, g,
-                         (l.w.first + l.j) * kKvTile, l.w.b, policy);
-        ++it;
         return true;
-      });
-      if (*abort_flag) {
-        for (int i = max(0, it - kStages); i < it; ++i) mbar_wait_drain(bar.v_full(i % kStages), (i / kStages) & 1);
-        if (rank == 0)
-          for (int i = max(0, asked - 2); i < asked; ++i) mbar_wait_drain(bar.q_full(i & 1), (i >> 1) & 1);
-      }
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------------ V rows nobody sees
-    CacheTiles<1> tiles(p, ranges);
-    ClearRows clear;
-    int it = 0;
-    if (rank == 0 && lane == 0 && tiles.l0.w.done()) p.merge[worker] = make_int4(-1, 0, 0, 0);
-    tiles.each([&](auto, CacheLane& l) {
-      if (rank == 0 && lane == 0 && l.j == 0 && l.w.after == 0) p.merge[worker] = goes_on(ranges, l.w, worker);
-      const bool fix = clear.prepare(p, l);
-      const int st = it % kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar.v_full(st), (it / kStages) & 1, abort_flag, p.status))) return false;
-      if (fix) clear.rows(p, l, [&](int r, int c) -> uint8_t* {
-        return c < 8 ? smem + L::kV + st * L::kStage + r * 128 + c * 16 : nullptr;  // this CTA's 64 columns
-      });
-      // rows cleared here are read by the pair's UMMAs: ordered at cluster scope
-      if (fix) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cta0(bar.v_ready(st)));
-      } else {
-        if (lane == 0) mbar_arrive_remote(cta0(bar.v_ready(st)));
-      }
-      ++it;
-      return true;
-    });
-  } else if (warp == 1) {
-    if (rank == 0) {
-      // ------------------------------------------------------------------ UMMA issuer of the pair
-      // The whole warp runs the loop (its waits are warp-uniform); one elected lane issues.
-      constexpr uint32_t idesc_s = idesc_bf16_f32(256, 128, 0, 0);   // Q, K both K-major
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(256, 128, 0, 1);  // P (TMEM), V MN-major
-      const uint32_t q_addr = smem_u32(smem), k_addr = smem_u32(smem + L::kK), v_addr = smem_u32(smem + L::kV);
-      CacheTiles<1> tiles(p, ranges);
-      auto wait = [&](uint64_t* b, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.status));
       };
-      auto wait_cluster = [&](uint64_t* b, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait_cluster(b, parity, abort_flag, p.status));
-      };
-      struct Pending {
-        int it, piece;
-        bool first, last, fix;  // first / last tile of the piece; rows of V are cleared
-      } pend{};
-      bool has_pend = false;
-      auto issue_pv = [&] {
-        const Pending d = pend;
-        has_pend = false;
-        const int slot = d.it & 1, o = d.piece & 1, vs = d.it % kStages;
-        // a new O takes the place of the one two pieces before
-        if (d.first && d.piece > 1 && !wait(bar.o_empty(o), ((d.piece >> 1) - 1) & 1)) return false;
-        if (!(d.fix ? wait_cluster(bar.v_ready(vs), (d.it / kStages) & 1) : wait(bar.v_ready(vs), (d.it / kStages) & 1)))
-          return false;
-        const uint64_t vd = sdesc_sw128(v_addr + vs * L::kStage, L::kStage, 1024);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          if (!wait(hf ? bar.p_hi(slot) : bar.p_lo(slot), (d.it >> 1) & 1)) return false;
-          tc_fence_after();
-          if (elect_one_sync()) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int kk = 4 * hf + i;
-              umma_ts_pair(tmem_base + 256 + o * 128, tmem_base + slot * 128 + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv,
-                           !(d.first && kk == 0));
+      bool ok = true;
+      for (int i = 0; i < kAhead && ok; ++i) ok = ask_k();
+      for (; ok && !vw.done(); next(vw)) {
+        for (int j = 0; j < vw.n; ++j) {
+          if (!(ok = ask_k() && mbar_wait(bar.v_empty(v.i), v.parity ^ 1u, abort_flag, p.status))) break;
+          uint8_t* dst = smem + L::kV + v.i * L::kStage;
+          const int g = vw.u / p.row_groups, key0 = (vw.first + j) * kKvTile;
+          if (cleared(vw, vw.first + j)) {
+            v_own |= 1u << v.i;
+            own_parity ^= 1u << v.i;
+            mbar_arrive_expect_tx(bar.v_full(v.i), L::kStage);
+            tma_load_4d_hint(dst, &tmV, bar.v_full(v.i), 64 * rank, g, key0, vw.b, policy);
+          } else {
+            v_own &= ~(1u << v.i);
+            if (rank == 0) {
+              mbar_arrive_expect_tx(bar.v_ready(v.i), 2 * L::kStage);
+              mbar_arrive(bar.v_ready(v.i));
             }
-            if (hf) {
-              umma_commit_pair(bar.v_empty(vs), 0x3);
-              if (d.last) umma_commit_pair(bar.o_full(o), 0x3);
-            }
+            tma_load_4d_pair_hint(dst, &tmV, cta0(bar.v_ready(v.i)), 64 * rank, g, key0, vw.b, policy);
           }
-          __syncwarp();
+          ++v_asked;
+          v.next();
         }
-        return true;
-      };
-      int it = 0;
-      const bool ok = tiles.each([&](auto, CacheLane& l) {
-        const bool first = l.j == 0, last = l.j == l.w.n - 1;
-        const int ks = it % kStages, slot = it & 1, at = l.piece & 1;
-        if (first && !wait(bar.q_full(at), (l.piece >> 1) & 1)) return false;
-        if (!wait(bar.k_full(ks), (it / kStages) & 1)) return false;
+        if (!ok) break;
+      }
+      // let copies still in flight land before the pair leaves (CTA 0's barriers count both CTAs' bytes)
+      if (*abort_flag) {
+        for (int i = max(0, k_asked - kStages); rank == 0 && i < k_asked; ++i)
+          mbar_wait_drain(bar.k_full(i % kStages), (i / kStages) & 1);
+        for (int i = max(0, v_asked - kStages); i < v_asked; ++i) {
+          const int at = i % kStages;
+          if ((v_own >> at) & 1)
+            mbar_wait_drain(bar.v_full(at), ((own_parity >> at) & 1) ^ 1u);
+          else if (rank == 0)
+            mbar_wait_drain(bar.v_ready(at), (i / kStages) & 1);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ queries; S = Q K^T of the pair
+    // The whole warp runs the loop (its waits are warp-uniform); one elected lane issues.  S is up to
+    // three tiles ahead of PV, so that a unit's queries arrive under the softmax of the unit before.
+    constexpr uint32_t idesc_s = idesc_bf16_f32(256, 128, 0, 0);  // Q, K both K-major
+    const uint64_t q_desc = sdesc_sw128(smem_u32(smem), 0, 1024);
+    const uint32_t k_addr = smem_u32(smem + L::kK);
+    RingPlace<kStages> k, v;  // v: of the PV whose P the tile's S takes the place of
+    RingPlace<kS> s;
+    KvWalk w = ranges.walk(0, p);
+    int piece = 0, free_s = kS;
+    bool ok = !no_loads;
+    for (; ok && !w.done(); next(w), ++piece) {
+      if (piece > 0 && !(ok = wait(bar.q_empty(), (piece - 1) & 1))) break;
+      if (elect_one_sync()) {
+        const int g = w.u / p.row_groups, t0 = (w.u - g * p.row_groups) * 64 + 32 * rank;
+        if (rank == 0) mbar_arrive_expect_tx(bar.q_full(), 2 * kKvTileBytes);
+        tma_load_4d_pair(smem, &tmQ, cta0(bar.q_full()), 0, 4 * g, t0, w.b);
+        tma_load_4d_pair(smem + kKvHalfBytes, &tmQ, cta0(bar.q_full()), 64, 4 * g, t0, w.b);
+      }
+      __syncwarp();
+      if (rank == 1) continue;
+      if (!(ok = wait(bar.q_full(), piece & 1))) {
+        if (lane == 0) mbar_wait_drain(bar.q_full(), piece & 1);  // (both CTAs' bytes)
+        break;
+      }
+      for (int j = 0; j < w.n; ++j) {
+        if (!(ok = wait(bar.k_full(k.i), k.parity))) break;
+        if (free_s > 0) {
+          --free_s;
+        } else {
+          if (!(ok = wait(bar.v_empty(v.i), v.parity))) break;
+          v.next();
+        }
         tc_fence_after();
         if (elect_one_sync()) {
-          const uint64_t qd = sdesc_sw128(q_addr + at * kKvTileBytes, 0, 1024);
-          const uint64_t kd = sdesc_sw128(k_addr + ks * L::kStage, 0, 1024);
+          const uint64_t kd = sdesc_sw128(k_addr + k.i * L::kStage, 0, 1024);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_ss_pair(tmem_base + slot * 128, qd + (((kk >> 2) * kKvHalfBytes + (kk & 3) * 32) >> 4),
+            umma_ss_pair(tmem_base + s.i * 128, q_desc + (((kk >> 2) * kKvHalfBytes + (kk & 3) * 32) >> 4),
                          kd + (((kk >> 2) * (L::kStage / 2) + (kk & 3) * 32) >> 4), idesc_s, kk != 0);
-          umma_commit_pair(bar.s_full(slot), 0x3);
-          umma_commit_pair(bar.k_empty(ks), 0x3);
-          if (last) umma_commit_pair(bar.q_empty(at), 0x3);
+          umma_commit_pair(bar.s_full(s.i), 0x3);
+          umma_commit_pair(bar.k_empty(k.i), 0x3);
+          if (j == w.n - 1) umma_commit_pair(bar.q_empty(), 0x3);
         }
         __syncwarp();
-        if (has_pend && !issue_pv()) return false;
-        pend = Pending{it, l.piece, first, last, (l.w.first + l.j + 1) * kKvTile > keys_all_see(p, l.w.len)};
-        has_pend = true;
-        ++it;
-        return true;
-      });
-      if (ok && has_pend) issue_pv();
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) {  // let issued UMMAs finish before TMEM is released
-        if (elect_one_sync()) umma_commit_pair(bar.drain(), 0x1);
-        __syncwarp();
-        mbar_wait_drain(bar.drain(), 0);
+        k.next();
+        s.next();
       }
+    }
+    if (rank == 0) drain(bar.drain(0));
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ V rows nobody sees
+    ClearRows clear;
+    uint32_t own_parity = 0;  // of V's places: parity of v_full's next phase
+    int it0 = 0;              // tiles before the piece
+    KvWalk w = ranges.walk(0, p);
+    if (rank == 0 && lane == 0 && w.done()) p.merge[worker] = make_int4(-1, 0, 0, 0);
+    bool ok = true;
+    for (; ok && !w.done(); it0 += w.n, next(w)) {
+      if (rank == 0 && lane == 0 && w.after == 0) p.merge[worker] = goes_on(ranges, w, worker);
+      for (int j = max(0, keys_all_see(p, w.len) / kKvTile - w.first); j < w.n; ++j) {
+        const CacheLane l{w, j, 0};
+        clear.prepare(p, l);
+        const int vs = (it0 + j) % kStages;
+        const uint32_t parity = (own_parity >> vs) & 1;
+        own_parity ^= 1u << vs;
+        if (!(ok = wait(bar.v_full(vs), parity))) break;
+        const bool any = clear.rows(p, l, [&](int r, int c) -> uint8_t* {
+          return c < 8 ? smem + L::kV + vs * L::kStage + r * 128 + c * 16 : nullptr;  // this CTA's 64 columns
+        });
+        // rows cleared here are read by the pair's UMMAs: ordered at cluster scope
+        if (any) {
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          if (any)
+            mbar_arrive_cluster(cta0(bar.v_ready(vs)));
+          else
+            mbar_arrive_remote(cta0(bar.v_ready(vs)));
+        }
+      }
+    }
+  } else if (warp == 3) {
+    if (rank == 0) {
+      // ---------------------------------------------------------------- O += P V of the pair
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(256, 128, 0, 1);  // P (TMEM), V MN-major
+      const uint32_t v_addr = smem_u32(smem + L::kV);
+      RingPlace<kStages> v;
+      RingPlace<kS> s;
+      KvWalk w = ranges.walk(0, p);
+      int piece = 0;
+      bool ok = true;
+      for (; ok && !w.done(); next(w), ++piece) {
+        // the piece's O takes the place of the piece's before
+        if (piece > 0 && !(ok = wait(bar.o_empty(0), (piece - 1) & 1))) break;
+        for (int j = 0; j < w.n; ++j) {
+          const bool there = cleared(w, w.first + j) ? wait_cluster(bar.v_ready(v.i), v.parity) : wait(bar.v_ready(v.i), v.parity);
+          if (!(ok = there && wait(bar.p_full(s.i), s.parity))) break;
+          tc_fence_after();
+          if (elect_one_sync()) {
+            const uint64_t vd = sdesc_sw128(v_addr + v.i * L::kStage, L::kStage, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              umma_ts_pair(tmem_base + kS * 128, tmem_base + s.i * 128 + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv,
+                           j + kk != 0);
+            umma_commit_pair(bar.v_empty(v.i), 0x3);
+            if (j == w.n - 1) umma_commit_pair(bar.o_full(0), 0x3);
+          }
+          __syncwarp();
+          v.next();
+          s.next();
+        }
+      }
+      drain(bar.drain(1));
     }
   } else {
     softmax_halves(
         p, ranges, bar, tmem_base, reinterpret_cast<float*>(smem + L::kExchange), rank, worker,
         [&](uint64_t* b, uint32_t parity) { return mbar_wait(b, parity, abort_flag, p.status); },
-        [&](int slot, int half) { mbar_arrive_remote(cta0(half ? bar.p_hi(slot) : bar.p_lo(slot))); },
+        [&](int slot, int) { mbar_arrive_remote(cta0(bar.p_full(slot))); },
         [&](int at) { mbar_arrive_remote(cta0(bar.o_empty(at))); });
   }
 

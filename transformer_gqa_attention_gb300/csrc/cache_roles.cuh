@@ -45,7 +45,8 @@ constexpr int kKStages = 2;
 constexpr int kVStages = 3;
 
 struct CacheBars {
-  static constexpr int kV = kVStages;  // V stages
+  static constexpr int kV = kVStages;      // V stages
+  static constexpr int kS = 2, kO = 2;     // buffers of S and O
   static constexpr int kCount = 28;
   static constexpr int kBytes = 256;  // barriers, TMEM address, abort flag
   uint64_t* bars;
@@ -295,17 +296,19 @@ struct ClearRows {
     }
     return true;
   }
-  // at(row, c): address of 16-byte chunk c (0..15) of a tile row, or null
+  // at(row, c): address of 16-byte chunk c (0..15) of a tile row, or null.  Whether there was such a row.
   template <typename F>
-  __device__ __forceinline__ void rows(const CacheAttnParams& p, const CacheLane& l, F at) const {
+  __device__ __forceinline__ bool rows(const CacheAttnParams& p, const CacheLane& l, F at) const {
     const int lane = threadIdx.x & 31;
     const bool bad = kv_end(l.w.len, p.n_new, p.S_max) < 0;
     const int d0 = (l.w.first + l.j) * kKvTile - keys_all_see(p, l.w.len);  // drafted index of row 0
+    bool any = false;
     for (int r0 = 0; r0 < kKvTile; r0 += 32) {
       const int d = d0 + r0 + lane;
       const uint32_t word = __shfl_sync(0xffffffffu, seen, (d >> 5) & 7);
       const bool dead = d >= 0 && (bad || d >= p.n_new || !((word >> (d & 31)) & 1u));
       uint32_t todo = __ballot_sync(0xffffffffu, dead);
+      any |= todo != 0;
       while (todo) {  // two rows at a time, 16 lanes each
         const int ra = __ffs(todo) - 1;
         todo &= todo - 1;
@@ -315,6 +318,7 @@ struct ClearRows {
         if (dst) *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
       }
     }
+    return any;
   }
 };
 
