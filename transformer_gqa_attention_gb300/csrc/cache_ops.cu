@@ -17,6 +17,9 @@ constexpr int kCommitSlices = 8;  // CTAs (one cluster) per sequence; each moves
 
 // Rows prefix + path[i] -> prefix + i of both caches.  path is strictly increasing, so path[i] >=
 // i: every row moves towards the front, and the rows of one step are read before any is written.
+// At most 2 MB move: a launch is what it costs (2.6 us in a graph for 1 and for 64 sequences), so the
+// slices of a row are CTAs of their own, and the length, which may be written over, is written once the
+// cluster has read it.
 __global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const CommitParams p) {
   griddep_wait();
   const int b = blockIdx.y, slice = blockIdx.x;
@@ -107,6 +110,9 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
 // counts through distributed shared memory and finds the digit; once all of a digit's positions are
 // wanted the search ends early.  Then everything above is kept, and the first of the equal ones: a
 // position's place is the number kept before it, a prefix sum over the slice and the CTAs before.
+// Reads each weight once (a slice stays in shared memory; only heads of more than 49152 positions read it
+// five times) and is bound by the passes' barriers and shared-memory atomics: 7 us of the 8.9 that
+// one sequence of 4100 positions takes, 18 of 140 for 32 of up to 8192.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
   __shared__ __align__(16) float stage[kSelChunk];
   __shared__ __align__(16) int hist[kSelBins];
@@ -275,7 +281,7 @@ constexpr int kMoveSlices = 2 * 16 / kMovePieces;  // of K and V; one more block
 // Rows kept[i] -> i: one CTA per (64-byte column slice of K or V, kv group, sequence), or several
 // that take steps in turn when the outputs are other buffers.  kept is ascending, so kept[i] >= i; in
 // place, a step's rows are all read before any is written, and no later step reads a row that it
-// wrote.
+// wrote.  Bound by memory: up to 4096 of up to 8192 positions of 32 sequences (820 MB) in 122 us, 6.7 TB/s.
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
   griddep_wait();
   const int slice = blockIdx.x % (kMoveSlices + 1), part = blockIdx.x / (kMoveSlices + 1), g = blockIdx.y, b = blockIdx.z;
