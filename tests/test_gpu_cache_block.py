@@ -330,6 +330,40 @@ def test_a_call_that_has_to_grow_is_refused_while_capturing(blk):
         abi.attn_destroy(ctx)
 
 
+def test_a_refused_capture_leaves_nothing_behind(blk):
+    # the block's workspace is large enough, the scratch of the attention is not: no kernel is recorded
+    ctx = abi.attn_create(*blk.w)
+    try:
+        T, S = 4, 300
+        vis, depth = tree(np.random.default_rng(12), 1, T)
+        x, k, v = draw(575, [200], T, S)
+        kd, vd = k.to(DEV), v.to(DEV)
+        bk, bv = gu.empty_cache(1, 256)
+        abi.attn_prefill(ctx, torch.zeros(1, 256, 4096, dtype=torch.bfloat16, device=DEV), 1, 256,
+                         torch.zeros(256, 64, 2, device=DEV), True, bk, bv, 256, 0, torch.empty(1, 256, 4096, device=DEV))
+        out = torch.zeros(1, T, 4096, device=DEV)
+        w = torch.zeros(1, 8, S, device=DEV)
+        args = (x.to(DEV), 1, T, rope(200 + depth).to(DEV), words(vis), kd, vd, S, ints([200]), out)
+        steps = (x[:, :1].contiguous().to(DEV), 1, rope(200 + depth)[:, 0].contiguous().to(DEV), kd, vd, S, ints([200]), w,
+                 out[:, :1].contiguous())
+        mark = torch.zeros(1, device=DEV)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            mark += 1
+            for call, a in ((abi.attn_prefill_tree, args), (abi.attn_decode_weights, steps)):
+                with pytest.raises(abi.GQAError) as err:
+                    call(ctx, *a)
+                assert err.value.status == 4
+        g.replay()
+        torch.cuda.synchronize()
+        assert mark.item() == 1 and (out == 0).all() and (w == 0).all()
+        assert torch.equal(kd.cpu().view(torch.int16), k.view(torch.int16))
+        assert torch.equal(vd.cpu().view(torch.int16), v.view(torch.int16))
+    finally:
+        abi.attn_destroy(ctx)
+
+
 def test_on_a_second_stream_behind_other_work(blk):
     # lengths, mask and queries are written on the stream just before the calls that read them
     T, S, B = 12, 700, 3

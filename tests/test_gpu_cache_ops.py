@@ -498,3 +498,21 @@ def test_a_wait_that_runs_out_is_reported(weights):
         run_weights(12, [700, 700], S=900)
     else:
         run_tree(12, [700, 700], 3, S=900)
+
+
+@pytest.mark.parametrize("T", [40, 200])
+def test_a_wait_of_a_pair_that_runs_out_is_reported(T):
+    # more than 32 tokens: the last pair of CTAs issues no loads, and the call after is right
+    ctx = context()
+    gen = torch.Generator().manual_seed(13)
+    k, v = (t.to(DEV) for t in draw_cache(gen, 2, 900, 8, [800, 800]))
+    q = torch.randn(2, T, 4096, generator=gen).to(torch.bfloat16).to(DEV)
+    h = torch.zeros(2, T, 4096, dtype=torch.bfloat16, device=DEV)
+    mask = torch.from_numpy(co.mask_words(np.stack([np.eye(T, dtype=bool)] * 2))).to(DEV)
+    abi.attn_debug_inject_timeout(ctx, "cache_attn")
+    abi.attn_tree_attention(ctx, q, 2, T, mask, k, v, 900, ints([600, 600]), h)
+    with pytest.raises(abi.GQAError) as err:
+        abi.attn_sync_status(ctx)
+    assert err.value.status == 5
+    abi.attn_sync_status(ctx)
+    run_tree(14, [600, 600], T, S=900)

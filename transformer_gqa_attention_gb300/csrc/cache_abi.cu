@@ -16,9 +16,58 @@
 
 using namespace gqa;
 
+namespace {
+
+// What a call keeps in the context's scratch, in bytes from its start.
+struct CacheLayout {
+  bool pair;
+  int group_pos, row_groups, part_rows;
+  size_t workers;
+  size_t merge, part_ml, part_o, total_tiles, scores, tile_unit, unit_ml, bytes;
+};
+
+CacheLayout cache_layout(const gqa_ctx* c, const CacheAttnCall& a) {
+  CacheLayout l{};
+  const int n_ctas = c->num_sms & ~1;  // persistent, one per SM (the GPU's 152: even)
+  l.pair = a.T > kOneTilePos;
+  l.group_pos = l.pair ? 64 : kOneTilePos;
+  l.row_groups = (a.T + l.group_pos - 1) / l.group_pos;
+  l.part_rows = static_cast<int>(round_up(4 * std::min(a.T, l.group_pos), 32));
+  auto take = [&](size_t bytes) {
+    const size_t at = l.bytes;
+    l.bytes = round_up(l.bytes + bytes, 256);
+    return at;
+  };
+  // workers: CTAs, with weights their two softmax slots, with many positions CTA pairs; each may hold
+  // two partial results
+  l.workers = a.weights ? 2 * n_ctas : l.pair ? n_ctas / 2 : n_ctas;
+  const size_t slots = 2 * l.workers;
+  l.merge = take(l.workers * sizeof(int4));
+  l.part_ml = take(slots * l.part_rows * sizeof(float2));
+  l.part_o = take(slots * l.part_rows * 128 * sizeof(float));
+  if (a.weights) {
+    const size_t units = static_cast<size_t>(a.B) * c->n_kv;
+    const size_t tiles = units * ((a.S_max + kKvTile - 1) / kKvTile);
+    l.total_tiles = take(sizeof(int));
+    l.scores = take(tiles * 4 * kKvTile * sizeof(float));
+    l.tile_unit = take(tiles * sizeof(int4));
+    l.unit_ml = take(units * 4 * sizeof(float2));
+  }
+  return l;
+}
+
+}  // namespace
+
+gqa_status gqa::reserve_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t s) {
+  return ensure_buffer(c, c->cache_ws, cache_layout(c, a).bytes, s);
+}
+
 gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t s) {
   const int G = c->n_kv;
-  const int n_ctas = c->num_sms & ~1;  // persistent, one per SM (the GPU's 152: even)
+  const CacheLayout l = cache_layout(c, a);
+  gqa_status st = ensure_buffer(c, c->cache_ws, l.bytes, s);
+  if (st != GQA_OK) return st;
+  uint8_t* ws = c->cache_ws.p;
   CacheAttnParams p{};
   p.B = a.B;
   p.T = a.T;
@@ -31,44 +80,17 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   p.weights = a.weights;
   p.status = c->status;
   p.scale_log2 = kScaleLog2;
-  const bool pair = a.T > kOneTilePos;
-  p.group_pos = pair ? 64 : kOneTilePos;
-  p.row_groups = (a.T + p.group_pos - 1) / p.group_pos;
-  p.part_rows = static_cast<int>(round_up(4 * std::min(a.T, p.group_pos), 32));
-
-  size_t off = 0;
-  auto take = [&](size_t bytes) {
-    const size_t at = off;
-    off = round_up(off + bytes, 256);
-    return at;
-  };
-  // workers: CTAs, with weights their two softmax slots, with many positions CTA pairs; each may hold
-  // two partial results
-  const size_t workers = a.weights ? 2 * n_ctas : pair ? n_ctas / 2 : n_ctas;
-  const size_t slots = 2 * workers;
-  const size_t merge = take(workers * sizeof(int4));
-  const size_t part_ml = take(slots * p.part_rows * sizeof(float2));
-  const size_t part_o = take(slots * p.part_rows * 128 * sizeof(float));
-  size_t total = 0, scores = 0, tile_unit = 0, unit_ml = 0;
+  p.group_pos = l.group_pos;
+  p.row_groups = l.row_groups;
+  p.part_rows = l.part_rows;
+  p.merge = reinterpret_cast<int4*>(ws + l.merge);
+  p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
+  p.part_o = reinterpret_cast<float*>(ws + l.part_o);
   if (a.weights) {
-    const size_t units = static_cast<size_t>(a.B) * G;
-    const size_t tiles = units * ((a.S_max + kKvTile - 1) / kKvTile);
-    total = take(sizeof(int));
-    scores = take(tiles * 4 * kKvTile * sizeof(float));
-    tile_unit = take(tiles * sizeof(int4));
-    unit_ml = take(units * 4 * sizeof(float2));
-  }
-  gqa_status st = ensure_buffer(c, c->cache_ws, off, s);
-  if (st != GQA_OK) return st;
-  uint8_t* ws = c->cache_ws.p;
-  p.merge = reinterpret_cast<int4*>(ws + merge);
-  p.part_ml = reinterpret_cast<float2*>(ws + part_ml);
-  p.part_o = reinterpret_cast<float*>(ws + part_o);
-  if (a.weights) {
-    p.total_tiles = reinterpret_cast<int*>(ws + total);
-    p.scores = reinterpret_cast<float*>(ws + scores);
-    p.tile_unit = reinterpret_cast<int4*>(ws + tile_unit);
-    p.unit_ml = reinterpret_cast<float2*>(ws + unit_ml);
+    p.total_tiles = reinterpret_cast<int*>(ws + l.total_tiles);
+    p.scores = reinterpret_cast<float*>(ws + l.scores);
+    p.tile_unit = reinterpret_cast<int4*>(ws + l.tile_unit);
+    p.unit_ml = reinterpret_cast<float2*>(ws + l.unit_ml);
   }
 
   CUtensorMap tq, tk, tv;
@@ -77,20 +99,20 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   const uint64_t strides[3] = {256, static_cast<uint64_t>(G) * 1024, static_cast<uint64_t>(a.T) * G * 1024};
   const uint32_t box[4] = {64, 4, a.weights ? 1u : kOneTilePos, 1};
   if (!make_map(&tq, a.q, 4, dims, strides, box) ||
-      !map_cache(&tk, a.cache_k, a.B, a.S_max, G, a.S_max, pair ? kKvTile / 2 : kKvTile) ||
+      !map_cache(&tk, a.cache_k, a.B, a.S_max, G, a.S_max, l.pair ? kKvTile / 2 : kKvTile) ||
       !map_cache(&tv, a.cache_v, a.B, a.S_max, G, a.S_max, kKvTile))
     return cuda_fail(cudaErrorInvalidValue);
   p.fault = take_fault(c, GQA_KERNEL_CACHE_ATTN);
   {
     ProfScope ps(c, GQA_KERNEL_CACHE_ATTN, s);
-    GQA_CUDA(launch_cache_attn(tq, tk, tv, p, n_ctas, s));
+    GQA_CUDA(launch_cache_attn(tq, tk, tv, p, c->num_sms & ~1, s));
   }
   if (a.weights) {
     ProfScope ps(c, GQA_KERNEL_CACHE_WEIGHTS, s);
-    GQA_CUDA(launch_cache_weights(p, static_cast<int>(workers), 8 * c->num_sms, s));
+    GQA_CUDA(launch_cache_weights(p, static_cast<int>(l.workers), 8 * c->num_sms, s));
   } else {
     ProfScope ps(c, GQA_KERNEL_CACHE_MERGE, s);
-    GQA_CUDA(launch_cache_merge(p, static_cast<int>(workers), s));
+    GQA_CUDA(launch_cache_merge(p, static_cast<int>(l.workers), s));
   }
   return GQA_OK;
 }

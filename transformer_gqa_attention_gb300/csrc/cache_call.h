@@ -21,6 +21,10 @@ struct CacheAttnCall {
   float* weights;        // T = 1 only; null: none
 };
 
+// Makes room for the call's scratch: a caller that enqueues other work first does so before, as a
+// refusal enqueues nothing.
+gqa_status reserve_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t s);
+
 // Arguments already checked; enqueues the attention on `s`.
 gqa_status run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t s);
 

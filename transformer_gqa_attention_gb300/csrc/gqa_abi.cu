@@ -535,13 +535,6 @@ gqa_status ragged_impl(gqa_ctx* c, const void* x, int B, int T, const float* R, 
   void* h = c->ws.p + w.h_off;
   c->last_q = q_r;
   c->last_h = h;
-  const float* row_scale = nullptr;
-  if (residual) {
-    if ((st = run_rms(c, x, n_tok, w, s)) != GQA_OK) return st;
-    row_scale = reinterpret_cast<const float*>(c->ws.p + w.rstd_off);
-  }
-  st = run_qkv(c, x, n_tok, T, R, cache_k, cache_v, S_max, 0, kv_len, q_r, w, sk, row_scale, s);
-  if (st != GQA_OK) return st;
   CacheAttnCall a{};
   a.B = B;
   a.T = T;
@@ -554,6 +547,14 @@ gqa_status ragged_impl(gqa_ctx* c, const void* x, int B, int T, const float* R, 
   a.cache_v = cache_v;
   a.h = h;
   a.weights = weights;
+  if ((st = reserve_cache_attn(c, a, s)) != GQA_OK) return st;
+  const float* row_scale = nullptr;
+  if (residual) {
+    if ((st = run_rms(c, x, n_tok, w, s)) != GQA_OK) return st;
+    row_scale = reinterpret_cast<const float*>(c->ws.p + w.rstd_off);
+  }
+  st = run_qkv(c, x, n_tok, T, R, cache_k, cache_v, S_max, 0, kv_len, q_r, w, sk, row_scale, s);
+  if (st != GQA_OK) return st;
   if ((st = run_cache_attn(c, a, s)) != GQA_OK) return st;
   return run_out(c, h, n_tok, delta, w, sk, residual ? x : nullptr, s);
 }
