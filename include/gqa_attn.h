@@ -475,14 +475,15 @@ gqa_status attn_debug_pair_schedule(int m_tiles, int n_tiles, int n_pairs, int *
  * attn_debug_cache_schedule — how tree attention and attn_decode_attention_weights share the
  * 128-key tiles of B sequences among `workers` workers (CTAs or their softmax slots), computed
  * on the host by the code that the kernel runs (for tests, no GPU needed).  lens [B] (host), n_new
- * keys behind each length, units (kv heads x groups of query rows) per sequence.  Writes the
+ * keys behind each length, units (kv heads x groups of query rows) per sequence, unit_cost (0 .. 64)
+ * the tiles that beginning and ending a unit counts for (8, 3 and 2 in the kernels).  Writes the
  * pieces in order as octuples (worker, sequence, unit, first tile, tiles, slot of its partial
  * result or -1 for a whole unit, last worker of the unit, number of the first tile among all
  * tiles) into pieces[8 * max_pieces]; *n_pieces gets their count.  Errors:
  * GQA_ERR_INVALID_ARG, GQA_ERR_SHAPE (more than max_pieces pieces; *n_pieces holds the count).
  */
-gqa_status attn_debug_cache_schedule(const int *lens, int B, int n_new, int S_max, int units, int workers,
-                                     int *pieces, int max_pieces, int *n_pieces);
+gqa_status attn_debug_cache_schedule(const int *lens, int B, int n_new, int S_max, int units, int unit_cost,
+                                     int workers, int *pieces, int max_pieces, int *n_pieces);
 
 /*
  * attn_debug_exp2 — the two exponentials the prefill softmax uses, on n fp32 device inputs a

@@ -1,6 +1,6 @@
 """How the attention over caches of per-sequence length shares its key tiles (host computation, the
 code the kernel runs; no GPU needed): every tile of every unit is taken once, in order, the workers'
-shares (tiles, and two more for each unit begun) are even, the partial results of a cut unit lie in
+shares (tiles, and unit_cost more for each unit begun) are even, the partial results of a cut unit lie in
 slots that no other unit uses, and the tiles are numbered without gaps."""
 import random
 
@@ -8,28 +8,26 @@ import pytest
 
 from transformer_gqa_attention_gb300 import _build, abi
 
-UNIT_COST = 2
-
 
 @pytest.fixture(scope="module", autouse=True)
 def _built():
     _build.build()
 
 
-def check(lens, n_new, S_max, units, workers):
-    pieces = abi.attn_debug_cache_schedule(lens, n_new, S_max, units, workers)
+def check(lens, n_new, S_max, units, workers, cost):
+    pieces = abi.attn_debug_cache_schedule(lens, n_new, S_max, units, cost, workers)
     tiles = [max(1, -(-(n + n_new) // 128)) if 0 <= n <= S_max - n_new else 1 for n in lens]
     want = [(b, u, t) for b in range(len(lens)) for u in range(units) for t in range(tiles[b])]
     got = [(b, u, t) for _, b, u, first, n, *_ in pieces for t in range(first, first + n)]
     assert got == want
-    places = sum((t + UNIT_COST) * units for t in tiles)
+    places = sum((t + cost) * units for t in tiles)
     share = places / min(workers, places)
     load = {}
     number = 0
     for c, b, u, first, n, _, _, flat in pieces:
         assert n > 0 and flat == number
         number += n
-        load[c] = load.get(c, 0) + n + (UNIT_COST if first == 0 and c in load else 0)
+        load[c] = load.get(c, 0) + n + (cost if first == 0 and c in load else 0)
     assert max(load.values()) <= share + 1
     assert [c for c, *_ in pieces] == sorted(c for c, *_ in pieces)
     cut, used = {}, {}
@@ -47,13 +45,14 @@ def check(lens, n_new, S_max, units, workers):
         assert parts[0][1] == 0 and len(parts) >= 2
 
 
+@pytest.mark.parametrize("cost", [0, 2, 3, 6, 9])
 @pytest.mark.parametrize("workers", [1, 2, 7, 76, 148, 304])
 @pytest.mark.parametrize("lens", [[0], [1], [127], [128], [129], [32000], [0, 0, 0], [5, 4000, 128, 1], [-1, 70, 2 ** 31 - 1],
                                   [300] * 33])
-def test_small_batches(lens, workers):
+def test_small_batches(lens, workers, cost):
     for units in (1, 8, 16, 32):
         for n_new in (0, 1, 26):
-            check(lens, n_new, 40000, units, workers)
+            check(lens, n_new, 40000, units, workers, cost)
 
 
 def test_random_batches():
@@ -62,13 +61,13 @@ def test_random_batches():
         B = rng.choice([1, 3, 40, 385, 800, 1024])
         top = rng.choice([10, 1000, 20000])
         check([rng.randint(-1, top) for _ in range(B)], rng.choice([0, 1, 64]), top + 64, rng.choice([1, 2, 8]),
-              rng.choice([76, 152, 304]))
+              rng.choice([76, 152, 304]), rng.choice([2, 3, 6]))
 
 
 def test_arguments():
-    for kw in (dict(units=0), dict(workers=0), dict(n_new=-1), dict(S_max=0)):
-        a = dict(n_new=1, S_max=10, units=1, workers=2) | kw
+    for kw in (dict(units=0), dict(unit_cost=-1), dict(workers=0), dict(n_new=-1), dict(S_max=0)):
+        a = dict(n_new=1, S_max=10, units=1, unit_cost=2, workers=2) | kw
         with pytest.raises(abi.GQAError):
             abi.attn_debug_cache_schedule([1], **a)
     with pytest.raises(abi.GQAError):
-        abi.attn_debug_cache_schedule([], 1, 10, 1, 2)
+        abi.attn_debug_cache_schedule([], 1, 10, 1, 2, 2)

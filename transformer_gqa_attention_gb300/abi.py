@@ -103,7 +103,7 @@ def lib() -> ctypes.CDLL:
         getattr(L, name).restype = i32
     L.attn_cache_evict.argtypes = [vp, vp, vp, vp, i32, i32, vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp]
     L.attn_cache_evict.restype = i32
-    L.attn_debug_cache_schedule.argtypes = [ip, i32, i32, i32, i32, i32, ip, i32, ip]
+    L.attn_debug_cache_schedule.argtypes = [ip, i32, i32, i32, i32, i32, i32, ip, i32, ip]
     L.attn_debug_cache_schedule.restype = i32
     L.attn_destroy.argtypes = [vp]
     L.attn_destroy.restype = None
@@ -323,7 +323,7 @@ def attn_cache_evict(ctx, cache_k, cache_v, weights, B, S_max, kv_len, budget, n
                                   _ptr(out_weights), int(S_out), _ptr(kept), _ptr(new_len), _stream(stream)))
 
 
-def attn_debug_cache_schedule(lens, n_new, S_max, units, workers):
+def attn_debug_cache_schedule(lens, n_new, S_max, units, unit_cost, workers):
     """The pieces in which workers share the sequences' key tiles (host computation, no GPU
     needed): a list of (worker, sequence, unit, first tile, tiles, partial slot or -1, the unit's
     last worker, the first tile's number among all tiles)."""
@@ -331,12 +331,12 @@ def attn_debug_cache_schedule(lens, n_new, S_max, units, workers):
     B = len(lens)
     arr, n = (i32 * B)(*lens), i32()
     L = lib()
-    st = L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, workers, None, 0, ctypes.byref(n))
+    st = L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, unit_cost, workers, None, 0, ctypes.byref(n))
     if st not in (0, 2):  # GQA_ERR_SHAPE: the count is in n
         _check("attn_debug_cache_schedule", st)
     buf = (i32 * (8 * max(n.value, 1)))()
     _check("attn_debug_cache_schedule",
-           L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, workers, buf, n.value, ctypes.byref(n)))
+           L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, unit_cost, workers, buf, n.value, ctypes.byref(n)))
     return [tuple(buf[8 * i:8 * i + 8]) for i in range(n.value)]
 
 

@@ -82,6 +82,7 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   p.scale_log2 = kScaleLog2;
   p.group_pos = l.group_pos;
   p.row_groups = l.row_groups;
+  p.unit_cost = a.weights ? kUnitCostDecode : l.pair ? kUnitCostPair : kUnitCostTile;
   p.part_rows = l.part_rows;
   p.merge = reinterpret_cast<int4*>(ws + l.merge);
   p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
@@ -284,15 +285,15 @@ gqa_status attn_cache_evict(gqa_ctx* c, const void* cache_k, const void* cache_v
   return GQA_OK;
 }
 
-gqa_status attn_debug_cache_schedule(const int* lens, int B, int n_new, int S_max, int units, int workers, int* pieces,
-                                     int max_pieces, int* n_pieces) {
+gqa_status attn_debug_cache_schedule(const int* lens, int B, int n_new, int S_max, int units, int unit_cost, int workers,
+                                     int* pieces, int max_pieces, int* n_pieces) {
   if (!lens || !n_pieces || (!pieces && max_pieces > 0) || B < 1 || n_new < 0 || S_max < 1 || units < 1 ||
-      workers < 1 || max_pieces < 0)
+      unit_cost < 0 || unit_cost > 64 || workers < 1 || max_pieces < 0)
     return GQA_ERR_INVALID_ARG;
   auto len_of = [&](int b) { return b < B ? lens[b] : 0; };
-  auto places_of = [&](int b) { return (kv_tiles(kv_end(len_of(b), n_new, S_max)) + kUnitCost) * units; };
+  auto places_of = [&](int b) { return (kv_tiles(kv_end(len_of(b), n_new, S_max)) + unit_cost) * units; };
   long long all = 0;
-  for (int b = 0; b < B; ++b) all += (static_cast<long long>(kv_tiles(kv_end(lens[b], n_new, S_max))) + kUnitCost) * units;
+  for (int b = 0; b < B; ++b) all += (static_cast<long long>(kv_tiles(kv_end(lens[b], n_new, S_max))) + unit_cost) * units;
   if (all > 0x7FFFFFFF) return GQA_ERR_SHAPE;
   const int total = static_cast<int>(all), n_work = range_workers(total, workers);
   int n = 0;
@@ -301,7 +302,7 @@ gqa_status attn_debug_cache_schedule(const int* lens, int B, int n_new, int S_ma
     int b = 0, at = 0;
     while (at + places_of(b) <= lo) at += places_of(b++);
     KvWalk w;
-    for (w.start(b, lo - at, len_of(b), n_new, S_max, lo, hi - lo); !w.done(); w.next(units, n_new, S_max, len_of), ++n) {
+    for (w.start(unit_cost, b, lo - at, len_of(b), n_new, S_max, lo, hi - lo); !w.done(); w.next(units, n_new, S_max, len_of), ++n) {
       if (n < max_pieces) {
         int* o = pieces + 8 * n;
         o[0] = c;

@@ -49,6 +49,45 @@ __device__ __forceinline__ void transpose8(uint4 (&x)[8]) {
   }
 }
 
+// The end of a piece for a row's thread, which has float4 columns 16 half .. + 15 of O, unnormalised, in v: a
+// whole unit goes to h, another into the scratch.  Called by whole warps.
+__device__ __forceinline__ void store_piece(const CacheAttnParams& p, const KvWalk& w, int end, int g, int t0, int tile,
+                                            int worker, int half, int quarter, float m, float l, const uint32_t (&v)[64]) {
+  const int lane = threadIdx.x & 31;
+      if (w.whole()) {
+        // no visible key: zeros; a length out of range: NaN
+        const float inv = end < 0 ? __int_as_float(0x7FC00000) : (l == 0.f ? 0.f : 1.f / l);
+        uint4 o[8];
+  #pragma unroll
+        for (int k = 0; k < 8; ++k)
+          o[k] = make_uint4(pack_bf16x2(__uint_as_float(v[8 * k + 0]) * inv, __uint_as_float(v[8 * k + 1]) * inv),
+                            pack_bf16x2(__uint_as_float(v[8 * k + 2]) * inv, __uint_as_float(v[8 * k + 3]) * inv),
+                            pack_bf16x2(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv),
+                            pack_bf16x2(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv));
+        // A lane has 128 bytes of its row; eight lanes exchange theirs, so that they store one row at a time
+        // (each lane its own row: 32 pieces of 16 bytes an instruction, 2 us a unit).
+        transpose8(o);
+  #pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = quarter * 32 + (lane & 24) + k, t = t0 + (row >> 2);
+          if (t < p.T)
+            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.h) +
+                                     (static_cast<size_t>(w.b) * p.T + t) * (p.n_kv * 512) + (g * 4 + (row & 3)) * 128 +
+                                     64 * half)[lane & 7] = o[k];
+        }
+      } else if (t0 + quarter * 8 + (lane >> 2) < p.T) {
+        const int row = 128 * tile + quarter * 32 + lane;
+        const size_t ps = partial_slot(worker, w.first > 0);
+        float4* part = reinterpret_cast<float4*>(p.part_o) + (ps * 32 + 16 * half) * p.part_rows + row;
+  #pragma unroll
+        for (int k = 0; k < 16; ++k)
+          part[k * p.part_rows] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                              __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+        if (half == 0) p.part_ml[ps * p.part_rows + row] = make_float2(m, l);
+      }
+      if (tile == 0 && quarter == 0 && lane == 0 && half == 0 && w.first == 0 && end < 0) atomicOr(p.status, kDevErrRange);
+}
+
 // The softmax warps of a row tile (warps 4..11), whose rows are positions t0 + 32 tile .. + 31 of a
 // unit.  Two threads share a row: warps 4..7 take keys 0..63 of a key tile, warps 8..11 keys 64..127
 // (TMEM lanes belong to a warp's number mod 4), which halves the time between a tile's S and its PV.
@@ -205,38 +244,7 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
     const float l_other = *other;
     const float l = half ? l_other + l_sum : l_sum + l_other;
     named_bar_sync(bar_id, 64);  // read before the next exchange
-    if (w.whole()) {
-      // no visible key: zeros; a length out of range: NaN
-      const float inv = end < 0 ? __int_as_float(0x7FC00000) : (l == 0.f ? 0.f : 1.f / l);
-      uint4 o[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        o[k] = make_uint4(pack_bf16x2(__uint_as_float(v[8 * k + 0]) * inv, __uint_as_float(v[8 * k + 1]) * inv),
-                          pack_bf16x2(__uint_as_float(v[8 * k + 2]) * inv, __uint_as_float(v[8 * k + 3]) * inv),
-                          pack_bf16x2(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv),
-                          pack_bf16x2(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv));
-      // A lane has 128 bytes of its row; eight lanes exchange theirs, so that they store one row at a time
-      // (each lane its own row: 32 pieces of 16 bytes an instruction, 2 us a unit).
-      transpose8(o);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int row = quarter * 32 + (lane & 24) + k, t = t0 + (row >> 2);
-        if (t < p.T)
-          reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.h) +
-                                   (static_cast<size_t>(w.b) * p.T + t) * (p.n_kv * 512) + (g * 4 + (row & 3)) * 128 +
-                                   64 * half)[lane & 7] = o[k];
-      }
-    } else if (t0 + (r >> 2) < p.T) {
-      const int row = 128 * tile + r;
-      const size_t ps = partial_slot(worker, w.first > 0);
-      float4* part = reinterpret_cast<float4*>(p.part_o) + (ps * 32 + 16 * half) * p.part_rows + row;
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        part[k * p.part_rows] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
-                                            __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
-      if (half == 0) p.part_ml[ps * p.part_rows + row] = make_float2(m_used, l);
-    }
-    if (tile == 0 && r == 0 && half == 0 && w.first == 0 && end < 0) atomicOr(p.status, kDevErrRange);
+    store_piece(p, w, end, g, t0, tile, worker, half, quarter, m_used, l, v);
   }
 }
 

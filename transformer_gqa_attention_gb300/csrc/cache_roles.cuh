@@ -91,7 +91,7 @@ struct CacheRanges {
     KvWalk w;
     w.n = 0;
     if (where[3 + 5 * s] > 0)
-      w.start(where[4 + 5 * s], where[5 + 5 * s], where[6 + 5 * s], p.n_new, p.S_max, where[2 + 5 * s], where[3 + 5 * s]);
+      w.start(p.unit_cost, where[4 + 5 * s], where[5 + 5 * s], where[6 + 5 * s], p.n_new, p.S_max, where[2 + 5 * s], where[3 + 5 * s]);
     return w;
   }
 
@@ -107,7 +107,7 @@ struct CacheRanges {
     for (int i = 0; i < 3; ++i) {
       const bool in = i < per && b0 + i < p.B;
       lens[i] = in ? __ldcg(p.kv_len + b0 + i) : 0;
-      places[i] = in ? (kv_tiles(kv_end(lens[i], p.n_new, p.S_max)) + kUnitCost) * units : 0;
+      places[i] = in ? (kv_tiles(kv_end(lens[i], p.n_new, p.S_max)) + p.unit_cost) * units : 0;
       mine += places[i];
     }
     int x = mine;
@@ -128,7 +128,7 @@ struct CacheRanges {
     if (threadIdx.x == 0) {
       where[0] = total;
       where[1] = n_work;
-      if (p.total_tiles && blockIdx.x == 0) *p.total_tiles = total - kUnitCost * units * p.B;
+      if (p.total_tiles && blockIdx.x == 0) *p.total_tiles = total - p.unit_cost * units * p.B;
     }
 #pragma unroll
     for (int s = 0; s < kWork; ++s) {

@@ -3,7 +3,7 @@
 //
 // A unit is (sequence b, kv head, group of query rows); it reads the ceil(end_b / 128) key tiles
 // of its sequence (at least one, so that every unit writes its rows).  Beginning and ending a unit
-// costs about as much as kUnitCost tiles, so each unit has that many empty places before its tiles.
+// costs about as much as `cost` tiles, so each unit has that many empty places before its tiles.
 // The units' places, unit after unit and sequence after sequence, form one row of `total` places, of
 // which worker c of n takes places c total / n .. (c + 1) total / n - 1: equal work whatever the
 // lengths are, without the host knowing them.  What a worker takes of one unit's tiles is a piece; a
@@ -20,11 +20,14 @@
 namespace gqa {
 
 constexpr int kKvTile = 128;
-// A tile takes 0.9 to 1.5 us, the end of a unit and the start of the next about 3.  Measured with 0, 2
-// and 4: 29.7, 27.1, 26.7 us for 8 ragged sequences of up to 4000 keys and 26 drafted tokens; 29.0,
-// 25.5, 23.4 for 6 of up to 2000 and 150 tokens; 34.2, 33.9, 35.0 for the decode step of 16 of up to
-// 4096 with key weights.
-constexpr int kUnitCost = 2;
+// Empty places per unit.  A tile takes 0.7 (pairs) to 1.5 us, the end of a unit and the start of the next
+// about 3.  Measured with 2, 4, 6, 8 and 10, us: pairs 37.0, 35.5, 35.7, 35.8, 35.7 for one sequence of 32000 keys and 60
+// tokens, 23.4, 20.9, 20.7, 20.4, 20.6 for 6 of up to 2000 and 150, 79.8, 69.2, 65.0, 62.8, 62.8 for a ragged batch of
+// 40 units of a dozen tiles a pair; with 2, 3, 4 and 6 one tile 26.2, 25.8, 26.0, 26.3 for 8 sequences of up to 4000 and 26 tokens,
+// 89.6, 89.8, 90.3, 90.8 for 32 of 4000 and 8; decode step 33.5, 34.5, 34.4, 35.5 for 16 of up to 4096 keys.
+constexpr int kUnitCostPair = 8;
+constexpr int kUnitCostTile = 3;
+constexpr int kUnitCostDecode = 2;
 
 // Keys that sequence b reads: its length and the n_new positions behind it; -1: out of range.
 GQA_HD int kv_end(int len, int n_new, int S_max) { return len < 0 || len > S_max - n_new ? -1 : len + n_new; }
@@ -53,6 +56,7 @@ GQA_HD int range_owner(int total, int n, int x) {
 
 // The pieces of one range, in order.
 struct KvWalk {
+  int cost;       // empty places of a unit
   int b, u;       // sequence, unit in it (kv head x row groups + row group)
   int len;        // the sequence's length
   int tiles;      // key tiles of each of the sequence's units
@@ -62,16 +66,17 @@ struct KvWalk {
   int lo;         // the unit's first place
 
   // A range of `count` places from place `begin` on, which is `offset` places into sequence b.
-  GQA_HD void start(int b_, int offset, int len_, int n_new, int S_max, int begin, int count) {
+  GQA_HD void start(int cost_, int b_, int offset, int len_, int n_new, int S_max, int begin, int count) {
+    cost = cost_;
     b = b_;
     len = len_;
     tiles = kv_tiles(kv_end(len, n_new, S_max));
-    u = offset / (tiles + kUnitCost);
-    const int pos = offset - u * (tiles + kUnitCost);
+    u = offset / (tiles + cost);
+    const int pos = offset - u * (tiles + cost);
     lo = begin - pos;
-    first = pos > kUnitCost ? pos - kUnitCost : 0;
-    const int mine = min_(tiles + kUnitCost - pos, count);
-    n = pos + mine - kUnitCost - first;
+    first = pos > cost ? pos - cost : 0;
+    const int mine = min_(tiles + cost - pos, count);
+    n = pos + mine - cost - first;
     if (n < 0) n = 0;
     after = rest_(count - mine);
     // (a range that ends inside the empty places has no tile of this unit, and none behind it)
@@ -84,25 +89,25 @@ struct KvWalk {
     n = 0;
     if (after == 0) return;
     first = 0;
-    lo += tiles + kUnitCost;
+    lo += tiles + cost;
     if (++u == units) {
       u = 0;
       len = len_of(++b);
       tiles = kv_tiles(kv_end(len, n_new, S_max));
     }
-    const int mine = min_(tiles + kUnitCost, after);
-    n = mine - kUnitCost;
+    const int mine = min_(tiles + cost, after);
+    n = mine - cost;
     after = rest_(after - mine);
   }
   // place of the unit's tile t
-  GQA_HD int place(int t) const { return lo + kUnitCost + t; }
+  GQA_HD int place(int t) const { return lo + cost + t; }
   // number of the unit's tile t among all tiles
-  GQA_HD int tile(int t, int units) const { return lo - kUnitCost * (b * units + u) + t; }
+  GQA_HD int tile(int t, int units) const { return lo - cost * (b * units + u) + t; }
 
  private:
   GQA_HD static int min_(int x, int y) { return x < y ? x : y; }
   // what is left of a range, if it reaches a tile of the next unit
-  GQA_HD static int rest_(int x) { return x > kUnitCost ? x : 0; }
+  GQA_HD int rest_(int x) const { return x > cost ? x : 0; }
 };
 
 // Slots of partial results: a worker has at most two pieces that are not whole units, the one its

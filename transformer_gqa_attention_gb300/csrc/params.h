@@ -109,6 +109,7 @@ struct CacheAttnParams {
   float scale_log2;        // log2(e) / sqrt(128)
   // rows: a kv head's T positions in row_groups groups of group_pos (kOneTilePos, or 64 on two tiles)
   int row_groups, group_pos;
+  int unit_cost;           // empty places of a unit in the workers' shares (kv_sched.h)
   // scratch: per worker the unit that goes on past its range (sequence or -1, unit, the unit's first
   // and last worker), the partial results of cut units ([2 workers][32 float4 columns][part_rows], with
   // weights [2 workers][part_rows][128]) and their (maximum, sum)

@@ -258,6 +258,11 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t n, bool v) {
   return r != 0;
 }
 
+// Arrive at named barrier `id` without waiting for the others.
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t n) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
 // Named barrier `id` over `n` threads (n a multiple of 32).
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
