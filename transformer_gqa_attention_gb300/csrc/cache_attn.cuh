@@ -131,6 +131,14 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
     for (int j = 0; j < w.n; ++j, ++it) {
       const int slot = it % Bars::kS;
       const uint32_t t_s = t_row + slot * 128;
+      const int key0 = (w.first + j) * kKvTile + 64 * half;
+      const bool masked = key0 + 64 > safe;
+      KeyWords<2> seen;
+      if (masked && warp_live) {
+        const int t = t0 + (r >> 2);
+        const bool live = t < p.T;
+        seen.load(p.mask ? p.mask + (static_cast<size_t>(w.b) * p.T + (live ? t : 0)) * W : nullptr, W, key0 - safe, live);
+      }
       if (!loading) ok = __all_sync(0xffffffffu, wait(bar.s_full(slot), (it / Bars::kS) & 1));
       if (!warp_live) {  // rows past the last position: whatever their P is, their O is not used
         if (!ok) break;
@@ -139,14 +147,10 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
       }
       if (!loading) load_s(slot);
       tmem_ld_wait();
-      const int key0 = (w.first + j) * kKvTile + 64 * half;
-      if (key0 + 64 > safe) {
-        const int t = t0 + (r >> 2);
-        const bool live = t < p.T;
-        const uint32_t* mask = p.mask ? p.mask + (static_cast<size_t>(w.b) * p.T + (live ? t : 0)) * W : nullptr;
+      if (masked) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const uint32_t bits = key_bits(mask, W, end < 0 ? 0 : p.n_new, key0 + 32 * c - safe, live);
+          const uint32_t bits = seen.bits(c, end < 0 ? 0 : p.n_new);
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (!((bits >> k) & 1u)) sv[32 * c + k] = 0xFF800000u;  // -inf

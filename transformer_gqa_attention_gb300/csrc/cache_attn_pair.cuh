@@ -135,6 +135,11 @@ __device__ __forceinline__ void softmax_in_turn(const CacheAttnParams& p, const 
     for (int j = (it & 1) ^ set; j < w.n; j += 2) {
       const int tile = it + j, slot = tile % kS;
       const uint32_t t_s = t_row + 128 * slot;
+      const int key0 = (w.first + j) * kKvTile;
+      const bool masked = key0 + kKvTile > safe;
+      KeyWords<4> seen;
+      if (masked && warp_live)
+        seen.load(p.mask ? p.mask + (static_cast<size_t>(w.b) * p.T + (live ? t : 0)) * W : nullptr, W, key0 - safe, live);
       ok = ok && wait(bar.s_full(slot), (tile / kS) & 1);
       if (!warp_live) {  // rows past the last position: whatever their P is, their O is not used
         if (!ok) break;
@@ -151,12 +156,10 @@ __device__ __forceinline__ void softmax_in_turn(const CacheAttnParams& p, const 
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
       tmem_ld_wait();
-      const int key0 = (w.first + j) * kKvTile;
-      if (key0 + kKvTile > safe) {
-        const uint32_t* mask = p.mask ? p.mask + (static_cast<size_t>(w.b) * p.T + (live ? t : 0)) * W : nullptr;
+      if (masked) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint32_t bits = key_bits(mask, W, end < 0 ? 0 : p.n_new, key0 + 32 * c - safe, live);
+          const uint32_t bits = seen.bits(c, end < 0 ? 0 : p.n_new);
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (!((bits >> k) & 1u)) sv[32 * c + k] = 0xFF800000u;  // -inf
@@ -448,8 +451,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           const uint32_t parity = (own_parity >> vs) & 1;
           own_parity ^= 1u << vs;
           if (!(ok = wait(bar.v_full(vs), parity))) break;
-          const bool any = clear.rows(p, l, [&](int r, int c) -> uint8_t* {
-            return c < 8 ? smem + L::kV + vs * L::kStage + r * 128 + c * 16 : nullptr;  // this CTA's 64 columns
+          const bool any = clear.rows<8>(p, l, [&](int r, int c) {
+            return smem + L::kV + vs * L::kStage + r * 128 + c * 16;  // this CTA's 64 columns
           });
           // rows cleared here are read by the pair's UMMAs: ordered at cluster scope
           if (any) {

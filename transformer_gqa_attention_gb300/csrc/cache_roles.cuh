@@ -296,29 +296,27 @@ struct ClearRows {
     }
     return true;
   }
-  // at(row, c): address of 16-byte chunk c (0..15) of a tile row, or null.  Whether there was such a row.
-  template <typename F>
+  // Zeroes them: a lane takes a row, at(row, c) is the address of its 16-byte chunk c < kChunks.  Whether
+  // there was such a row.
+  template <int kChunks, typename F>
   __device__ __forceinline__ bool rows(const CacheAttnParams& p, const CacheLane& l, F at) const {
     const int lane = threadIdx.x & 31;
     const bool bad = kv_end(l.w.len, p.n_new, p.S_max) < 0;
     const int d0 = (l.w.first + l.j) * kKvTile - keys_all_see(p, l.w.len);  // drafted index of row 0
     bool any = false;
+#pragma unroll
     for (int r0 = 0; r0 < kKvTile; r0 += 32) {
       const int d = d0 + r0 + lane;
       const uint32_t word = __shfl_sync(0xffffffffu, seen, (d >> 5) & 7);
       const bool dead = d >= 0 && (bad || d >= p.n_new || !((word >> (d & 31)) & 1u));
-      uint32_t todo = __ballot_sync(0xffffffffu, dead);
-      any |= todo != 0;
-      while (todo) {  // two rows at a time, 16 lanes each
-        const int ra = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int rb = todo ? __ffs(todo) - 1 : ra;
-        todo &= todo - 1;
-        uint8_t* dst = at(r0 + (lane < 16 ? ra : rb), lane & 15);
-        if (dst) *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+      any |= dead;
+      if (dead) {
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k)  // (eight lanes at a time: in other banks)
+          *reinterpret_cast<uint4*>(at(r0 + lane, (k + lane) % kChunks)) = make_uint4(0, 0, 0, 0);
       }
     }
-    return any;
+    return __any_sync(0xffffffffu, any);
   }
 };
 
@@ -343,7 +341,7 @@ __device__ __forceinline__ void clear_v(const CacheAttnParams& p, const CacheRan
     const int st = it % kVStages;
     if (!__all_sync(0xffffffffu, mbar_wait(bar.v_full(st), (it / kVStages) & 1, abort_flag, p.status))) return false;
     if (fix) {
-      clear.rows(p, l, [&](int r, int c) {
+      clear.rows<16>(p, l, [&](int r, int c) {
         return ring + st * kKvTileBytes + (c >> 3) * kKvHalfBytes + r * 128 + (c & 7) * 16;
       });
       fence_proxy_async_smem();
@@ -439,19 +437,29 @@ __device__ __forceinline__ void issue_all(const CacheAttnParams& p, const CacheR
   }
 }
 
-// Visibility bits of the 32 keys whose drafted index starts at `base` (negative: prefix, always
-// seen) for a mask row of W words over n_new drafted positions; a row without a mask (null) that
-// is live sees all n_new.
-__device__ __forceinline__ uint32_t key_bits(const uint32_t* mask, int W, int n_new, int base, bool live) {
-  if (base <= -32) return 0xFFFFFFFFu;
-  if (base >= n_new) return 0u;
-  const int q = base >> 5;  // floor: -1 where the word straddles the prefix
-  const uint32_t none = !live ? 0u : 0xFFFFFFFFu;
-  const uint32_t lo = q < 0 ? 0xFFFFFFFFu : (mask ? (live ? __ldcg(mask + q) : 0u) : none);
-  const uint32_t hi = q + 1 < W ? (mask ? (live ? __ldcg(mask + q + 1) : 0u) : none) : 0u;
-  const uint32_t bits = __funnelshift_r(lo, hi, base & 31);
-  const int rem = n_new - base;
-  return rem < 32 ? bits & ((1u << rem) - 1u) : bits;
-}
+// Visibility of 32 N keys to one row, whose first has drafted index `base` (negative: prefix, always seen),
+// over n_new drafted positions: the mask row's N + 1 words around them, loaded ahead of their use.  A row
+// without a mask (null) that is live sees all n_new.
+template <int N>
+struct KeyWords {
+  uint32_t w[N + 1];
+  int base;
+  __device__ __forceinline__ void load(const uint32_t* mask, int W, int base_, bool live) {
+    base = base_;
+    const int q = base >> 5;  // floor
+#pragma unroll
+    for (int i = 0; i <= N; ++i) {
+      // (without conditions, so that all are in flight together)
+      const uint32_t word = mask ? __ldcg(mask + min(max(q + i, 0), W - 1)) : 0xFFFFFFFFu;
+      w[i] = q + i < 0 ? 0xFFFFFFFFu : q + i < W && live ? word : 0u;
+    }
+  }
+  // of keys 32 c .. 32 c + 31
+  __device__ __forceinline__ uint32_t bits(int c, int n_new) const {
+    const uint32_t x = __funnelshift_r(w[c], w[c + 1], base & 31);
+    const int rem = n_new - (base + 32 * c);
+    return rem <= 0 ? 0u : rem < 32 ? x & ((1u << rem) - 1u) : x;
+  }
+};
 
 }  // namespace gqa
