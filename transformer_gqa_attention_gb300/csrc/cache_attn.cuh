@@ -49,56 +49,53 @@ __device__ __forceinline__ void transpose8(uint4 (&x)[8]) {
   }
 }
 
-// The end of a piece for a row's thread, which has float4 columns 16 half .. + 15 of O, unnormalised, in v: a
-// whole unit goes to h, another into the scratch.  Called by whole warps.
+// The end of a piece for a row's thread, which has columns 64 half .. + 63 of O, unnormalised, in v: a whole
+// unit goes to h, another into the scratch.  Called by whole warps; row tile `tile` of the worker's.
 __device__ __forceinline__ void store_piece(const CacheAttnParams& p, const KvWalk& w, int end, int g, int t0, int tile,
                                             int worker, int half, int quarter, float m, float l, const uint32_t (&v)[64]) {
   const int lane = threadIdx.x & 31;
-      if (w.whole()) {
-        // no visible key: zeros; a length out of range: NaN
-        const float inv = end < 0 ? __int_as_float(0x7FC00000) : (l == 0.f ? 0.f : 1.f / l);
-        uint4 o[8];
-  #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          o[k] = make_uint4(pack_bf16x2(__uint_as_float(v[8 * k + 0]) * inv, __uint_as_float(v[8 * k + 1]) * inv),
-                            pack_bf16x2(__uint_as_float(v[8 * k + 2]) * inv, __uint_as_float(v[8 * k + 3]) * inv),
-                            pack_bf16x2(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv),
-                            pack_bf16x2(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv));
-        // A lane has 128 bytes of its row; eight lanes exchange theirs, so that they store one row at a time
-        // (each lane its own row: 32 pieces of 16 bytes an instruction, 2 us a unit).
-        transpose8(o);
-  #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int row = quarter * 32 + (lane & 24) + k, t = t0 + (row >> 2);
-          if (t < p.T)
-            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.h) +
-                                     (static_cast<size_t>(w.b) * p.T + t) * (p.n_kv * 512) + (g * 4 + (row & 3)) * 128 +
-                                     64 * half)[lane & 7] = o[k];
-        }
-      } else if (t0 + quarter * 8 + (lane >> 2) < p.T) {
-        const int row = 128 * tile + quarter * 32 + lane;
-        const size_t ps = partial_slot(worker, w.first > 0);
-        float4* part = reinterpret_cast<float4*>(p.part_o) + (ps * 32 + 16 * half) * p.part_rows + row;
-  #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          part[k * p.part_rows] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
-                                              __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
-        if (half == 0) p.part_ml[ps * p.part_rows + row] = make_float2(m, l);
-      }
-      if (tile == 0 && quarter == 0 && lane == 0 && half == 0 && w.first == 0 && end < 0) atomicOr(p.status, kDevErrRange);
+  auto value = [&](int i) { return __uint_as_float(v[i]); };
+  if (w.whole()) {
+    // no visible key: zeros; a length out of range: NaN
+    const float inv = end < 0 ? __int_as_float(0x7FC00000) : (l == 0.f ? 0.f : 1.f / l);
+    uint4 o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      o[k] = make_uint4(pack_bf16x2(value(8 * k) * inv, value(8 * k + 1) * inv),
+                        pack_bf16x2(value(8 * k + 2) * inv, value(8 * k + 3) * inv),
+                        pack_bf16x2(value(8 * k + 4) * inv, value(8 * k + 5) * inv),
+                        pack_bf16x2(value(8 * k + 6) * inv, value(8 * k + 7) * inv));
+    // A lane has 128 bytes of its row; eight lanes exchange theirs, so that they store one row at a time
+    // (each lane its own row would be 32 pieces of 16 bytes an instruction).
+    transpose8(o);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int row = quarter * 32 + (lane & 24) + k, t = t0 + (row >> 2);
+      if (t < p.T)
+        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.h) +
+                                 (static_cast<size_t>(w.b) * p.T + t) * (p.n_kv * 512) + (g * 4 + (row & 3)) * 128 +
+                                 64 * half)[lane & 7] = o[k];
+    }
+  } else if (t0 + quarter * 8 + (lane >> 2) < p.T) {
+    const int row = 128 * tile + quarter * 32 + lane;
+    const size_t ps = partial_slot(worker, w.first > 0);
+    float4* part = reinterpret_cast<float4*>(p.part_o) + (ps * 32 + 16 * half) * p.part_rows + row;
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      part[k * p.part_rows] = make_float4(value(4 * k), value(4 * k + 1), value(4 * k + 2), value(4 * k + 3));
+    if (half == 0) p.part_ml[ps * p.part_rows + row] = make_float2(m, l);
+  }
+  if (tile == 0 && quarter == 0 && lane == 0 && half == 0 && w.first == 0 && end < 0) atomicOr(p.status, kDevErrRange);
 }
 
-// The softmax warps of a row tile (warps 4..11), whose rows are positions t0 + 32 tile .. + 31 of a
-// unit.  Two threads share a row: warps 4..7 take keys 0..63 of a key tile, warps 8..11 keys 64..127
+// The softmax warps (warps 4..11), whose rows are positions t0 .. t0 + 31 of a unit.  Two threads share a row: warps 4..7 take keys 0..63 of a key tile, warps 8..11 keys 64..127
 // (TMEM lanes belong to a warp's number mod 4), which halves the time between a tile's S and its PV.
 // The row maximum is only needed to keep 2^(c s - m) in range: m follows the scores when one of them
 // passes m + 8, on a vote of the 64 threads of a row group; then the two halves' maxima are exchanged
 // and O and l rescaled.
-//   wait(barrier, parity); arrive_p(S buffer, half), arrive_o(O buffer): a warp's arrivals, by its lane 0
-template <typename Bars, typename FW, typename FP, typename FO>
-__device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const CacheRanges& ranges, const Bars& bar,
-                                               uint32_t tmem_base, float* exchange, int tile, int worker, FW wait,
-                                               FP arrive_p, FO arrive_o) {
+__device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const CacheRanges& ranges, const CacheBars& bar,
+                                               uint32_t tmem_base, float* exchange) {
+  constexpr int kS = 2, kO = 2;  // buffers of S and O
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = (warp - 4) >> 2;  // keys 64 half .. + 63; columns 64 half .. + 63 of O
   const int quarter = warp & 3;
@@ -109,6 +106,11 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
   const float* other = exchange + (half ^ 1) * 128 + r;
   const int W = (p.T + 31) / 32;
   const int units = p.n_kv * p.row_groups;
+  volatile int* abort_flag = bar.abort_flag();
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.status));
+  };
+  auto arrive_p = [&](int slot) { mbar_arrive(half ? bar.p_hi(slot) : bar.p_lo(slot)); };
   KvWalk w = ranges.walk(0, p);
   int it = 0, piece = 0;
   bool ok = true;
@@ -116,9 +118,9 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
     const int end = kv_end(w.len, p.n_new, p.S_max);
     const int safe = keys_all_see(p, w.len);
     const int g = w.u / p.row_groups;
-    const int t0 = (w.u - g * p.row_groups) * p.group_pos + 32 * tile;
+    const int t0 = (w.u - g * p.row_groups) * p.group_pos;
     const bool warp_live = t0 + quarter * 8 < p.T;
-    const uint32_t t_o = t_row + 128 * (Bars::kS + piece % Bars::kO) + 64 * half;  // this half's columns of O
+    const uint32_t t_o = t_row + 128 * (kS + piece % kO) + 64 * half;  // this half's columns of O
     float m_used = -INFINITY, l_sum = 0.f;
     uint32_t sv[64];
     bool loading = false;  // the tile's S is on its way
@@ -129,7 +131,7 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
       tmem_ld32(at + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
     };
     for (int j = 0; j < w.n; ++j, ++it) {
-      const int slot = it % Bars::kS;
+      const int slot = it % kS;
       const uint32_t t_s = t_row + slot * 128;
       const int key0 = (w.first + j) * kKvTile + 64 * half;
       const bool masked = key0 + 64 > safe;
@@ -139,10 +141,10 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
         const bool live = t < p.T;
         seen.load(p.mask ? p.mask + (static_cast<size_t>(w.b) * p.T + (live ? t : 0)) * W : nullptr, W, key0 - safe, live);
       }
-      if (!loading) ok = __all_sync(0xffffffffu, wait(bar.s_full(slot), (it / Bars::kS) & 1));
+      if (!loading) ok = wait(bar.s_full(slot), (it / kS) & 1);
       if (!warp_live) {  // rows past the last position: whatever their P is, their O is not used
         if (!ok) break;
-        if (lane == 0) arrive_p(slot, half);
+        if (lane == 0) arrive_p(slot);
         continue;
       }
       if (!loading) load_s(slot);
@@ -180,7 +182,7 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
         if (j > 0) {
           // O holds the sum through the tile before once its PV, issued behind this tile's S, is done and
           // has released its V (a wait given up shows at the next tile)
-          __all_sync(0xffffffffu, wait(bar.v_empty((it - 1) % Bars::kV), ((it - 1) / Bars::kV) & 1));
+          wait(bar.v_empty((it - 1) % kVStages), ((it - 1) / kVStages) & 1);
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -215,24 +217,24 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
         tmem_st16(t_s + 32 * half + c * 16, pw);
       }
       // the next tile's S, if it is there, comes in under the rest of this one
-      const int s_next = (it + 1) % Bars::kS;
+      const int s_next = (it + 1) % kS;
       loading = j + 1 < w.n &&
-                __all_sync(0xffffffffu, mbar_test_wait(bar.s_full(s_next), ((it + 1) / Bars::kS) & 1));
+                __all_sync(0xffffffffu, mbar_test_wait(bar.s_full(s_next), ((it + 1) / kS) & 1));
       if (loading) load_s(s_next);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_p(slot, half);
+      if (lane == 0) arrive_p(slot);
       const float2 l2 = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
       l_sum += l2.x + l2.y;
     }
     // ---------------------------------------------------------------- end of a piece
-    const int at = piece % Bars::kO;
+    const int at = piece % kO;
     // one decision of the row group's warps, with or without live rows, whether a wait was given up
-    ok = ok && __all_sync(0xffffffffu, wait(bar.o_full(at), (piece / Bars::kO) & 1));
+    ok = ok && wait(bar.o_full(at), (piece / kO) & 1);
     if (!(ok = named_bar_and(bar_id, 64, ok))) break;
     if (!warp_live) {
-      if (lane == 0) arrive_o(at);
+      if (lane == 0) mbar_arrive(bar.o_empty(at));
       continue;
     }
     tc_fence_after();
@@ -243,12 +245,12 @@ __device__ __forceinline__ void softmax_halves(const CacheAttnParams& p, const C
     tmem_ld_wait();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) arrive_o(at);
+    if (lane == 0) mbar_arrive(bar.o_empty(at));
     named_bar_sync(bar_id, 64);
     const float l_other = *other;
     const float l = half ? l_other + l_sum : l_sum + l_other;
     named_bar_sync(bar_id, 64);  // read before the next exchange
-    store_piece(p, w, end, g, t0, tile, worker, half, quarter, m_used, l, v);
+    store_piece(p, w, end, g, t0, 0, blockIdx.x, half, quarter, m_used, l, v);
   }
 }
 
@@ -314,11 +316,7 @@ __global__ void __launch_bounds__(384, 1)
           }
         });
   } else {
-    softmax_halves(
-        p, ranges, bar, tmem_base, reinterpret_cast<float*>(smem + L::kExchange), 0, blockIdx.x,
-        [&](uint64_t* b, uint32_t parity) { return mbar_wait(b, parity, bar.abort_flag(), p.status); },
-        [&](int slot, int half) { mbar_arrive(half ? bar.p_hi(slot) : bar.p_lo(slot)); },
-        [&](int at) { mbar_arrive(bar.o_empty(at)); });
+    softmax_halves(p, ranges, bar, tmem_base, reinterpret_cast<float*>(smem + L::kExchange));
   }
 
   tc_fence_before();

@@ -7,21 +7,23 @@
 // costs one SM 32 KB instead of 64.
 // A tile's chain is long (K lands, S, softmax, P's word to CTA 0, PV, V's stage and S's buffer free
 // again), so its steps are kept apart: S has three buffers and a warp of its own issues it, up to
-// three tiles ahead of PV, and the next unit's first S wait for nothing but their queries.
+// three tiles ahead of PV; the softmax's two warpgroups have a tile each on their hands.
 // Warps of a CTA (384 threads):
 //   warp 0      TMA producer of K and V
 //   warp 1      TMEM owner; a unit's queries; in CTA 0 issues the pair's S (M = 256)
 //   warp 2      the rows of its half of V that no row sees, in the tiles that have such rows
 //   warp 3      in CTA 0 issues the pair's PV
-//   warps 4..11 softmax (softmax_halves)
+//   warps 4..11 softmax (softmax_in_turn)
 // Barriers that the issuers wait on are CTA 0's, and their commits arrive on both CTAs' barriers.
 //
-// What it does per key tile is 4 x 256 x 128 x 128 FLOP in 1040 cycles of UMMAs; it takes about 1500,
-// the softmax of 64 keys a thread with its waits (0.8 us, where reading the tile takes 0.73).  32
-// sequences of 8128 keys and 64 tokens (1.1 GB, 275 GFLOP): 202 to 210 us, 5.4 TB/s; one of 32000 keys
-// and 60 tokens 38; 32 of 4000 keys 116, where one CTA with two row tiles (no room for a second S
-// buffer, a ring of two and a half tiles) took 2.0 us per tile.  One issuing warp for S and PV and two
-// buffers of S: 212, 40 and 122 us; alternate tiles for the two softmax warpgroups: 10 % slower.
+// A key tile is 4 x 256 x 128 x 128 FLOP, 1040 cycles of UMMAs, and takes 0.73 us to read; it takes
+// 0.75 to 0.8.  32 sequences of 8128 keys and 64 tokens (1.1 GB, 275 GFLOP): 190 to 198 us, 5.7 TB/s;
+// 32 of 4000 keys 108; one of 32000 keys and 60 tokens 35; 18 of up to 2105 and 103 tokens 58, where a
+// unit's begin and end (tail of the last PV, O, stores, the first softmax) cost as much as its tiles.
+// Measured against: two row tiles in one CTA (no room for a second S buffer, a ring of two and a half
+// tiles) 2.0 us per tile; one issuing warp for S and PV, two buffers of S and two softmax threads per row
+// in step with each other 212, 122, 40 and 80 us for the same cases, with the issuers and buffers of
+// today 208, 117 and 38.  Rings of 3, 4 and 6 stages: 5, 1 and 3 % slower than 5 for the first.
 //
 // TMEM columns (each CTA, its own rows): S_0/P_0, S_1/P_1, S_2/P_2 at 0, 128, 256, O at 384.
 #pragma once
@@ -33,8 +35,7 @@ namespace gqa {
 
 struct CachePairBars {
   static constexpr int kStages = 5;     // each of K and V
-  static constexpr int kV = kStages;
-  static constexpr int kS = 3, kO = 1;  // buffers of S and O
+  static constexpr int kS = 3;          // buffers of S
   static constexpr int kRing = 6 + 2 * kS;
   static constexpr int kCount = kRing + 5 * kStages;
   static constexpr int kBytes = 384;
@@ -47,10 +48,10 @@ struct CachePairBars {
   __device__ __forceinline__ uint64_t* v_ready(int i) const { return bars + kRing + kStages + i; }
   // CTA 0's: an arrival of every softmax warp of both CTAs that has written its part of P, or read O
   __device__ __forceinline__ uint64_t* p_full(int i) const { return bars + 6 + i; }
-  __device__ __forceinline__ uint64_t* o_empty(int) const { return bars + 1; }
+  __device__ __forceinline__ uint64_t* o_empty() const { return bars + 1; }
   // each CTA's own
   __device__ __forceinline__ uint64_t* q_empty() const { return bars + 2; }
-  __device__ __forceinline__ uint64_t* o_full(int) const { return bars + 3; }
+  __device__ __forceinline__ uint64_t* o_full() const { return bars + 3; }
   __device__ __forceinline__ uint64_t* drain(int i) const { return bars + 4 + i; }
   __device__ __forceinline__ uint64_t* s_full(int i) const { return bars + 6 + kS + i; }
   __device__ __forceinline__ uint64_t* k_empty(int i) const { return bars + kRing + 2 * kStages + i; }
@@ -229,7 +230,7 @@ __device__ __forceinline__ void softmax_in_turn(const CacheAttnParams& p, const 
     it += w.n;
     // ---------------------------------------------------------------- end of a piece
     // one decision of the two warps, with or without live rows, whether a wait was given up
-    ok = ok && wait(bar.o_full(0), piece & 1);
+    ok = ok && wait(bar.o_full(), piece & 1);
     if (!named_bar_and(bar_id, 64, ok)) break;
     if (!warp_live) {
       if (lane == 0) arrive_o();
@@ -479,7 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         bool ok = true;
         for (; ok && !w.done(); next(w), ++piece) {
           // the piece's O takes the place of the piece's before
-          if (piece > 0 && !(ok = wait(bar.o_empty(0), (piece - 1) & 1))) break;
+          if (piece > 0 && !(ok = wait(bar.o_empty(), (piece - 1) & 1))) break;
           for (int j = 0; j < w.n; ++j) {
             const bool there = cleared(w, w.first + j) ? wait_cluster(bar.v_ready(v.i), v.parity) : wait(bar.v_ready(v.i), v.parity);
             if (!(ok = there && wait(bar.p_full(s.i), s.parity))) break;
@@ -491,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                 umma_ts_pair(tmem_base + kS * 128, tmem_base + s.i * 128 + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv,
                              j + kk != 0);
               umma_commit_pair(bar.v_empty(v.i), 0x3);
-              if (j == w.n - 1) umma_commit_pair(bar.o_full(0), 0x3);
+              if (j == w.n - 1) umma_commit_pair(bar.o_full(), 0x3);
             }
             __syncwarp();
             v.next();
@@ -506,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     softmax_in_turn(
         p, ranges, bar, tmem_base, reinterpret_cast<float*>(smem + L::kExchange), rank, worker,
         [&](int slot) { mbar_arrive_remote(cta0(bar.p_full(slot))); },
-        [&] { mbar_arrive_remote(cta0(bar.o_empty(0))); });
+        [&] { mbar_arrive_remote(cta0(bar.o_empty())); });
   }
 
   tc_fence_before();

@@ -45,8 +45,6 @@ constexpr int kKStages = 2;
 constexpr int kVStages = 3;
 
 struct CacheBars {
-  static constexpr int kV = kVStages;      // V stages
-  static constexpr int kS = 2, kO = 2;     // buffers of S and O
   static constexpr int kCount = 28;
   static constexpr int kBytes = 256;  // barriers, TMEM address, abort flag
   uint64_t* bars;
