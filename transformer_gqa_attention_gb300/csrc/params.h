@@ -88,9 +88,9 @@ struct DecodeParams {
 };
 
 // At most this many positions run on one 128-row tile (positions x 4 heads), more on the two tiles of a
-// CTA pair, which a few positions leave half empty: at T = 8, 26 and 32, us, 8 sequences of 4000 keys
-// take 31, 35 and 35 on one tile, 37, 40 and 41 on a pair; 32 sequences 88, 92, 95 and 103, 114, 116; one
-// of 300 10.7, 12.6, 12.5 and 12.4, 13.3, 13.6.
+// CTA pair, which a few positions leave half empty: at T = 8, 26 and 32, us, 32 sequences of 4000 keys take
+// 89, 92, 95 on one tile and 95, 99, 101 on a pair; 8 of 4000 30.9, 34.9, 35.3 and 34.1, 35.7, 36.2; one of 8000
+// 16.3, 18.2, 18.7 and 16.4, 17.6, 18.0; one of 300 10.1, 11.8, 12.1 and 10.9, 11.8, 12.0.
 constexpr int kOneTilePos = 32;
 
 // Attention of a few positions per sequence over caches of per-sequence length (tree attention,
