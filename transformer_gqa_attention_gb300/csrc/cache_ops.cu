@@ -139,7 +139,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   const int mid0 = p.n_first, mid1 = len - p.n_recent;  // the heaviest of these stay
   const bool staged = per <= kSelChunk;
   auto load_chunk = [&](int s0) {
-    for (int i = tid; i < min(kSelChunk, hi - s0); i += kSelThreads) stage[i] = __ldcg(w + s0 + i);
+    float v[kSelEach];  // (without conditions, so that all are in flight together)
+#pragma unroll
+    for (int q = 0; q < kSelEach; ++q) v[q] = __ldcg(w + min(s0 + q * kSelThreads + tid, hi - 1));
+#pragma unroll
+    for (int q = 0; q < kSelEach; ++q) stage[q * kSelThreads + tid] = v[q];
     __syncthreads();
   };
   auto sync_all = [&] {
