@@ -40,9 +40,6 @@ struct GemmParams {
   void* out2;        // kQkvRope: cache_v
   const float* R;    // Q/K/V epilogues: [T,64,2] (with seq_start: [tokens,64,2])
   int T, S_max, start_pos;
-  // Q/K/V epilogues: first position of each sequence [B] (device), read in place of start_pos; a
-  // sequence whose T positions do not fit the cache is not written.  Null: start_pos for all.
-  const int* seq_start;
   int ldo;           // kStoreF32: row stride (floats)
   void* fin0;        // split-K final outputs: Q_r [N,q_cols] bf16 | Delta [N,4096] fp32
   void* fin1;        // kSplitKQkv: cache_k
@@ -52,6 +49,9 @@ struct GemmParams {
   // residual form of the block (both null for the block alone)
   const float* row_scale;  // Q/K/V epilogues: 1 / rms of each token row (attention_norm)
   const void* residual;    // Delta epilogues: x [tokens, 4096] bf16, added to Delta
+  // Q/K/V epilogues: first position of each sequence [B] (device), read in place of start_pos; a
+  // sequence whose T positions do not fit the cache is not written.  Null: start_pos for all.
+  const int* seq_start;
 };
 
 struct FlashParams {
