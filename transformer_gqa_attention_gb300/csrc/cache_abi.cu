@@ -21,36 +21,39 @@ namespace {
 // What a call keeps in the context's scratch, in bytes from its start.
 struct CacheLayout {
   bool pair;
-  int group_pos, row_groups, part_rows;
-  size_t workers;
+  int group_pos, row_groups, unit_cost, part_rows, n_ctas;
+  size_t tiles, workers;  // tiles: at most
   size_t merge, part_ml, part_o, total_tiles, scores, tile_unit, unit_ml, bytes;
 };
 
 CacheLayout cache_layout(const gqa_ctx* c, const CacheAttnCall& a) {
   CacheLayout l{};
-  const int n_ctas = c->num_sms & ~1;  // persistent, one per SM (the GPU's 152: even)
   l.pair = a.T > kOneTilePos;
   l.group_pos = l.pair ? 64 : kOneTilePos;
   l.row_groups = (a.T + l.group_pos - 1) / l.group_pos;
+  l.unit_cost = a.weights ? kUnitCostDecode : l.pair ? kUnitCostPair : kUnitCostTile;
   l.part_rows = static_cast<int>(round_up(4 * std::min(a.T, l.group_pos), 32));
   auto take = [&](size_t bytes) {
     const size_t at = l.bytes;
     l.bytes = round_up(l.bytes + bytes, 256);
     return at;
   };
+  // persistent CTAs, one per SM (the GPU's 152: even), or as many as the caches have places for
+  const size_t units = static_cast<size_t>(a.B) * c->n_kv * l.row_groups;
+  l.tiles = units * ((a.S_max + kKvTile - 1) / kKvTile);
+  const size_t places = l.tiles + units * l.unit_cost, ctas = c->num_sms & ~1;
+  l.n_ctas = static_cast<int>(std::min(ctas, a.weights ? (places + 1) / 2 : l.pair ? 2 * places : places));
   // workers: CTAs, with weights their two softmax slots, with many positions CTA pairs; each may hold
   // two partial results
-  l.workers = a.weights ? 2 * n_ctas : l.pair ? n_ctas / 2 : n_ctas;
+  l.workers = a.weights ? 2 * l.n_ctas : l.pair ? l.n_ctas / 2 : l.n_ctas;
   const size_t slots = 2 * l.workers;
   l.merge = take(l.workers * sizeof(int4));
   l.part_ml = take(slots * l.part_rows * sizeof(float2));
   l.part_o = take(slots * l.part_rows * 128 * sizeof(float));
   if (a.weights) {
-    const size_t units = static_cast<size_t>(a.B) * c->n_kv;
-    const size_t tiles = units * ((a.S_max + kKvTile - 1) / kKvTile);
     l.total_tiles = take(sizeof(int));
-    l.scores = take(tiles * 4 * kKvTile * sizeof(float));
-    l.tile_unit = take(tiles * sizeof(int4));
+    l.scores = take(l.tiles * 4 * kKvTile * sizeof(float));
+    l.tile_unit = take(l.tiles * sizeof(int4));
     l.unit_ml = take(units * 4 * sizeof(float2));
   }
   return l;
@@ -82,7 +85,7 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   p.scale_log2 = kScaleLog2;
   p.group_pos = l.group_pos;
   p.row_groups = l.row_groups;
-  p.unit_cost = a.weights ? kUnitCostDecode : l.pair ? kUnitCostPair : kUnitCostTile;
+  p.unit_cost = l.unit_cost;
   p.part_rows = l.part_rows;
   p.merge = reinterpret_cast<int4*>(ws + l.merge);
   p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
@@ -106,11 +109,14 @@ gqa_status gqa::run_cache_attn(gqa_ctx* c, const CacheAttnCall& a, cudaStream_t 
   p.fault = take_fault(c, GQA_KERNEL_CACHE_ATTN);
   {
     ProfScope ps(c, GQA_KERNEL_CACHE_ATTN, s);
-    GQA_CUDA(launch_cache_attn(tq, tk, tv, p, c->num_sms & ~1, s));
+    GQA_CUDA(launch_cache_attn(tq, tk, tv, p, l.n_ctas, s));
   }
   if (a.weights) {
     ProfScope ps(c, GQA_KERNEL_CACHE_WEIGHTS, s);
-    GQA_CUDA(launch_cache_weights(p, static_cast<int>(l.workers), 8 * c->num_sms, s));
+    // a warp per tile, at most four blocks per SM (two: 7 us more for 64 sequences of 8192 keys; eight: 1 us more
+    // for one of 700)
+    const int blocks = static_cast<int>(std::min<size_t>(4 * c->num_sms, (l.tiles + 7) / 8));
+    GQA_CUDA(launch_cache_weights(p, static_cast<int>(l.workers), blocks, s));
   } else {
     ProfScope ps(c, GQA_KERNEL_CACHE_MERGE, s);
     GQA_CUDA(launch_cache_merge(p, static_cast<int>(l.workers), s));

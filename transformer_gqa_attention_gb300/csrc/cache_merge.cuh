@@ -79,8 +79,6 @@ __device__ __forceinline__ uint2 pack4(float4 v, float f) {
   return make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
 }
 
-constexpr int kMergeY = 8;  // blocks per worker
-
 // Joins the pieces of the unit that goes on past worker v's range, described by d.  A unit of n
 // pieces goes on past n - 1 workers, whose blocks share it: of theirs, this is block i of `blocks`.
 // A task is N rows x 128 columns with kByRow, else 32 rows x 16 columns (N = 4); ks of a block's
