@@ -6,7 +6,7 @@
 // positions: 4 T rows do 4 T x 128 x 4 FLOP per key of 512 bytes, far below what the tensor cores could
 // do, so reading the keys and values bounds it: 32 sequences of 4000 keys (528 MB) take 88 us with 8
 // tokens (6.0 TB/s) and 95 with 32, with the merge; 8 ragged ones of up to 4000 keys and 26 tokens (73 MB)
-// 25, of which the merge is 4 and a CTA's first tile 5; one of 300 keys and 8 tokens 10.2, all latency.
+// 23.5, of which the merge is 3 and a CTA's first tile 5; one of 300 keys and 8 tokens 9.1, all latency.
 // Keys on the tensor core's rows, as the decode step has them (cache_decode.cuh): 106 us for 8 tokens
 // where this takes 87.
 //   S = Q K^T into TMEM, softmax, P over S in TMEM, O += P V.

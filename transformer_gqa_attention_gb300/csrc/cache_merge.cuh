@@ -4,15 +4,15 @@
 // Merge: pieces k of a unit give O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k with M = max_k m_k.
 // The lengths are on the device, so which units are cut is too, and the launch is made in any case.
 // At most two pieces a worker, 20 MB in all: bound by latency (launch, the record, the pieces in L2),
-// 4 us behind the attention of 8 ragged sequences and 26 tokens, 2 where nothing was cut.  The
+// 3 us behind the attention of 8 ragged sequences and 26 tokens, 2 where nothing was cut.  The
 // workers' blocks share a unit by rows and columns, and a block's warps its pieces where these are many,
 // added up in a fixed order: results do not depend on which block is first.
 //
 // Weights: w[s] += sum over the four heads of 2^(c s - M) / l, from the scores that the attention left
 // behind.  They can only be had once M and l are known, so the scores make a trip through memory: 64
 // sequences of 8192 keys write and read 67 MB, most of it in L2 as the cache leaves it first, and update
-// 17 MB of sums in 22 us behind 338 us of attention.  Blocks of 256 threads at four per SM (27 us with
-// as many registers as it likes).
+// 17 MB of sums in 22 us behind 338 us of attention.  Blocks of 256 threads, four per SM (27 us with
+// as many registers as it likes, 29 with two blocks).
 #pragma once
 
 #include <type_traits>
