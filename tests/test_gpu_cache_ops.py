@@ -179,6 +179,13 @@ def test_tree_attention_with_more_units_than_ctas(T):
     run_tree(94, [(53 * b) % 700 for b in range(40)], T)
 
 
+@pytest.mark.parametrize("T", [20, 40, 103])
+def test_tree_attention_of_many_short_units_with_rising_scores(T):
+    # units of one to six tiles, several to a worker, whose maximum grows from tile to tile
+    lens = [int(n) for n in np.random.default_rng(T).integers(0, 700, 30)]
+    run_tree(15 + T, lens, T, ramp=2.0)
+
+
 def test_causal_chain_equals_the_prefill_mask():
     # a chain (every token sees all before it) is a causal prefill of T positions
     T, L = 24, 200
