@@ -180,7 +180,6 @@ __global__ void __launch_bounds__(384, 1)
             }
             tmem_st16(t_o, o);
             tmem_st_wait();
-            tc_fence_before();
           }
         }
         const float4 m4 = *reinterpret_cast<const float4*>(mu);
@@ -191,6 +190,8 @@ __global__ void __launch_bounds__(384, 1)
         // P as bf16 for the tensor product (the sum stays fp32)
         *reinterpret_cast<uint2*>(P) = make_uint2(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]));
         fence_proxy_async_smem();
+        // this arrival lets the issuer write the next tile's scores over the ones read above, and add to O
+        tc_fence_before();
         mbar_arrive(bar.p_lo(slot));
       }
       // ---------------------------------------------------------------- end of a piece
