@@ -1,6 +1,8 @@
 """Order between the warps of the cache attention kernels (GPU): workers with many tiles whose
 maximum stays, so that nothing but the hand-over of a tile separates its readers from the next
-tile's writers.  Results are held to float64 and to the same bits from call to call."""
+tile's writers; and tiles of drafted positions that every row sees, none of whose values is cleared
+before CTA 0 of a pair is told that the other's half is there.  Results are held to float64 and to the
+same bits from call to call."""
 import numpy as np
 import pytest
 import torch
@@ -71,3 +73,22 @@ def test_counted_decode_of_many_tiles_whose_maximum_stays(ctx, B, length):
     d = check_h(gu.np64(h[0, some]).reshape(ref.shape), ref, av, mag)
     # a weight: its score's error and a handful of fp32 roundings of sums of positive numbers
     assert (np.abs(gu.np64(w[0, some]) - wr) <= (d + 2.0 ** -20) * wr + 1e-30).all()
+
+
+@pytest.mark.parametrize("T,lens", [(40, [88, 216, 1112]), (64, [64, 0, 192, 4032]), (128, [0, 128, 896]),
+                                    (200, [56, 312]), (256, [0, 128, 2048])])
+def test_tree_of_a_pair_whose_last_tiles_are_seen_by_every_row(ctx, T, lens):
+    B, S = len(lens), max(lens) + T
+    assert any((n + T) % 128 == 0 for n in lens)
+    k, v, q = draw(4, B, S, 8, 128), draw(5, B, S, 8, 128), draw(6, B, T, 4096)
+    vis = np.ones((B, T, T), dtype=bool)
+    mask = torch.from_numpy(co.mask_words(vis)).to(DEV)
+    kd, vd, qd = k.to(DEV), v.to(DEV), q.to(DEV)
+    h = torch.full((CALLS, B, T, 4096), float("nan"), dtype=torch.bfloat16, device=DEV)
+    for i in range(CALLS):
+        abi.attn_tree_attention(ctx, qd, B, T, mask, kd, vd, S, ints(lens), h[i])
+    abi.attn_sync_status(ctx)
+    for i in range(1, CALLS):
+        assert torch.equal(h[i].view(torch.int16), h[0].view(torch.int16)), i
+    ref, av, _, mag = co.cache_attention(gu.np64(q).reshape(B, T, 8, 4, 128), gu.np64(k), gu.np64(v), lens, vis, T)
+    check_h(gu.np64(h[0]).reshape(ref.shape), ref, av, mag)

@@ -456,17 +456,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           const bool any = clear.rows<8>(p, l, [&](int r, int c) {
             return smem + L::kV + vs * L::kStage + r * 128 + c * 16;  // this CTA's 64 columns
           });
-          // rows cleared here are read by the pair's UMMAs: ordered at cluster scope
           if (any) {
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (lane == 0) {
-            if (any)
-              mbar_arrive_cluster(cta0(bar.v_ready(vs)));
-            else
-              mbar_arrive_remote(cta0(bar.v_ready(vs)));
-          }
+          // this CTA's half of V, as it landed or as cleared here, is read by products that CTA 0 issues: ordered
+          // at cluster scope in either case
+          if (lane == 0) mbar_arrive_cluster(cta0(bar.v_ready(vs)));
         }
       }
     } else if (warp == 3) {
