@@ -114,3 +114,33 @@ def test_counted_decode_reads_the_rotations_behind_the_kernel_that_writes_them(b
         return out, k, v, w
 
     check(blk, B, 2, call)
+
+
+@pytest.mark.parametrize("B,T", [(1, 1), (2, 16), (1, 60), (4, 16), (1, 100), (2, 300)])
+def test_prefill_reads_the_rotations_behind_the_kernel_that_writes_them(blk, B, T):
+    S = T + 3
+    bufs = [[(x, k.clone(), v.clone(), torch.empty(B, T, 4096, device=DEV)) for x, k, v in buffers(30, B, T, S)]
+            for _ in range(2)]
+    turn = iter(range(2 * STEPS))
+
+    def call(step, R):
+        x, k, v, out = bufs[next(turn) // STEPS][step]
+        abi.attn_prefill(blk.ctx, x, B, T, R, True, k, v, S, 2, out)
+        return out, k, v
+
+    check(blk, T, 3, call)
+
+
+@pytest.mark.parametrize("B", [1, 40, 80])
+def test_decode_reads_the_rotation_behind_the_kernel_that_writes_it(blk, B):
+    S = 90
+    bufs = [[(x, k.clone(), v.clone(), torch.empty(B, 1, 4096, device=DEV)) for x, k, v in buffers(40, B, 1, S)]
+            for _ in range(2)]
+    turn = iter(range(2 * STEPS))
+
+    def call(step, R):
+        x, k, v, out = bufs[next(turn) // STEPS][step]
+        abi.attn_decode(blk.ctx, x, B, 80, R, k, v, S, out)
+        return out, k, v
+
+    check(blk, 1, 4, call)

@@ -114,8 +114,8 @@ __device__ __forceinline__ void load_rope(const GemmParams& p, const QkvRows& q,
   for (int k = 0; k < 4; ++k) {
     const float4* rp = reinterpret_cast<const float4*>(
         p.R + (static_cast<size_t>(kSeq ? min(q.m[k], p.M - 1) : q.t[k]) * 64 + j0) * 2);
-    cs[k][0] = kSeq ? ld_behind_wait(rp) : __ldg(rp);
-    cs[k][1] = kSeq ? ld_behind_wait(rp + 1) : __ldg(rp + 1);
+    cs[k][0] = ld_behind_wait(rp);
+    cs[k][1] = ld_behind_wait(rp + 1);
   }
 }
 
@@ -371,8 +371,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     const int quarter = warp & 3;  // TMEM lanes 32*quarter .. +31
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     float* stage = reinterpret_cast<float*>(smem + L::kEpiOffset) + (warp - 2) * kEpiWarpFloats;
-    // a row of R per token is a step's own data: the kernel before this one may write it
-    if constexpr (EPI == kQkvRopeSeq) griddep_wait();
+    // R may be written by the kernel before this one
+    if constexpr (EPI == kQkvRope || EPI == kQkvRopeSeq) griddep_wait();
     int lt = 0;
     int mt, n0, w;
     for (; pair_item(p, pair, n_pairs, lt, mt, n0, w); ++lt) {
@@ -612,8 +612,7 @@ __global__ void __launch_bounds__(192, (STAGES <= 5 ? 2 : 1))
     if constexpr (EPI == kSplitKQkv || EPI == kSplitKQkvSeq) {
       const int m = m0 + 4 * lane;  // pairs (m & 127) / 2 and the next one
       const bool rope = m < p.q_cols + p.kv_cols;
-      // a row of R per token is a step's own data: the kernel before this one may write it
-      if constexpr (EPI == kSplitKQkvSeq) griddep_wait();
+      griddep_wait();  // R may be written by the kernel before this one
 #pragma unroll
       for (int j = 0; j < kTokPerWarp; ++j) {
         const int tok = t_lo + (warp - 2) + 4 * j;
@@ -621,7 +620,7 @@ __global__ void __launch_bounds__(192, (STAGES <= 5 ? 2 : 1))
         if (rope && tok < t_hi) {
           const int t = EPI == kSplitKQkvSeq ? tok : tok - (tok / p.T) * p.T;
           const float4* r = reinterpret_cast<const float4*>(p.R + (static_cast<size_t>(t) * 64 + ((m & 127) >> 1)) * 2);
-          cs[j] = EPI == kSplitKQkvSeq ? ld_behind_wait(r) : __ldg(r);
+          cs[j] = ld_behind_wait(r);
         }
       }
     }

@@ -58,12 +58,12 @@ __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wa
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-// Loads of what an earlier kernel on the stream may have written, for use behind griddep_wait().  As
-// volatile asm they stay behind it (__ldg promises the compiler that nothing writes the data while this
-// kernel lives, which such a kernel may still do); from L2, as a line of this SM's L1 may be older.
+// Loads of what an earlier kernel on the stream may have written, for use behind griddep_wait(), which
+// makes that visible to them.  As volatile asm they stay behind it: __ldg promises the compiler that nothing
+// writes the data while this kernel lives, which such a kernel may still do.
 __device__ __forceinline__ float4 ld_behind_wait(const float4* p) {
   float4 v;
-  asm volatile("ld.global.cg.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
   return v;
 }
 
