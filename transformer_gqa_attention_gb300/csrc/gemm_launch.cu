@@ -42,7 +42,6 @@ int gemm_pair_max_clusters() {
 
 cudaError_t launch_gemm_qkv_rope(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& bt,
                                  const GemmParams& p, int grid, cudaStream_t s) {
-  if (p.seq_start) return launch_gemm_qkv_rope_seq(a, b, bt, p, grid, s);
   return launch_pdl(gemm_tc_pair_kernel<6, kQkvRope>, dim3(grid), dim3(192), PairSmem::kBytes, s, 0, a, b, bt, p);
 }
 
@@ -55,7 +54,7 @@ int splitk_token_tile(int n_tok) { return n_tok <= 32 ? 32 : 64; }
 
 cudaError_t launch_gemm_splitk_qkv(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
                                    cudaStream_t s) {
-  return p.seq_start ? launch_gemm_splitk_qkv_seq(a, b, p, s) : launch_splitk<kSplitKQkv>(a, b, p, s);
+  return launch_splitk<kSplitKQkv>(a, b, p, s);
 }
 
 cudaError_t launch_gemm_splitk_out(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,

@@ -19,17 +19,13 @@ constexpr int kDeepStages = 8;
 using DeepSmem = GemmSmem<64, kDeepStages>;
 
 cudaError_t configure_gemm_seq_kernels();
-cudaError_t launch_gemm_qkv_rope_seq(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& bt,
-                                     const GemmParams& p, int grid, cudaStream_t s);
-cudaError_t launch_gemm_splitk_qkv_seq(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
-                                       cudaStream_t s);
 
 // One cluster of p.splits CTAs per 128-feature tile (cluster rank = k split).
 // The activation map's box must be splitk_token_tile(p.N) rows.
 // Ring per case: at most 32 tokens, the 5-stage 32-column ring; 33-64 tokens, the 4-stage
 // 64-column ring for Q/K/V and the 8-stage one (one CTA per SM) for W_O.
 template <int EPI>
-static cudaError_t launch_splitk(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p, cudaStream_t s) {
+static cudaError_t launch_splitk(const CUtensorMap& a, const CUtensorMap& b, const EpiParams<EPI>& p, cudaStream_t s) {
   // the reduction serves 2..8 splits (cluster sizes) of at most 64 tokens
   if (p.splits < 2 || p.splits > 8 || p.N < 1 || p.N > 64) return cudaErrorInvalidValue;
   const dim3 grid(p.m_tiles * p.splits);

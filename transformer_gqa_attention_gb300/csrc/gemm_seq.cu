@@ -1,5 +1,5 @@
 // gemm_seq.cu — the Q/K/V projections whose sequences have their own starts in the cache
-// (GemmParams::seq_start).  A translation unit of their own: beside them in gemm_launch.cu the other
+// (GemmSeqParams::seq_start).  A translation unit of their own: beside them in gemm_launch.cu the other
 // instantiations start 0.2 to 0.5 us later in steps of 32 to 139 us.
 #include "gemm_rings.cuh"
 
@@ -17,11 +17,11 @@ cudaError_t configure_gemm_seq_kernels() {
 }
 
 cudaError_t launch_gemm_qkv_rope_seq(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& bt,
-                                     const GemmParams& p, int grid, cudaStream_t s) {
+                                     const GemmSeqParams& p, int grid, cudaStream_t s) {
   return launch_pdl(gemm_tc_pair_kernel<6, kQkvRopeSeq>, dim3(grid), dim3(192), PairSmem::kBytes, s, 0, a, b, bt, p);
 }
 
-cudaError_t launch_gemm_splitk_qkv_seq(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
+cudaError_t launch_gemm_splitk_qkv_seq(const CUtensorMap& a, const CUtensorMap& b, const GemmSeqParams& p,
                                        cudaStream_t s) {
   return launch_splitk<kSplitKQkvSeq>(a, b, p, s);
 }

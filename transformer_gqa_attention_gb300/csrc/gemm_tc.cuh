@@ -28,7 +28,7 @@
 //   kStoreF32 — Delta = H W_O^T (step 14) stored fp32 row-major.
 //   kSplitKQkv / kSplitKOut — the same two epilogues for the few-token kernel.
 //   kQkvRopeSeq / kSplitKQkvSeq — kQkvRope / kSplitKQkv where every sequence has its own start in the
-//               cache (GemmParams::seq_start) and R has a row per token.
+//               cache (GemmSeqParams::seq_start) and R has a row per token.
 #pragma once
 
 #include "pair_sched.h"
@@ -99,7 +99,7 @@ __device__ __forceinline__ void qkv_row_scales(const GemmParams& p, QkvRows& q) 
 // Cache position of position t of sequence b, or -1: a sequence whose p.T positions do not fit the
 // cache is not written.  The starts may come from the previous kernel: read, like the row scales,
 // after the accumulator wait (or behind the reduction, which follows it).
-__device__ __forceinline__ int seq_position(const GemmParams& p, int b, int t) {
+__device__ __forceinline__ int seq_position(const GemmSeqParams& p, int b, int t) {
   const int start = __ldcg(p.seq_start + b);
   return start >= 0 && start <= p.S_max - p.T ? start + t : -1;
 }
@@ -223,7 +223,7 @@ struct GemmPairSmem {
 template <int STAGES, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                        const __grid_constant__ CUtensorMap tmBt, const GemmParams p) {
+                        const __grid_constant__ CUtensorMap tmBt, const EpiParams<EPI> p) {
   using L = GemmPairSmem<STAGES>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -488,7 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
 template <int EPI, int STAGES, int BN>
 __global__ void __launch_bounds__(192, (STAGES <= 5 ? 2 : 1))
     gemm_splitk_cluster_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                               const GemmParams p) {
+                               const EpiParams<EPI> p) {
   static_assert(BN == 32 || BN == 64, "token tile of 32 or 64");
   using L = GemmSmem<BN, STAGES>;
   // after the main loop the stage buffers hold this CTA's partial tile, token-major

@@ -146,7 +146,7 @@ WsLayout ws_layout(long long n_tok, int n_kv, const SkinnyPlan* sk, const Decode
 gqa_status run_qkv(gqa_ctx* c, const void* x, int n_tok, int T, const float* R, void* ck, void* cv,
                    int S_max, int start_pos, const int* seq_start, void* q_out, const WsLayout& w, const SkinnyPlan* sk,
                    const float* row_scale, cudaStream_t s) {
-  GemmParams p{};
+  GemmSeqParams p{};
   // residual form: the folded weights, each token row scaled by its 1 / rms
   const __nv_bfloat16* wqkv = row_scale ? c->w_qkv_norm : c->w_qkv;
   p.row_scale = row_scale;
@@ -173,7 +173,10 @@ gqa_status run_qkv(gqa_ctx* c, const void* x, int n_tok, int T, const float* R, 
     p.fin2 = cv;
     p.R = R;
     p.fault = take_fault(c, GQA_KERNEL_QKV_SPLITK);
-    { ProfScope ps(c, GQA_KERNEL_QKV_SPLITK, s); GQA_CUDA(launch_gemm_splitk_qkv(ta, tb, p, s)); }
+    {
+      ProfScope ps(c, GQA_KERNEL_QKV_SPLITK, s);
+      GQA_CUDA(seq_start ? launch_gemm_splitk_qkv_seq(ta, tb, p, s) : launch_gemm_splitk_qkv(ta, tb, p, s));
+    }
   } else {
     // CTA pairs, 256x256 tiles: each CTA loads 128-row boxes of x and of W_QKV
     if (!map_rows(&ta, x, n_tok, 4096, 128) || !map_weight_tiled(&tb, wqkv, rows, 64, 128))
@@ -191,7 +194,11 @@ gqa_status run_qkv(gqa_ctx* c, const void* x, int n_tok, int T, const float* R, 
     CUtensorMap tbt = tb;  // boxes of tail_w / 2 rows for the pieces of a partial last round
     if (p.tail_w && !map_weight_tiled(&tbt, wqkv, rows, 64, p.tail_w / 2)) return cuda_fail(cudaErrorInvalidValue);
     p.fault = take_fault(c, GQA_KERNEL_QKV_GEMM);
-    { ProfScope ps(c, GQA_KERNEL_QKV_GEMM, s); GQA_CUDA(launch_gemm_qkv_rope(ta, tb, tbt, p, grid, s)); }
+    {
+      ProfScope ps(c, GQA_KERNEL_QKV_GEMM, s);
+      GQA_CUDA(seq_start ? launch_gemm_qkv_rope_seq(ta, tb, tbt, p, grid, s)
+                         : launch_gemm_qkv_rope(ta, tb, tbt, p, grid, s));
+    }
   }
   return GQA_OK;
 }

@@ -63,6 +63,11 @@ cudaError_t launch_gemm_splitk_qkv(const CUtensorMap& a, const CUtensorMap& b, c
                                    cudaStream_t s);
 cudaError_t launch_gemm_splitk_out(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
                                    cudaStream_t s);
+// The two Q/K/V ones with a start in the cache for every sequence.
+cudaError_t launch_gemm_qkv_rope_seq(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& bt,
+                                     const GemmSeqParams& p, int grid, cudaStream_t s);
+cudaError_t launch_gemm_splitk_qkv_seq(const CUtensorMap& a, const CUtensorMap& b, const GemmSeqParams& p,
+                                       cudaStream_t s);
 
 cudaError_t launch_flash_prefill(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                                  const CUtensorMap& h, const FlashParams& p, dim3 grid, cudaStream_t s);
