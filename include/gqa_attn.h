@@ -383,14 +383,22 @@ enum {
  * attn_profile_begin — from now on, every kernel this context launches is bracketed by
  * two CUDA events recorded on the launch stream (up to 65536 launches).  Recording adds
  * two event records per launch and nothing else.
- * attn_profile_end — stop recording, synchronise `stream`, and write, per kernel kind,
- * the summed device time in milliseconds (ms_per_kind[GQA_KERNEL_KINDS]) and the number
- * of launches (launches_per_kind[GQA_KERNEL_KINDS]) since attn_profile_begin.  Either
- * output may be NULL.  Errors: GQA_ERR_INVALID_ARG (null context), GQA_ERR_CUDA.
+ * attn_profile_end_kinds — stop recording, synchronise `stream`, and write, for the first
+ * n_kinds kernel kinds, the summed device time in milliseconds (ms_per_kind[n_kinds]) and the
+ * number of launches (launches_per_kind[n_kinds]) since attn_profile_begin; 0 for kinds that
+ * this library does not have.  Either output may be NULL.  Errors: GQA_ERR_INVALID_ARG (null
+ * context, n_kinds < 0), GQA_ERR_CUDA.
+ * attn_profile_end — the same for all GQA_KERNEL_KINDS kinds of the header that a program is
+ * built with.  The library's function of that name writes the first seven kinds, which is what
+ * the arrays of programs built before there were more hold.
  */
 gqa_status attn_profile_begin(gqa_ctx *ctx);
+gqa_status attn_profile_end_kinds(gqa_ctx *ctx, double *ms_per_kind, int *launches_per_kind, int n_kinds,
+                                  gqa_stream_t stream);
 gqa_status attn_profile_end(gqa_ctx *ctx, double *ms_per_kind, int *launches_per_kind,
                             gqa_stream_t stream);
+#define attn_profile_end(ctx, ms_per_kind, launches_per_kind, stream) \
+    attn_profile_end_kinds(ctx, ms_per_kind, launches_per_kind, GQA_KERNEL_KINDS, stream)
 
 /*
  * attn_decode_attention_noalloc — the decode attention of attn_decode (key/value head

@@ -19,7 +19,7 @@ STATUS_NAMES = {0: "GQA_OK", 1: "GQA_ERR_INVALID_ARG", 2: "GQA_ERR_SHAPE", 3: "G
 # Every symbol include/gqa_attn.h declares.
 EXPORTED = ("attn_create", "attn_create_shard", "attn_prefill", "attn_decode", "attn_set_norm", "attn_prefill_residual",
             "attn_decode_residual", "attn_sync_status", "attn_debug_buffers",
-            "attn_profile_begin", "attn_profile_end", "attn_debug_inject_timeout",
+            "attn_profile_begin", "attn_profile_end", "attn_profile_end_kinds", "attn_debug_inject_timeout",
             "attn_debug_pair_schedule", "attn_debug_exp2", "attn_decode_attention_noalloc",
             "attn_decode_attention_noalloc_status", "attn_decode_attention_noalloc_debug_inject_timeout",
            "attn_tree_attention", "attn_prefill_tree", "attn_prefill_tree_residual", "attn_cache_commit",
@@ -27,7 +27,7 @@ EXPORTED = ("attn_create", "attn_create_shard", "attn_prefill", "attn_decode", "
            "attn_cache_evict", "attn_debug_cache_schedule",
             "attn_destroy", "attn_strerror", "attn_last_cuda_error")
 
-# Kernel kinds of attn_profile_end (GQA_KERNEL_* in include/gqa_attn.h).
+# Kernel kinds of attn_profile_end_kinds (GQA_KERNEL_* in include/gqa_attn.h).
 KERNEL_KINDS = ("qkv_gemm", "qkv_splitk", "flash_prefill", "decode_attn", "out_gemm", "out_splitk",
                 "rms_norm", "cache_attn", "cache_merge", "cache_weights", "cache_commit", "evict_select", "evict_move")
 
@@ -76,6 +76,8 @@ def lib() -> ctypes.CDLL:
     L.attn_profile_begin.restype = i32
     L.attn_profile_end.argtypes = [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i32), vp]
     L.attn_profile_end.restype = i32
+    L.attn_profile_end_kinds.argtypes = [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i32), i32, vp]
+    L.attn_profile_end_kinds.restype = i32
     L.attn_debug_inject_timeout.argtypes = [vp, i32]
     L.attn_debug_inject_timeout.restype = i32
     ip = ctypes.POINTER(i32)
@@ -204,7 +206,7 @@ def attn_profile_end(ctx, stream=None):
     n = len(KERNEL_KINDS)
     ms = (ctypes.c_double * n)()
     cnt = (ctypes.c_int * n)()
-    _check("attn_profile_end", lib().attn_profile_end(ctx, ms, cnt, _stream(stream)))
+    _check("attn_profile_end_kinds", lib().attn_profile_end_kinds(ctx, ms, cnt, n, _stream(stream)))
     return {k: (ms[i], cnt[i]) for i, k in enumerate(KERNEL_KINDS)}
 
 

@@ -733,8 +733,9 @@ gqa_status attn_profile_begin(gqa_ctx* c) {
   return GQA_OK;
 }
 
-gqa_status attn_profile_end(gqa_ctx* c, double* ms_per_kind, int* launches_per_kind, gqa_stream_t stream) {
-  if (!c) return GQA_ERR_INVALID_ARG;
+gqa_status attn_profile_end_kinds(gqa_ctx* c, double* ms_per_kind, int* launches_per_kind, int n_kinds,
+                                  gqa_stream_t stream) {
+  if (!c || n_kinds < 0) return GQA_ERR_INVALID_ARG;
   c->profiling = false;
   GQA_CUDA(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
   double ms[GQA_KERNEL_KINDS] = {0};
@@ -749,11 +750,17 @@ gqa_status attn_profile_end(gqa_ctx* c, double* ms_per_kind, int* launches_per_k
     }
   }
   c->ev_used = 0;
-  for (int k = 0; k < GQA_KERNEL_KINDS; ++k) {
-    if (ms_per_kind) ms_per_kind[k] = ms[k];
-    if (launches_per_kind) launches_per_kind[k] = n[k];
+  for (int k = 0; k < n_kinds; ++k) {
+    if (ms_per_kind) ms_per_kind[k] = k < GQA_KERNEL_KINDS ? ms[k] : 0.0;
+    if (launches_per_kind) launches_per_kind[k] = k < GQA_KERNEL_KINDS ? n[k] : 0;
   }
   return GQA_OK;
+}
+
+// (in brackets: the header's macro of this name is for its callers)
+gqa_status (attn_profile_end)(gqa_ctx* c, double* ms_per_kind, int* launches_per_kind, gqa_stream_t stream) {
+  constexpr int kFirstKinds = 7;
+  return attn_profile_end_kinds(c, ms_per_kind, launches_per_kind, kFirstKinds, stream);
 }
 
 void attn_destroy(gqa_ctx* c) {
