@@ -484,7 +484,7 @@ gqa_status attn_debug_pair_schedule(int m_tiles, int n_tiles, int n_pairs, int *
  * 128-key tiles of B sequences among `workers` workers (CTAs or their softmax slots), computed
  * on the host by the code that the kernel runs (for tests, no GPU needed).  lens [B] (host), n_new
  * keys behind each length, units (kv heads x groups of query rows) per sequence, unit_cost (0 .. 64)
- * the tiles that beginning and ending a unit counts for (8, 3 and 2 in the kernels).  Writes the
+ * the tiles that beginning and ending a unit counts for (8, 3 and 2 in the kernels), workers 1 .. 32768.  Writes the
  * pieces in order as octuples (worker, sequence, unit, first tile, tiles, slot of its partial
  * result or -1 for a whole unit, last worker of the unit, number of the first tile among all
  * tiles) into pieces[8 * max_pieces]; *n_pieces gets their count.  Errors:

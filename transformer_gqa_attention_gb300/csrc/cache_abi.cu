@@ -294,7 +294,7 @@ gqa_status attn_cache_evict(gqa_ctx* c, const void* cache_k, const void* cache_v
 gqa_status attn_debug_cache_schedule(const int* lens, int B, int n_new, int S_max, int units, int unit_cost, int workers,
                                      int* pieces, int max_pieces, int* n_pieces) {
   if (!lens || !n_pieces || (!pieces && max_pieces > 0) || B < 1 || n_new < 0 || S_max < 1 || units < 1 ||
-      unit_cost < 0 || unit_cost > 64 || workers < 1 || max_pieces < 0)
+      unit_cost < 0 || unit_cost > 64 || workers < 1 || workers > kMaxRangeWorkers || max_pieces < 0)
     return GQA_ERR_INVALID_ARG;
   auto len_of = [&](int b) { return b < B ? lens[b] : 0; };
   auto places_of = [&](int b) { return (kv_tiles(kv_end(len_of(b), n_new, S_max)) + unit_cost) * units; };

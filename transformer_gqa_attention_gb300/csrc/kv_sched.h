@@ -38,7 +38,8 @@ GQA_HD int kv_tiles(int end) { return end <= kKvTile ? 1 : (end + kKvTile - 1) /
 // workers.
 GQA_HD int range_workers(int total, int most) { return total < most ? total : most; }
 
-// floor(c total / n) in 32-bit arithmetic (n <= 32768)
+// floor(c total / n) in 32-bit arithmetic, which holds for this many workers (a GPU has a few hundred)
+constexpr int kMaxRangeWorkers = 32768;
 GQA_HD int range_start(int total, int n, int c) {
   const unsigned q = static_cast<unsigned>(total) / static_cast<unsigned>(n);
   const unsigned rem = static_cast<unsigned>(total) - q * n;
