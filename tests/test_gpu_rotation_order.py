@@ -144,3 +144,27 @@ def test_decode_reads_the_rotation_behind_the_kernel_that_writes_it(blk, B):
         return out, k, v
 
     check(blk, 1, 4, call)
+
+
+@pytest.mark.parametrize("B,T", [(1, 16), (4, 16), (2, 100)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_residual_forms_read_what_the_kernels_in_front_write(blk, B, T, tree):
+    """R by the call in front, each row's 1 / rms by the call's own first kernel."""
+    abi.attn_set_norm(blk.ctx, gin.norm_weight(600).to(DEV), 1e-5)
+    S = T + 40
+    lens = torch.tensor([(13 * b) % 40 for b in range(B)], dtype=torch.int32, device=DEV)
+    mask = torch.full((B, T, (T + 31) // 32), -1, dtype=torch.int32, device=DEV)
+    # each step's x has another size, and with it another 1 / rms
+    bufs = [[(x * 2.0 ** i, k.clone(), v.clone(), torch.empty(B, T, 4096, device=DEV))
+             for i, (x, k, v) in enumerate(buffers(60, B, T, S))] for _ in range(2)]
+    turn = iter(range(2 * STEPS))
+
+    def call(step, R):
+        x, k, v, out = bufs[next(turn) // STEPS][step]
+        if tree:
+            abi.attn_prefill_tree_residual(blk.ctx, x, B, T, R, mask, k, v, S, lens, out)
+        else:
+            abi.attn_prefill_residual(blk.ctx, x, B, T, R, True, k, v, S, 2, out)
+        return out, k, v
+
+    check(blk, B * T if tree else T, 5, call)

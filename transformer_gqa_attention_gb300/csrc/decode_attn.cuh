@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(160)
           (g * 4 + (row & 3)) * 128);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        qa[kk][h] = live ? __ldg(qp + (kk * 16 + qc) / 2) : 0u;          // k = qc, qc + 1
-        qa[kk][2 + h] = live ? __ldg(qp + (kk * 16 + qc + 8) / 2) : 0u;  // k = qc + 8, qc + 9
+        qa[kk][h] = live ? ld_behind_wait(qp + (kk * 16 + qc) / 2) : 0u;          // k = qc, qc + 1
+        qa[kk][2 + h] = live ? ld_behind_wait(qp + (kk * 16 + qc + 8) / 2) : 0u;  // k = qc + 8, qc + 9
       }
     }
     float o[16][4];

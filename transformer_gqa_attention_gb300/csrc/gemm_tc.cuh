@@ -93,7 +93,7 @@ __device__ __forceinline__ QkvRows qkv_rows(const GemmParams& p, int lane, int m
 __device__ __forceinline__ void qkv_row_scales(const GemmParams& p, QkvRows& q) {
   if (!p.row_scale) return;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) q.rs[k] = __ldg(p.row_scale + min(q.m[k], p.M - 1));
+  for (int k = 0; k < 4; ++k) q.rs[k] = ld_behind_wait(p.row_scale + min(q.m[k], p.M - 1));
 }
 
 // Cache position of position t of sequence b, or -1: a sequence whose p.T positions do not fit the
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(192, (STAGES <= 5 ? 2 : 1))
         *reinterpret_cast<float4*>(static_cast<float*>(p.fin0) + static_cast<size_t>(tok) * 4096 + m) = acc;
       } else {
         if (p.row_scale) {  // attention_norm: the token row's 1 / rms
-          const float rs = __ldg(p.row_scale + tok);
+          const float rs = ld_behind_wait(p.row_scale + tok);
           acc = make_float4(acc.x * rs, acc.y * rs, acc.z * rs, acc.w * rs);
         }
         const int b = tok / p.T;

@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(128) rms_rstd_kernel(const __nv_bfloat16* __re
   const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * 4096);
   uint4 v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __ldg(src + threadIdx.x + 128 * i);
+  for (int i = 0; i < 4; ++i) v[i] = ld_behind_wait(src + threadIdx.x + 128 * i);
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
