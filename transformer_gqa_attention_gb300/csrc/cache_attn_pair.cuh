@@ -17,8 +17,8 @@
 // Barriers that the issuers wait on are CTA 0's, and their commits arrive on both CTAs' barriers.
 //
 // A key tile is 4 x 256 x 128 x 128 FLOP, 1040 cycles of UMMAs, and takes 0.73 us to read; it takes
-// 0.75 to 0.8.  32 sequences of 8128 keys and 64 tokens (1.1 GB, 275 GFLOP): 190 to 198 us, 5.7 TB/s (227
-// where such calls follow one another for seconds: 1360 W at 1.55 GHz);
+// 0.75 to 0.8.  32 sequences of 8128 keys and 64 tokens (1.1 GB, 275 GFLOP): 218 us, 5.1 TB/s, where such calls
+// follow one another (227 after seconds of them: 1360 W at 1.55 GHz), 190 to 198 in runs of 2.5 ms;
 // 32 of 4000 keys 108; one of 32000 keys and 60 tokens 35; 18 of up to 2105 and 103 tokens 58, where a
 // unit's begin and end (tail of the last PV, O, stores, the first softmax) cost as much as its tiles.
 // Measured against: two row tiles in one CTA (no room for a second S buffer, a ring of two and a half

@@ -17,9 +17,11 @@ constexpr int kCommitSlices = 8;  // CTAs (one cluster) per sequence; each moves
 
 // Rows prefix + path[i] -> prefix + i of both caches.  path is strictly increasing, so path[i] >=
 // i: every row moves towards the front, and the rows of one step are read before any is written.
-// At most 2 MB move: a launch is what it costs (2.6 us in a graph for 1 and for 64 sequences), so the
-// slices of a row are CTAs of their own, and the length, which may be written over, is written once the
-// cluster has read it.
+// An accepted path has a few tokens, one step of the loop: a launch is what that costs (2.6 us in a graph for
+// 1 and for 64 sequences), so the slices of a row are CTAs of their own, and the length, which may be
+// written over, is written once the cluster has read it.  Long paths are bound by the steps' round trips, 8
+// rows each with 8 kv heads: 128 tokens of one sequence take 18 us, 256 (2 MB) 34, 128 of 64 sequences (67 MB)
+// 32, of 256 sequences (268 MB) 105.
 __global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const CommitParams p) {
   griddep_wait();
   const int b = blockIdx.y, slice = blockIdx.x;
@@ -285,7 +287,10 @@ constexpr int kMoveSlices = 2 * 16 / kMovePieces;  // of K and V; one more block
 // Rows kept[i] -> i: one CTA per (64-byte column slice of K or V, kv group, sequence), or several
 // that take steps in turn when the outputs are other buffers.  kept is ascending, so kept[i] >= i; in
 // place, a step's rows are all read before any is written, and no later step reads a row that it
-// wrote.  Bound by memory: up to 4096 of up to 8192 positions of 32 sequences (820 MB) in 122 us, 6.7 TB/s.
+// wrote.  For a batch bound by memory: up to 4096 of up to 8192 positions of 32 sequences (820 MB) to other
+// buffers in 122 us, 6.7 TB/s.  For one sequence by the steps of a CTA, in place by all of a slice's and to other
+// buffers by those of the one CTA that moves a head's weights (whole evictions, us, other buffers / in place,
+// 8 kv heads: 4100 to 1024 positions 11 / 12, 32768 to 16384 47 / 70; one kv head: 32768 to 16384 25 / 61).
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
   griddep_wait();
   const int slice = blockIdx.x % (kMoveSlices + 1), part = blockIdx.x / (kMoveSlices + 1), g = blockIdx.y, b = blockIdx.z;
