@@ -38,7 +38,8 @@
  *    also when a later call needs a larger workspace.
  *  - Kernels bound every wait on the device.  A wait that runs out records
  *    GQA_ERR_TIMEOUT in the context's device status word and the kernel returns; read
- *    it with attn_sync_status.
+ *    it with attn_sync_status.  Until it has been read, the outputs of later calls on the
+ *    context are undefined as well.
  */
 #ifndef GQA_ATTN_H
 #define GQA_ATTN_H
@@ -283,6 +284,8 @@ gqa_status attn_cache_commit(gqa_ctx *ctx, void *cache_k, void *cache_v, int B, 
  * key received, summed over the query heads of its kv head, to a running sum; when a cache has
  * grown past its budget, each kv head keeps its first and its most recent positions and the
  * heaviest of the others.  Keys keep the rotation of the position they were written for.
+ * Only attn_decode_attention_weights and attn_decode_weights add weights: behind a prefill or
+ * a verified tree the sums are what they were, and equal weights leave the lower positions.
  */
 
 /*
@@ -294,7 +297,7 @@ gqa_status attn_cache_commit(gqa_ctx *ctx, void *cache_k, void *cache_v, int B, 
  * kv_len  [B] int32: 0 .. S_max (0: h is zero).  Out of range: the sequence's h is NaN, its
  *         weights stay as they are, and attn_sync_status reports GQA_ERR_SHAPE.
  * weights [B,n_kv,S_max] fp32, updated at s < kv_len[b]; the other entries are not touched.
- * h       [B,512 n_kv] bf16 output.
+ * h       [B,512 n_kv] bf16 output; h and weights must not overlap the inputs or each other.
  * Requires 1 <= B <= 1024, 1 <= S_max <= 1048576.
  */
 gqa_status attn_decode_attention_weights(gqa_ctx *ctx, const void *q_r, const void *cache_k, const void *cache_v,
@@ -347,7 +350,8 @@ gqa_status attn_cache_evict(gqa_ctx *ctx, const void *cache_k, const void *cache
  * attn_sync_status — synchronise `stream`, then read and clear the context's device
  * status word.  Returns GQA_OK, GQA_ERR_TIMEOUT (a bounded device wait ran out in some
  * earlier call), GQA_ERR_SHAPE (a per-sequence length or path of some earlier call was out
- * of range) or GQA_ERR_CUDA (the synchronisation itself failed).
+ * of range; GQA_ERR_TIMEOUT comes first where both happened) or GQA_ERR_CUDA (the
+ * synchronisation itself failed).
  */
 gqa_status attn_sync_status(gqa_ctx *ctx, gqa_stream_t stream);
 
