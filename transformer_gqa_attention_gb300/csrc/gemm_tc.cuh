@@ -167,7 +167,8 @@ __device__ __forceinline__ float4 bf16x4_to_float4(uint2 v) {
 }
 
 // Residual values (bf16, 4 per lane and pass) a lane adds in store_f32_chunk for the chunk at
-// columns col0 .. col0+31.
+// columns col0 .. col0+31.  They need no wait: the call's first kernel (rms_rstd_kernel) waits for whoever
+// wrote x before it lets a later one start.
 __device__ __forceinline__ void load_residual_chunk(const GemmParams& p, int lane, int m_base, int col0,
                                                     uint2 (&rv)[8]) {
   const int c4 = col0 + 4 * (lane & 7);
