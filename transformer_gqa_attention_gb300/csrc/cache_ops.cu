@@ -288,9 +288,10 @@ constexpr int kMoveSlices = 2 * 16 / kMovePieces;  // of K and V; one more block
 // that take steps in turn when the outputs are other buffers.  kept is ascending, so kept[i] >= i; in
 // place, a step's rows are all read before any is written, and no later step reads a row that it
 // wrote.  For a batch bound by memory: up to 4096 of up to 8192 positions of 32 sequences (820 MB) to other
-// buffers in 122 us, 6.7 TB/s.  For one sequence by the steps of a CTA, in place by all of a slice's and to other
-// buffers by those of the one CTA that moves a head's weights (whole evictions, us, other buffers / in place,
-// 8 kv heads: 4100 to 1024 positions 11 / 12, 32768 to 16384 47 / 70; one kv head: 32768 to 16384 25 / 61).
+// buffers in 122 us, 6.7 TB/s.  For one sequence in place by the steps, which one CTA takes one after another
+// (whole evictions, us, other buffers / in place, 8 kv heads: 4100 to 1024 positions 11 / 12, 32768 to 16384
+// 47 / 70; one kv head: 32768 to 16384 25 / 61; without the one CTA that moves a head's weights 44 and 22 to other
+// buffers, the others the same).
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
   griddep_wait();
   const int slice = blockIdx.x % (kMoveSlices + 1), part = blockIdx.x / (kMoveSlices + 1), g = blockIdx.y, b = blockIdx.z;
