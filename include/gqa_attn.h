@@ -347,6 +347,179 @@ gqa_status attn_cache_evict(gqa_ctx *ctx, const void *cache_k, const void *cache
                             gqa_stream_t stream);
 
 /*
+ * Paged caches.  A server that shares one pool of cache memory among its sequences hands it out in
+ * pages of page_size positions; a page table names the pages of each sequence in order.  Position s
+ * of sequence b is slot s % page_size of page page_table[b, s / page_size].  Three steps use it:
+ * attn_rope_apply rotates queries, attn_paged_append rotates keys and writes them and the values to
+ * their pages, attn_paged_decode_attention attends with one new token per sequence;
+ * attn_decode_paged is the whole block over such a cache.
+ */
+
+/* Which elements of a head are rotated together by pair j of rot_dim / 2; elements from rot_dim on
+ * are not rotated. */
+enum {
+    GQA_ROPE_PAIRS = 0, /* (2j, 2j + 1), as the block's projections do */
+    GQA_ROPE_HALVES = 1 /* (j, j + rot_dim / 2) */
+};
+
+/* How the frequencies w_j = theta^(-2j / rot_dim) are scaled for contexts longer than the model was
+ * trained with. */
+enum {
+    GQA_ROPE_PLAIN = 0,  /* not at all */
+    GQA_ROPE_LINEAR = 1, /* w / factor */
+    GQA_ROPE_BANDS = 2,  /* by wavelength 2 pi / w: shorter than context / high keeps w, longer than context / low
+                            takes w / factor, and in between (1 - m) w / factor + m w with
+                            m = (context / wavelength - low) / (high - low) */
+    GQA_ROPE_RAMP = 3    /* m w / factor + (1 - m) w, m = clamp((j - a) / (b - a), 0, 1); a and b are the pairs that
+                            turn `high` and `low` times over the context, pair(n) =
+                            rot_dim ln(context / (2 pi n)) / (2 ln theta), a = max(floor pair(high), 0),
+                            b = min(ceil pair(low), rot_dim - 1) (b - a: at least 0.001); the rotated part
+                            is multiplied by gain = 0.1 ln(factor) + 1 */
+};
+
+typedef struct {
+    int kind;                          /* GQA_ROPE_PLAIN .. GQA_ROPE_RAMP */
+    double factor, low, high, context; /* those that the kind does not use are not read */
+} gqa_rope_scaling;
+
+/* A rotation, filled in by attn_rope_init and kept by the caller (host memory, no pointers in it:
+ * may be copied).  turns[j]: revolutions per position of pair j, as a fraction of 2^64. */
+typedef struct {
+    unsigned long long turns[64];
+    float gain;
+    int layout, rot_dim, check;
+} gqa_rope;
+
+/*
+ * attn_rope_init — set up a rotation (host only; needs no GPU).  layout as above; rot_dim a
+ * multiple of 16 in 16 .. 128; theta > 1; scaling may be NULL (GQA_ROPE_PLAIN).
+ * Pair j at position p turns by p turns[j] / 2^64 revolutions, an exact integer product of which the
+ * whole revolutions fall away: far positions lose nothing to the size of the angle.
+ * Errors: GQA_ERR_INVALID_ARG (null; layout or kind unknown; a parameter not finite or out of
+ * range: theta > 1, factor >= 1, context > 0, 0 < low < high), GQA_ERR_SHAPE (rot_dim).
+ */
+gqa_status attn_rope_init(gqa_rope *rope, int layout, int rot_dim, double theta, const gqa_rope_scaling *scaling);
+
+/*
+ * attn_rope_apply — rotate n_heads heads of n_tok tokens: (a, b) of pair j becomes
+ * gain (a cos - b sin, a sin + b cos) of the angle of positions[t], in fp32, rounded once.
+ *
+ * x       bf16: head h of token t at x + t stride + 128 h (elements); rows of a fused projection
+ *         may be given as they are.
+ * positions [n_tok] int32, any value (a negative one turns backwards).
+ * out     bf16, the same form with its own stride; x itself with the same stride rotates in
+ *         place, otherwise it must not overlap x.
+ * Requires 1 <= n_tok <= 262144, 1 <= n_heads <= 1024, both strides multiples of 8 and at least
+ * 128 n_heads (and below 2^31).
+ */
+gqa_status attn_rope_apply(gqa_ctx *ctx, const gqa_rope *rope, const void *x, int n_tok, int n_heads,
+                           long long stride, const int *positions, void *out, long long out_stride,
+                           gqa_stream_t stream);
+
+/*
+ * attn_rope_table — the table R [n_tok,64,2] fp32 of (cos, sin) that the block forms take, for
+ * positions[t] [n_tok] int32; pairs from rot_dim / 2 on are (1, 0).  1 <= n_tok <= 262144.
+ * A rotation in halves has no such table (GQA_ERR_INVALID_ARG).
+ */
+gqa_status attn_rope_table(gqa_ctx *ctx, const gqa_rope *rope, const int *positions, int n_tok, float *R,
+                           gqa_stream_t stream);
+
+enum {
+    GQA_CACHE_BF16 = 0, /* bfloat16 */
+    GQA_CACHE_E4M3 = 1  /* 8-bit floating point (4 exponent bits, 3 mantissa bits) times a scale per kv head */
+};
+
+typedef struct gqa_paged gqa_paged; /* opaque */
+
+/*
+ * attn_paged_create — describe the two pools of a paged cache for the context's kv heads (host only,
+ * enqueues nothing).  Element d of head g in slot i of page n is at
+ *     n stride_page + i stride_pos + g stride_head + d    (elements),
+ * so [page, slot, head, 128], [page, head, slot, 128] and pools that keep a page's keys and values
+ * side by side are all described.
+ *
+ * k_pages, v_pages  the pools, owned by the caller; they must outlive the description.
+ * dtype   GQA_CACHE_BF16 or GQA_CACHE_E4M3.
+ * strides multiples of 16 bytes, and such that no two rows of 128 elements overlap; the stride of
+ *         an extent of 1 is not read.
+ * k_scale, v_scale  GQA_CACHE_E4M3: [n_kv] fp32 on the device, positive and normal: a key or value is the
+ *         stored number times its head's scale (NULL: 1).  Read by every call that uses the pools.
+ *         NULL for bf16.
+ * Requires n_pages >= 1, page_size a multiple of 8 in 8 .. 1048576, strides below 2^39 bytes
+ * and pools that span at most 2^46 elements.
+ * Errors: GQA_ERR_INVALID_ARG (null, dtype unknown, scales with bf16, rows that overlap, the same
+ * pool twice), GQA_ERR_SHAPE, GQA_ERR_ALIGN, GQA_ERR_OOM, GQA_ERR_CUDA.
+ * A description may be used with any context of as many kv heads on the same device.
+ */
+gqa_status attn_paged_create(gqa_ctx *ctx, void *k_pages, void *v_pages, int n_pages, int page_size, int dtype,
+                             long long stride_page, long long stride_pos, long long stride_head,
+                             const float *k_scale, const float *v_scale, gqa_paged **out);
+
+/* attn_paged_destroy — free a description (not the pools).  Work that is enqueued does not need it.
+ * NULL is ignored. */
+void attn_paged_destroy(gqa_paged *paged);
+
+/*
+ * attn_paged_append — write n_new[b] new positions of each sequence behind its kv_len[b]:
+ *     K[kv_len[b] + t] = rotation of k[b,t],  V[kv_len[b] + t] = v[b,t],  t < n_new[b].
+ * The rotation is in fp32 and rounded once to the pools' type (e4m3: times the reciprocal of the
+ * head's scale, saturating at 448; a NaN stays one).
+ *
+ * k, v    bf16: head g of token t of sequence b at b stride_b + t stride_t + 128 g (elements): rows of
+ *         a fused projection, or a dense cache [B,S_max,n_kv,128] that attn_prefill has filled.
+ *         Strides multiples of 8, stride_t at least 128 n_kv, both below 2^31; stride_b is not read for
+ *         B = 1, nor stride_t for T = 1.  No row may overlap the pools.
+ * rope    the rotation; NULL: keys are written as they are (already rotated).
+ * rope_pos [B] int32: position of each sequence's first new token in its text; NULL: kv_len[b].
+ * page_table [B,max_pages] int32; entries of pages that hold no new position are not read.
+ * kv_len  [B] int32; not changed by the call.
+ * n_new   [B] int32: 0 .. T, or NULL: T for every sequence; k and v from n_new[b] on are not read.
+ * A sequence with n_new[b] outside 0 .. T, or kv_len[b] outside 0 .. max_pages page_size -
+ * n_new[b], is left out, and so are positions whose page is outside 0 .. n_pages - 1;
+ * attn_sync_status then reports GQA_ERR_SHAPE.  No two new positions may share a slot.
+ * Requires 1 <= B <= 1024, T >= 1, B T <= 262144, 1 <= max_pages, max_pages page_size <= 1048576.
+ */
+gqa_status attn_paged_append(gqa_ctx *ctx, const gqa_paged *paged, const void *k, const void *v, int B, int T,
+                             long long stride_b, long long stride_t, const gqa_rope *rope, const int *rope_pos,
+                             const int *page_table, int max_pages, const int *kv_len, const int *n_new,
+                             gqa_stream_t stream);
+
+/*
+ * attn_paged_decode_attention — attention of one query position per sequence over keys 0 ..
+ * kv_len[b] - 1 of a paged cache.
+ *
+ * q_r     [B,512 n_kv] bf16 rotated queries.
+ * page_table [B,max_pages] int32; entries from ceil(kv_len[b] / page_size) on are not read, and
+ *         neither are slots from kv_len[b] on.  Sequences may share pages.
+ * kv_len  [B] int32: 0 .. max_pages page_size (0: h is zero).  Out of range, or with a page outside
+ *         0 .. n_pages - 1 among those it reads: the sequence's h is NaN and attn_sync_status reports
+ *         GQA_ERR_SHAPE.
+ * h       [B,512 n_kv] bf16 output; must not overlap the inputs.
+ * Limits as attn_paged_append; the scratch (at most 2 MB) is the context's and grows with the first call.
+ */
+gqa_status attn_paged_decode_attention(gqa_ctx *ctx, const gqa_paged *paged, const void *q_r, int B,
+                                       const int *page_table, int max_pages, const int *kv_len, void *h,
+                                       gqa_stream_t stream);
+
+/*
+ * attn_decode_paged — the block for one new token per sequence over a paged cache, at position
+ * kv_len[b] (0 .. max_pages page_size - 1): writes its K_r and V to their page, attends over keys
+ * 0 .. kv_len[b].  kv_len itself is not changed.
+ *
+ * x [B,1,4096] bf16; R [B,64,2] fp32: rotation of each sequence's new token (attn_rope_table);
+ * delta [B,1,4096] fp32 (NaN for a sequence whose kv_len or a page is out of range; its cache is
+ * not written where the new position's page is).  With an e4m3 cache the new key and value are rounded to
+ * bf16 and then to e4m3.
+ * attn_decode_paged_residual — the same in the residual form (see attn_decode_residual).
+ */
+gqa_status attn_decode_paged(gqa_ctx *ctx, const gqa_paged *paged, const void *x, int B, const float *R,
+                             const int *page_table, int max_pages, const int *kv_len, float *delta,
+                             gqa_stream_t stream);
+gqa_status attn_decode_paged_residual(gqa_ctx *ctx, const gqa_paged *paged, const void *x, int B, const float *R,
+                                      const int *page_table, int max_pages, const int *kv_len, float *h_out,
+                                      gqa_stream_t stream);
+
+/*
  * attn_sync_status — synchronise `stream`, then read and clear the context's device
  * status word.  Returns GQA_OK, GQA_ERR_TIMEOUT (a bounded device wait ran out in some
  * earlier call), GQA_ERR_SHAPE (a per-sequence length or path of some earlier call was out
@@ -380,7 +553,10 @@ enum {
     GQA_KERNEL_CACHE_COMMIT = 10,  /* accepted path moved behind the prefix */
     GQA_KERNEL_EVICT_SELECT = 11,  /* positions that an eviction keeps */
     GQA_KERNEL_EVICT_MOVE = 12,    /* their keys and values moved */
-    GQA_KERNEL_KINDS = 13
+    GQA_KERNEL_PAGED_ATTN = 13,    /* decode attention over a paged cache, with its merge */
+    GQA_KERNEL_PAGED_APPEND = 14,  /* new keys (rotated) and values written to their pages */
+    GQA_KERNEL_ROPE = 15,          /* rotation of queries, or the table of a rotation */
+    GQA_KERNEL_KINDS = 16
 };
 
 /*
@@ -457,8 +633,8 @@ gqa_status attn_decode_attention_noalloc_debug_inject_timeout(void);
 /*
  * attn_debug_inject_timeout — test hook for the failure path (no counterpart on the pages).
  * Arms a one-shot flag: on the next launch of kernel kind `kind` (GQA_KERNEL_QKV_GEMM,
- * _QKV_SPLITK, _FLASH_PREFILL, _DECODE_ATTN, _OUT_GEMM, _OUT_SPLITK or _CACHE_ATTN) made through this
- * context, the first work unit's (_CACHE_ATTN: the last worker's) TMA producer issues no loads.  Its consumers' bounded
+ * _QKV_SPLITK, _FLASH_PREFILL, _DECODE_ATTN, _OUT_GEMM, _OUT_SPLITK, _CACHE_ATTN or _PAGED_ATTN) made through this
+ * context, the first work unit's (_CACHE_ATTN, _PAGED_ATTN: the last worker's) TMA producer issues no loads.  Its consumers' bounded
  * waits then run out (about 2 s), the unit records GQA_ERR_TIMEOUT in the status word,
  * releases its tensor memory and returns; kernels queued after it on the stream may time
  * out too.  Nothing faults or hangs.  The outputs of that call are undefined; the next

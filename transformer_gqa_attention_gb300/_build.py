@@ -19,7 +19,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libgqa_attn.so")
 
 SOURCES = ["gqa_abi.cu", "gemm_launch.cu", "attn_launch.cu", "norm.cu", "decode_noalloc.cu",
-           "cache_abi.cu", "cache_attn.cu", "cache_ops.cu", "gemm_seq.cu"]
+           "cache_abi.cu", "cache_attn.cu", "cache_ops.cu", "gemm_seq.cu", "paged_abi.cu", "paged_attn.cu",
+           "paged_ops.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

@@ -25,11 +25,32 @@ EXPORTED = ("attn_create", "attn_create_shard", "attn_prefill", "attn_decode", "
            "attn_tree_attention", "attn_prefill_tree", "attn_prefill_tree_residual", "attn_cache_commit",
            "attn_decode_attention_weights", "attn_decode_weights", "attn_decode_weights_residual",
            "attn_cache_evict", "attn_debug_cache_schedule",
+            "attn_rope_init", "attn_rope_apply", "attn_rope_table", "attn_paged_create", "attn_paged_destroy",
+            "attn_paged_append", "attn_paged_decode_attention", "attn_decode_paged", "attn_decode_paged_residual",
             "attn_destroy", "attn_strerror", "attn_last_cuda_error")
 
 # Kernel kinds of attn_profile_end_kinds (GQA_KERNEL_* in include/gqa_attn.h).
 KERNEL_KINDS = ("qkv_gemm", "qkv_splitk", "flash_prefill", "decode_attn", "out_gemm", "out_splitk",
-                "rms_norm", "cache_attn", "cache_merge", "cache_weights", "cache_commit", "evict_select", "evict_move")
+                "rms_norm", "cache_attn", "cache_merge", "cache_weights", "cache_commit", "evict_select", "evict_move",
+                "paged_attn", "paged_append", "rope")
+
+# Layouts and scalings of a rotation, types of a paged cache (GQA_ROPE_*, GQA_CACHE_* in include/gqa_attn.h).
+ROPE_LAYOUTS = ("pairs", "halves")
+ROPE_SCALINGS = ("plain", "linear", "bands", "ramp")
+CACHE_DTYPES = ("bf16", "e4m3")
+
+
+class RopeScaling(ctypes.Structure):
+    """gqa_rope_scaling."""
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("context", ctypes.c_double)]
+
+
+class Rope(ctypes.Structure):
+    """gqa_rope: a rotation set up by attn_rope_init."""
+    _fields_ = [("turns", ctypes.c_uint64 * 64), ("gain", ctypes.c_float), ("layout", ctypes.c_int),
+                ("rot_dim", ctypes.c_int), ("check", ctypes.c_int)]
+
 
 _lib = None
 
@@ -107,6 +128,24 @@ def lib() -> ctypes.CDLL:
     L.attn_cache_evict.restype = i32
     L.attn_debug_cache_schedule.argtypes = [ip, i32, i32, i32, i32, i32, i32, ip, i32, ip]
     L.attn_debug_cache_schedule.restype = i32
+    i64, rope = ctypes.c_longlong, ctypes.POINTER(Rope)
+    L.attn_rope_init.argtypes = [rope, i32, i32, ctypes.c_double, ctypes.POINTER(RopeScaling)]
+    L.attn_rope_init.restype = i32
+    L.attn_rope_apply.argtypes = [vp, rope, vp, i32, i32, i64, vp, vp, i64, vp]
+    L.attn_rope_apply.restype = i32
+    L.attn_rope_table.argtypes = [vp, rope, vp, i32, vp, vp]
+    L.attn_rope_table.restype = i32
+    L.attn_paged_create.argtypes = [vp, vp, vp, i32, i32, i32, i64, i64, i64, vp, vp, ctypes.POINTER(vp)]
+    L.attn_paged_create.restype = i32
+    L.attn_paged_destroy.argtypes = [vp]
+    L.attn_paged_destroy.restype = None
+    L.attn_paged_append.argtypes = [vp, vp, vp, vp, i32, i32, i64, i64, rope, vp, vp, i32, vp, vp, vp]
+    L.attn_paged_append.restype = i32
+    L.attn_paged_decode_attention.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, vp]
+    L.attn_paged_decode_attention.restype = i32
+    for name in ("attn_decode_paged", "attn_decode_paged_residual"):
+        getattr(L, name).argtypes = [vp, vp, vp, i32, vp, vp, i32, vp, vp, vp]
+        getattr(L, name).restype = i32
     L.attn_destroy.argtypes = [vp]
     L.attn_destroy.restype = None
     L.attn_strerror.argtypes = [i32]
@@ -343,6 +382,78 @@ def attn_debug_cache_schedule(lens, n_new, S_max, units, unit_cost, workers):
     _check("attn_debug_cache_schedule",
            L.attn_debug_cache_schedule(arr, B, n_new, S_max, units, unit_cost, workers, buf, n.value, ctypes.byref(n)))
     return [tuple(buf[8 * i:8 * i + 8]) for i in range(n.value)]
+
+
+def attn_rope_init(layout, rot_dim, theta, scaling=None, factor=0.0, low=0.0, high=0.0, context=0.0) -> Rope:
+    """Set up a rotation (host only): layout from ROPE_LAYOUTS, scaling from ROPE_SCALINGS or None."""
+    rope = Rope()
+    how = RopeScaling(ROPE_SCALINGS.index(scaling or "plain"), factor, low, high, context)
+    _check("attn_rope_init", lib().attn_rope_init(ctypes.byref(rope), ROPE_LAYOUTS.index(layout), int(rot_dim),
+                                                  float(theta), ctypes.byref(how)))
+    return rope
+
+
+def attn_rope_apply(ctx, rope, x, n_tok, n_heads, stride, positions, out, out_stride, stream=None):
+    """Rotate n_heads heads of n_tok tokens by positions [n_tok] int32; strides in elements between
+    tokens; out may be x."""
+    _check("attn_rope_apply",
+           lib().attn_rope_apply(ctx, rope, _ptr(x), int(n_tok), int(n_heads), int(stride), _ptr(positions), _ptr(out),
+                                 int(out_stride), _stream(stream)))
+
+
+def attn_rope_table(ctx, rope, positions, n_tok, R, stream=None):
+    """The table R [n_tok, 64, 2] fp32 that the block forms take, for positions [n_tok] int32."""
+    _check("attn_rope_table",
+           lib().attn_rope_table(ctx, rope, _ptr(positions), int(n_tok), _ptr(R), _stream(stream)))
+
+
+def attn_paged_create(ctx, k_pages, v_pages, n_pages, page_size, dtype, stride_page, stride_pos, stride_head,
+                      k_scale=None, v_scale=None) -> int:
+    """Describe the two pools of a paged cache: dtype from CACHE_DTYPES, strides in elements, scales
+    [n_kv] fp32 (e4m3).  The pools and scales stay the caller's and have to outlive the description."""
+    paged = ctypes.c_void_p()
+    _check("attn_paged_create",
+           lib().attn_paged_create(ctx, _ptr(k_pages), _ptr(v_pages), int(n_pages), int(page_size),
+                                   CACHE_DTYPES.index(dtype), int(stride_page), int(stride_pos), int(stride_head),
+                                   _ptr(k_scale), _ptr(v_scale), ctypes.byref(paged)))
+    return paged.value
+
+
+def attn_paged_destroy(paged):
+    if paged:
+        lib().attn_paged_destroy(paged)
+
+
+def attn_paged_append(ctx, paged, k, v, B, T, stride_b, stride_t, rope, rope_pos, page_table, max_pages, kv_len,
+                      n_new=None, stream=None):
+    """Write n_new[b] (None: T) keys, rotated by rope (None: as they are), and values behind kv_len[b];
+    strides of k and v in elements between sequences and between tokens."""
+    _check("attn_paged_append",
+           lib().attn_paged_append(ctx, paged, _ptr(k), _ptr(v), int(B), int(T), int(stride_b), int(stride_t), rope,
+                                   _ptr(rope_pos), _ptr(page_table), int(max_pages), _ptr(kv_len), _ptr(n_new),
+                                   _stream(stream)))
+
+
+def attn_paged_decode_attention(ctx, paged, q_r, B, page_table, max_pages, kv_len, h, stream=None):
+    """Attention of one token per sequence over keys 0 .. kv_len[b]-1 of a paged cache; page_table
+    [B, max_pages] and kv_len [B] int32 on the device."""
+    _check("attn_paged_decode_attention",
+           lib().attn_paged_decode_attention(ctx, paged, _ptr(q_r), int(B), _ptr(page_table), int(max_pages),
+                                             _ptr(kv_len), _ptr(h), _stream(stream)))
+
+
+def attn_decode_paged(ctx, paged, x, B, R, page_table, max_pages, kv_len, delta, stream=None):
+    """The block for one new token per sequence over a paged cache, written at position kv_len[b];
+    R [B, 64, 2]."""
+    _check("attn_decode_paged",
+           lib().attn_decode_paged(ctx, paged, _ptr(x), int(B), _ptr(R), _ptr(page_table), int(max_pages),
+                                   _ptr(kv_len), _ptr(delta), _stream(stream)))
+
+
+def attn_decode_paged_residual(ctx, paged, x, B, R, page_table, max_pages, kv_len, h_out, stream=None):
+    _check("attn_decode_paged_residual",
+           lib().attn_decode_paged_residual(ctx, paged, _ptr(x), int(B), _ptr(R), _ptr(page_table), int(max_pages),
+                                            _ptr(kv_len), _ptr(h_out), _stream(stream)))
 
 
 def attn_destroy(ctx):

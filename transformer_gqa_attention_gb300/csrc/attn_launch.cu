@@ -13,6 +13,8 @@ cudaError_t configure_kernels() {
   if (e != cudaSuccess) return e;
   e = configure_cache_attn();
   if (e != cudaSuccess) return e;
+  e = configure_paged_attn();
+  if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(flash_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            FlashSmem::kBytes);
   if (e != cudaSuccess) return e;

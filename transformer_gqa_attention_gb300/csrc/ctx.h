@@ -47,6 +47,7 @@ struct gqa_ctx {
   float norm_eps = 0.f;
   int* status = nullptr;           // device status word (kDevErr* bits)
   int* old_len = nullptr;          // [kDecodeMaxBatch] lengths before an eviction (behind the status word)
+  int* zeros = nullptr;            // [kDecodeMaxBatch] zeros (behind old_len)
   int* counters = nullptr;         // arrival counters of the decode split merge (kCounterInts)
   gqa::DeviceBuffer ws;            // workspace of the block forms
   gqa::DeviceBuffer cache_ws;      // scratch of the attention over caches of per-sequence length
@@ -101,9 +102,10 @@ inline EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// bf16 tensor map with 128-byte swizzle; dims[0] innermost; strides in bytes for dims 1..
+// Tensor map (bf16 unless `type` says otherwise) with 128-byte swizzle; dims[0] innermost; strides in
+// bytes for dims 1..
 inline bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-              const uint32_t* box) {
+              const uint32_t* box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t d[5], s[4];
@@ -114,7 +116,7 @@ inline bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t*
     e[i] = 1;
   }
   for (int i = 0; i < rank - 1; ++i) s[i] = strides[i];
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, s, b, e,
+  return fn(m, type, rank, const_cast<void*>(base), d, s, b, e,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -192,7 +194,7 @@ constexpr size_t kMaxProfiledLaunches = 65536;
 inline const char* const kKindNames[GQA_KERNEL_KINDS] = {"gqa.qkv_gemm", "gqa.qkv_splitk", "gqa.flash_prefill",
                                                   "gqa.decode_attn", "gqa.out_gemm", "gqa.out_splitk",
                                                   "gqa.rms_norm", "gqa.cache_attn", "gqa.cache_merge", "gqa.cache_weights", "gqa.cache_commit", "gqa.evict_select",
-                                                         "gqa.evict_move"};
+                                                         "gqa.evict_move", "gqa.paged_attn", "gqa.paged_append", "gqa.rope"};
 
 // RAII NVTX range around one entry point's host work (its launches nest inside it).
 struct CallRange {

@@ -12,6 +12,7 @@
 #include "ctx.h"
 #include "gqa_attn.h"
 #include "launch.h"
+#include "paged_call.h"
 #include "pair_sched.h"
 #include "params.h"
 
@@ -296,13 +297,15 @@ gqa_status create_impl(const void* wq, const void* wk, const void* wv, const voi
   };
   const size_t rows = c->qkv_rows(), qc = c->q_cols(), kvc = c->kv_cols();
   if (cudaMalloc(&c->w_qkv, rows * 4096 * 2) != cudaSuccess || cudaMalloc(&c->w_o, 4096 * qc * 2) != cudaSuccess ||
-      cudaMalloc(&c->status, (64 + kDecodeMaxBatch) * sizeof(int)) != cudaSuccess ||
+      cudaMalloc(&c->status, (64 + 2 * kDecodeMaxBatch) * sizeof(int)) != cudaSuccess ||
       cudaMalloc(&c->counters, kCounterInts * sizeof(int)) != cudaSuccess) {
     cudaGetLastError();
     return fail(GQA_ERR_OOM);
   }
   c->old_len = c->status + 64;
+  c->zeros = c->old_len + kDecodeMaxBatch;
   cudaError_t e = cudaMemsetAsync(c->status, 0, sizeof(int), s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(c->zeros, 0, kDecodeMaxBatch * sizeof(int), s);
   if (e == cudaSuccess) e = cudaMemsetAsync(c->counters, 0, kCounterInts * sizeof(int), s);
   // k-block-major copies: W_Q rows 0..qc-1, W_K qc..qc+kvc-1, W_V qc+kvc.. of W_QKV; W_O
   if (e == cudaSuccess) e = copy_weight_tiled(c->w_qkv, wq, qc, 0, rows, 64, s);
@@ -566,9 +569,72 @@ gqa_status ragged_impl(gqa_ctx* c, const void* x, int B, int T, const float* R, 
   return run_out(c, h, n_tok, delta, w, sk, residual ? x : nullptr, s);
 }
 
+// The block for one new token per sequence over a paged cache: the projections leave K_r and V of the B
+// tokens in the workspace (a cache of one position each), which the append moves to their pages.
+gqa_status paged_impl(gqa_ctx* c, const gqa_paged* paged, const void* x, int B, const float* R, const int* page_table,
+                      int max_pages, const int* kv_len, float* delta, bool residual, cudaStream_t s) {
+  if (!c || !paged || !x || !R || !page_table || !kv_len || !delta) return GQA_ERR_INVALID_ARG;
+  if (B < 1 || B > kDecodeMaxBatch || max_pages < 1) return GQA_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(R) || !aligned16(page_table) || !aligned16(kv_len) || !aligned16(delta))
+    return GQA_ERR_ALIGN;
+  if (residual && !c->w_qkv_norm) return GQA_ERR_INVALID_ARG;  // attn_set_norm not called (never on a shard)
+  gqa_status st = check_device(c);
+  if (st != GQA_OK) return st;
+  if ((st = check_paged(c, paged, max_pages)) != GQA_OK) return st;
+
+  SkinnyPlan sk_v = skinny_plan(B);
+  const SkinnyPlan* sk = B <= kSkinnyMaxTokens ? &sk_v : nullptr;
+  const WsLayout w = ws_layout(B, c->n_kv, sk, nullptr, 0);
+  const size_t kv_bytes = round_up(static_cast<size_t>(B) * c->kv_cols() * 2, 256);
+  st = ensure_buffer(c, c->ws, w.total + 2 * kv_bytes, s);
+  if (st != GQA_OK) return st;
+  if ((st = reserve_paged_attn(c, s)) != GQA_OK) return st;
+  void* q_r = c->ws.p + w.q_off;
+  void* h = c->ws.p + w.h_off;
+  uint8_t* new_k = c->ws.p + w.total;
+  uint8_t* new_v = new_k + kv_bytes;
+  c->last_q = q_r;
+  c->last_h = h;
+  const float* row_scale = nullptr;
+  if (residual) {
+    if ((st = run_rms(c, x, B, w, s)) != GQA_OK) return st;
+    row_scale = reinterpret_cast<const float*>(c->ws.p + w.rstd_off);
+  }
+  st = run_qkv(c, x, B, 1, R, new_k, new_v, 1, 0, c->zeros, q_r, w, sk, row_scale, s);
+  if (st != GQA_OK) return st;
+  PagedAppendCall a{};
+  a.k = new_k;
+  a.v = new_v;
+  a.B = B;
+  a.T = 1;
+  a.stride_b = c->kv_cols();
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.kv_len = kv_len;
+  if ((st = run_paged_append(c, paged, a, s)) != GQA_OK) return st;
+  if ((st = run_paged_attn(c, paged, q_r, B, page_table, max_pages, kv_len, 1, h, s)) != GQA_OK) return st;
+  return run_out(c, h, B, delta, w, sk, residual ? x : nullptr, s);
+}
+
 }  // namespace
 
 extern "C" {
+
+gqa_status attn_decode_paged(gqa_ctx* c, const gqa_paged* paged, const void* x, int B, const float* R,
+                             const int* page_table, int max_pages, const int* kv_len, float* delta,
+                             gqa_stream_t stream) {
+  CallRange range("gqa.attn_decode_paged");
+  return paged_impl(c, paged, x, B, R, page_table, max_pages, kv_len, delta, false,
+                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+gqa_status attn_decode_paged_residual(gqa_ctx* c, const gqa_paged* paged, const void* x, int B, const float* R,
+                                      const int* page_table, int max_pages, const int* kv_len, float* h_out,
+                                      gqa_stream_t stream) {
+  CallRange range("gqa.attn_decode_paged_residual");
+  return paged_impl(c, paged, x, B, R, page_table, max_pages, kv_len, h_out, true,
+                    reinterpret_cast<cudaStream_t>(stream));
+}
 
 gqa_status attn_prefill(gqa_ctx* c, const void* x, int B, int T, const float* R, int causal, void* cache_k,
                         void* cache_v, int S_max, int start_pos, float* delta, gqa_stream_t stream) {
@@ -685,6 +751,7 @@ gqa_status attn_debug_inject_timeout(gqa_ctx* c, int kind) {
     case GQA_KERNEL_OUT_GEMM:
     case GQA_KERNEL_OUT_SPLITK:
     case GQA_KERNEL_CACHE_ATTN:
+    case GQA_KERNEL_PAGED_ATTN:
       c->fault_kind = kind;
       return GQA_OK;
     default:

@@ -87,6 +87,12 @@ cudaError_t launch_cache_weights(const CacheAttnParams& p, int workers, int n_bl
 cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t s);
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s);
 cudaError_t launch_evict_move(const EvictParams& p, cudaStream_t s);
+// Paged caches (dtype: GQA_CACHE_*) and rotation.
+cudaError_t configure_paged_attn();
+cudaError_t launch_paged_attn(const PagedAttnParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_rope_apply(const RopeParams& p, cudaStream_t s);
+cudaError_t launch_rope_table(const RopeParams& p, cudaStream_t s);
 cudaError_t launch_rms_rstd(const void* x, int rows, float eps, float* r, cudaStream_t s);
 cudaError_t launch_fold_norm_weight(const void* src, const void* w, int rows, void* dst, cudaStream_t s);
 

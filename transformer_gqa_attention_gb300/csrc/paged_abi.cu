@@ -1,0 +1,299 @@
+// paged_abi.cu — the entry points of include/gqa_attn.h for paged caches and rotations: the set-up of
+// a rotation, its application, the description of a paged cache, the append to it and the attention
+// over it.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <new>
+
+#include "ctx.h"
+#include "gqa_attn.h"
+#include "launch.h"
+#include "paged_call.h"
+#include "params.h"
+
+using namespace gqa;
+
+namespace {
+
+constexpr int kRopeCheck = 0x726f7065;
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+bool valid(const gqa_rope* r) {
+  return r->check == kRopeCheck && (r->layout == GQA_ROPE_PAIRS || r->layout == GQA_ROPE_HALVES) && r->rot_dim >= 16 &&
+         r->rot_dim <= 128 && r->rot_dim % 16 == 0;
+}
+
+// w of pair j, scaled.
+double frequency(int rot_dim, int j, double theta, const gqa_rope_scaling& s) {
+  constexpr double kTwoPi = 6.283185307179586476925;
+  const double w = std::pow(theta, -2.0 * j / rot_dim);
+  switch (s.kind) {
+    case GQA_ROPE_LINEAR: return w / s.factor;
+    case GQA_ROPE_BANDS: {
+      const double turns = s.context * w / kTwoPi;  // over the original context
+      if (turns > s.high) return w;
+      if (turns < s.low) return w / s.factor;
+      const double m = (turns - s.low) / (s.high - s.low);
+      return (1.0 - m) * w / s.factor + m * w;
+    }
+    case GQA_ROPE_RAMP: {
+      auto pair = [&](double n) { return rot_dim * std::log(s.context / (n * kTwoPi)) / (2.0 * std::log(theta)); };
+      const double a = std::max(std::floor(pair(s.high)), 0.0);
+      const double b = std::min(std::ceil(pair(s.low)), rot_dim - 1.0);
+      const double m = std::min(std::max((j - a) / std::max(b - a, 0.001), 0.0), 1.0);
+      return m * w / s.factor + (1.0 - m) * w;
+    }
+    default: return w;
+  }
+}
+
+// Elements from a row's start that rows 0 .. n - 1 of `stride` reach.
+size_t reach(long long n, long long stride) { return static_cast<size_t>(n - 1) * static_cast<size_t>(stride); }
+
+size_t pool_bytes(const gqa_paged* g) {
+  const PagedPool& p = g->pool;
+  return (reach(p.n_pages, p.page) + reach(p.page_size, p.pos) + reach(g->n_kv, p.head) + 128) *
+         (g->dtype == GQA_CACHE_BF16 ? 2 : 1);
+}
+
+}  // namespace
+
+gqa_status gqa::check_paged(gqa_ctx* c, const gqa_paged* g, int max_pages) {
+  if (g->n_kv != c->n_kv) return GQA_ERR_INVALID_ARG;
+  if (g->device != c->device) return GQA_ERR_DEVICE;
+  if (static_cast<long long>(max_pages) * g->pool.page_size > kMaxSMax) return GQA_ERR_SHAPE;
+  return GQA_OK;
+}
+
+gqa_status gqa::reserve_paged_attn(gqa_ctx*, cudaStream_t) { return GQA_OK; }
+
+gqa_status gqa::run_paged_append(gqa_ctx* c, const gqa_paged* g, const PagedAppendCall& a, cudaStream_t s) {
+  PagedAppendParams p{};
+  if (a.rope) p.rope = *a.rope;
+  p.rotate = a.rope != nullptr;
+  p.B = a.B;
+  p.T = a.T;
+  p.n_kv = c->n_kv;
+  p.max_pages = a.max_pages;
+  p.stride_b = a.stride_b;
+  p.stride_t = a.stride_t;
+  p.pool = g->pool;
+  p.k = a.k;
+  p.v = a.v;
+  p.rope_pos = a.rope_pos;
+  p.page_table = a.page_table;
+  p.kv_len = a.kv_len;
+  p.n_new = a.n_new;
+  p.status = c->status;
+  ProfScope ps(c, GQA_KERNEL_PAGED_APPEND, s);
+  GQA_CUDA(launch_paged_append(p, g->dtype, s));
+  return GQA_OK;
+}
+
+gqa_status gqa::run_paged_attn(gqa_ctx* c, const gqa_paged* g, const void* q, int B, const int* page_table,
+                               int max_pages, const int* kv_len, int n_new, void* h, cudaStream_t s) {
+  PagedAttnParams p{};
+  p.B = B;
+  p.n_kv = c->n_kv;
+  p.n_new = n_new;
+  p.max_pages = max_pages;
+  p.pool = g->pool;
+  p.q = q;
+  p.page_table = page_table;
+  p.kv_len = kv_len;
+  p.h = h;
+  p.status = c->status;
+  p.scale_log2 = kScaleLog2;
+  ProfScope ps(c, GQA_KERNEL_PAGED_ATTN, s);
+  GQA_CUDA(launch_paged_attn(p, g->dtype, s));
+  return GQA_OK;
+}
+
+extern "C" {
+
+gqa_status attn_rope_init(gqa_rope* rope, int layout, int rot_dim, double theta, const gqa_rope_scaling* scaling) {
+  if (!rope || (layout != GQA_ROPE_PAIRS && layout != GQA_ROPE_HALVES)) return GQA_ERR_INVALID_ARG;
+  if (rot_dim < 16 || rot_dim > 128 || rot_dim % 16) return GQA_ERR_SHAPE;
+  gqa_rope_scaling s{};
+  if (scaling) s = *scaling;
+  if (!std::isfinite(theta) || !(theta > 1.0) || s.kind < GQA_ROPE_PLAIN || s.kind > GQA_ROPE_RAMP) return GQA_ERR_INVALID_ARG;
+  if (s.kind != GQA_ROPE_PLAIN && (!std::isfinite(s.factor) || !(s.factor >= 1.0))) return GQA_ERR_INVALID_ARG;
+  if ((s.kind == GQA_ROPE_BANDS || s.kind == GQA_ROPE_RAMP) &&
+      (!std::isfinite(s.context) || !(s.context > 0.0) || !(s.low > 0.0) || !std::isfinite(s.high) || !(s.high > s.low)))
+    return GQA_ERR_INVALID_ARG;
+  *rope = gqa_rope{};
+  for (int j = 0; j < rot_dim / 2; ++j)  // w <= 1: less than a sixth of a revolution
+    rope->turns[j] =
+        static_cast<unsigned long long>(frequency(rot_dim, j, theta, s) * (18446744073709551616.0 / 6.283185307179586476925));
+  rope->gain = s.kind == GQA_ROPE_RAMP ? static_cast<float>(0.1 * std::log(s.factor) + 1.0) : 1.f;
+  rope->layout = layout;
+  rope->rot_dim = rot_dim;
+  rope->check = kRopeCheck;
+  return GQA_OK;
+}
+
+gqa_status attn_rope_apply(gqa_ctx* c, const gqa_rope* rope, const void* x, int n_tok, int n_heads, long long stride,
+                           const int* positions, void* out, long long out_stride, gqa_stream_t stream) {
+  if (!c || !rope || !x || !positions || !out || !valid(rope)) return GQA_ERR_INVALID_ARG;
+  const long long width = 128LL * n_heads, most = 1LL << 31;
+  if (n_tok < 1 || n_tok > kMaxTokens || n_heads < 1 || n_heads > 1024 || stride < width || out_stride < width ||
+      stride >= most || out_stride >= most)
+    return GQA_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(positions) || !aligned16(out) || stride % 8 || out_stride % 8) return GQA_ERR_ALIGN;
+  const size_t in_bytes = 2 * (reach(n_tok, stride) + width), out_bytes = 2 * (reach(n_tok, out_stride) + width);
+  if (!(out == x && (out_stride == stride || n_tok == 1)) && overlap(out, out_bytes, x, in_bytes)) return GQA_ERR_INVALID_ARG;
+  if (overlap(out, out_bytes, positions, 4 * static_cast<size_t>(n_tok))) return GQA_ERR_INVALID_ARG;
+  gqa_status st = check_device(c);
+  if (st != GQA_OK) return st;
+  CallRange range("gqa.attn_rope_apply");
+  RopeParams p{};
+  p.rope = *rope;
+  p.n_tok = n_tok;
+  p.n_heads = n_heads;
+  p.heads_each = n_heads;
+  p.stride = stride;
+  p.out_stride = out_stride;
+  p.x = x;
+  p.positions = positions;
+  p.out = out;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(c, GQA_KERNEL_ROPE, s);
+  GQA_CUDA(launch_rope_apply(p, s));
+  return GQA_OK;
+}
+
+gqa_status attn_rope_table(gqa_ctx* c, const gqa_rope* rope, const int* positions, int n_tok, float* R,
+                           gqa_stream_t stream) {
+  if (!c || !rope || !positions || !R || !valid(rope) || rope->layout != GQA_ROPE_PAIRS) return GQA_ERR_INVALID_ARG;
+  if (n_tok < 1 || n_tok > kMaxTokens) return GQA_ERR_SHAPE;
+  if (!aligned16(positions) || !aligned16(R)) return GQA_ERR_ALIGN;
+  if (overlap(R, 512 * static_cast<size_t>(n_tok), positions, 4 * static_cast<size_t>(n_tok))) return GQA_ERR_INVALID_ARG;
+  gqa_status st = check_device(c);
+  if (st != GQA_OK) return st;
+  CallRange range("gqa.attn_rope_table");
+  RopeParams p{};
+  p.rope = *rope;
+  p.n_tok = n_tok;
+  p.positions = positions;
+  p.out = R;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(c, GQA_KERNEL_ROPE, s);
+  GQA_CUDA(launch_rope_table(p, s));
+  return GQA_OK;
+}
+
+gqa_status attn_paged_create(gqa_ctx* c, void* k_pages, void* v_pages, int n_pages, int page_size, int dtype,
+                             long long stride_page, long long stride_pos, long long stride_head, const float* k_scale,
+                             const float* v_scale, gqa_paged** out) {
+  if (!out) return GQA_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!c || !k_pages || !v_pages || k_pages == v_pages || (dtype != GQA_CACHE_BF16 && dtype != GQA_CACHE_E4M3) ||
+      (dtype == GQA_CACHE_BF16 && (k_scale || v_scale)))
+    return GQA_ERR_INVALID_ARG;
+  if (n_pages < 1 || page_size < 8 || page_size % 8 || page_size > kMaxSMax) return GQA_ERR_SHAPE;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_scale) || !aligned16(v_scale)) return GQA_ERR_ALIGN;
+  const int size = dtype == GQA_CACHE_BF16 ? 2 : 1;
+  // dimensions with more than one entry, the narrowest stride first: each has to step over all of those before
+  struct Dim {
+    long long n, stride;
+  } dims[3];
+  int used = 0;
+  const Dim all[3] = {{n_pages, stride_page}, {page_size, stride_pos}, {c->n_kv, stride_head}};
+  for (const Dim& d : all)
+    if (d.n > 1) {
+      if (d.stride < 1 || d.stride >= (1LL << 39) / size || d.stride > (1LL << 46) / d.n) return GQA_ERR_SHAPE;
+      if (d.stride * size % 16) return GQA_ERR_ALIGN;
+      dims[used++] = d;
+    }
+  std::sort(dims, dims + used, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  long long row = 128;
+  for (int i = 0; i < used; ++i) {
+    if (dims[i].stride < row) return GQA_ERR_INVALID_ARG;
+    row = dims[i].stride * (dims[i].n - 1) + row;
+  }
+  gqa_paged* g = new (std::nothrow) gqa_paged();
+  if (!g) return GQA_ERR_OOM;
+  g->device = c->device;
+  g->n_kv = c->n_kv;
+  g->dtype = dtype;
+  g->pool = {n_pages,
+             page_size,
+             n_pages > 1 ? stride_page : 128,
+             stride_pos,
+             c->n_kv > 1 ? stride_head : 128,
+             k_pages,
+             v_pages,
+             k_scale,
+             v_scale};
+  *out = g;
+  return GQA_OK;
+}
+
+void attn_paged_destroy(gqa_paged* g) { delete g; }
+
+gqa_status attn_paged_append(gqa_ctx* c, const gqa_paged* g, const void* k, const void* v, int B, int T,
+                             long long stride_b, long long stride_t, const gqa_rope* rope, const int* rope_pos,
+                             const int* page_table, int max_pages, const int* kv_len, const int* n_new,
+                             gqa_stream_t stream) {
+  if (!c || !g || !k || !v || !page_table || !kv_len || (rope && !valid(rope))) return GQA_ERR_INVALID_ARG;
+  if (B < 1 || B > kDecodeMaxBatch || T < 1 || static_cast<long long>(B) * T > kMaxTokens || max_pages < 1) return GQA_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(rope_pos) || !aligned16(page_table) || !aligned16(kv_len) ||
+      !aligned16(n_new))
+    return GQA_ERR_ALIGN;
+  if (B == 1) stride_b = 0;
+  if (T == 1) stride_t = 0;
+  if (stride_b % 8 || stride_t % 8) return GQA_ERR_ALIGN;
+  if (stride_b < 0 || stride_t < 0 || stride_b >= 1LL << 31 || stride_t >= 1LL << 31) return GQA_ERR_SHAPE;
+  gqa_status st = check_device(c);
+  if (st != GQA_OK) return st;
+  if ((st = check_paged(c, g, max_pages)) != GQA_OK) return st;
+  const long long width = 128LL * c->n_kv;
+  if ((T > 1 && stride_t < width) || (B > 1 && stride_b < width)) return GQA_ERR_SHAPE;
+  const size_t rows = 2 * (reach(B, stride_b) + reach(T, stride_t) + width), pool = pool_bytes(g);
+  for (const void* src : {k, v})
+    for (const void* dst : {g->pool.k, g->pool.v})
+      if (overlap(src, rows, dst, pool)) return GQA_ERR_INVALID_ARG;
+  CallRange range("gqa.attn_paged_append");
+  PagedAppendCall a{};
+  a.k = k;
+  a.v = v;
+  a.B = B;
+  a.T = T;
+  a.stride_b = stride_b;
+  a.stride_t = stride_t;
+  a.rope = rope;
+  a.rope_pos = rope_pos;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.kv_len = kv_len;
+  a.n_new = n_new;
+  return run_paged_append(c, g, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+gqa_status attn_paged_decode_attention(gqa_ctx* c, const gqa_paged* g, const void* q_r, int B, const int* page_table,
+                                       int max_pages, const int* kv_len, void* h, gqa_stream_t stream) {
+  if (!c || !g || !q_r || !page_table || !kv_len || !h) return GQA_ERR_INVALID_ARG;
+  if (B < 1 || B > kDecodeMaxBatch || max_pages < 1) return GQA_ERR_SHAPE;
+  if (!aligned16(q_r) || !aligned16(page_table) || !aligned16(kv_len) || !aligned16(h)) return GQA_ERR_ALIGN;
+  gqa_status st = check_device(c);
+  if (st != GQA_OK) return st;
+  if ((st = check_paged(c, g, max_pages)) != GQA_OK) return st;
+  const size_t heads = static_cast<size_t>(B) * c->n_kv * 1024;
+  if (overlap(h, heads, q_r, heads) || overlap(h, heads, kv_len, 4 * static_cast<size_t>(B)) ||
+      overlap(h, heads, page_table, 4 * static_cast<size_t>(B) * max_pages))
+    return GQA_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = reserve_paged_attn(c, s)) != GQA_OK) return st;
+  CallRange range("gqa.attn_paged_decode_attention");
+  return run_paged_attn(c, g, q_r, B, page_table, max_pages, kv_len, 0, h, s);
+}
+
+}  // extern "C"

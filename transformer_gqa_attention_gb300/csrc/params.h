@@ -7,6 +7,8 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "gqa_attn.h"
+
 namespace gqa {
 
 // Status bits OR-ed into the context's device status word.
@@ -162,6 +164,54 @@ struct EvictParams {
   int* new_len;           // [B], may be kv_len
   int* old_len;           // [B] scratch: kv_len as the selection read it (-1: out of range)
   int* status;
+};
+
+// Rotation of heads by position (attn_rope_apply), or the table of it.
+struct RopeParams {
+  gqa_rope rope;
+  int n_tok, n_heads;
+  int heads_each;          // heads that one warp takes of a token (of 4 at a time)
+  long long stride, out_stride;
+  const void* x;           // bf16
+  const int* positions;    // [n_tok]
+  void* out;               // bf16, may be x; table: fp32 [n_tok, 64, 2]
+};
+
+// A pool of cache pages: element d of head g in slot i of page n is at n page + i pos + g head + d.
+struct PagedPool {
+  int n_pages, page_size;
+  long long page, pos, head;  // elements
+  void* k;
+  void* v;
+  const float* k_scale;    // [n_kv] of e4m3 pools, or null
+  const float* v_scale;
+};
+
+struct PagedAppendParams {
+  gqa_rope rope;
+  int rotate;              // 0: keys as they are
+  int B, T, n_kv, max_pages;
+  long long stride_b, stride_t;
+  PagedPool pool;
+  const void* k;
+  const void* v;
+  const int* rope_pos;     // [B] or null: kv_len
+  const int* page_table;   // [B, max_pages]
+  const int* kv_len;       // [B]
+  const int* n_new;        // [B] or null: T
+  int* status;
+};
+
+// Attention of one token per sequence over pages: keys 0 .. kv_len[b] + n_new - 1.
+struct PagedAttnParams {
+  int B, n_kv, n_new, max_pages;
+  PagedPool pool;
+  const void* q;           // [B, 512 n_kv] bf16
+  const int* page_table;   // [B, max_pages]
+  const int* kv_len;       // [B]
+  void* h;                 // [B, 512 n_kv] bf16
+  int* status;
+  float scale_log2;        // log2(e) / sqrt(128)
 };
 
 }  // namespace gqa
