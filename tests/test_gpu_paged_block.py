@@ -299,3 +299,27 @@ def test_steps_are_profiled():
     assert [got[k][1] for k in ("rope", "paged_append", "paged_attn")] == [1, 1, 1]
     assert all(got[k][0] > 0 for k in ("rope", "paged_append", "paged_attn"))
     abi.attn_destroy(s.ctx)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_waits_that_run_out(dtype):
+    ctx = _zero_context(8)
+    pools = Pools(ctx, 64, 64, dtype)
+    for c in (pools.k, pools.v):
+        c.copy_(torch.randint(0, 100, c.shape, device=DEV, dtype=torch.uint8) if dtype == "e4m3" else torch.randn(c.shape, device=DEV))
+    t, lens = ints(np.arange(64).reshape(2, 32)), ints([2048, 1500])
+    q, h = torch.randn(2, 4096, device=DEV).to(torch.bfloat16), torch.empty(2, 4096, dtype=torch.bfloat16, device=DEV)
+    abi.attn_paged_decode_attention(ctx, pools.p, q, 2, t, 32, lens, h)
+    abi.attn_sync_status(ctx)
+    want = h.clone()
+    abi.attn_debug_inject_timeout(ctx, "paged_attn")
+    abi.attn_paged_decode_attention(ctx, pools.p, q, 2, t, 32, lens, h)
+    with pytest.raises(abi.GQAError) as e:
+        abi.attn_sync_status(ctx)
+    assert e.value.status == 5
+    for _ in range(2):
+        h.fill_(0)
+        abi.attn_paged_decode_attention(ctx, pools.p, q, 2, t, 32, lens, h)
+        abi.attn_sync_status(ctx)
+        assert torch.equal(h.view(torch.int16), want.view(torch.int16))
+    abi.attn_destroy(ctx)

@@ -11,6 +11,7 @@
 
 #include "ctx.h"
 #include "gqa_attn.h"
+#include "kv_sched.h"
 #include "launch.h"
 #include "paged_call.h"
 #include "params.h"
@@ -58,6 +59,39 @@ double frequency(int rot_dim, int j, double theta, const gqa_rope_scaling& s) {
 // Elements from a row's start that rows 0 .. n - 1 of `stride` reach.
 size_t reach(long long n, long long stride) { return static_cast<size_t>(n - 1) * static_cast<size_t>(stride); }
 
+// A pool as the attention copies it: boxes of 2^log_box slots of one head and page, bf16 rows as two halves of
+// 64 elements.
+bool map_pool(CUtensorMap* m, const void* base, const gqa_paged* g) {
+  const PagedPool& p = g->pool;
+  const uint64_t n_pages = p.n_pages, slots = p.page_size, heads = g->n_kv;
+  const uint32_t box = 1u << g->log_box;
+  if (g->dtype == GQA_CACHE_E4M3) {
+    const uint64_t dims[4] = {128, slots, heads, n_pages};
+    const uint64_t strides[3] = {static_cast<uint64_t>(p.pos), static_cast<uint64_t>(p.head), static_cast<uint64_t>(p.page)};
+    const uint32_t shape[4] = {128, box, 1, 1};
+    return make_map(m, base, 4, dims, strides, shape, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+  }
+  const uint64_t dims[5] = {64, slots, 2, heads, n_pages};
+  const uint64_t strides[4] = {2 * static_cast<uint64_t>(p.pos), 128, 2 * static_cast<uint64_t>(p.head),
+                               2 * static_cast<uint64_t>(p.page)};
+  const uint32_t shape[5] = {64, box, 2, 1, 1};
+  return make_map(m, base, 5, dims, strides, shape);
+}
+
+// Scratch of the attention: partial results of at most two pieces a CTA.
+struct PagedScratch {
+  int ctas;
+  size_t part_o, part_ml, bytes;
+};
+PagedScratch paged_scratch(const gqa_ctx* c) {
+  PagedScratch l{};
+  l.ctas = 2 * c->num_sms;
+  const size_t rows = 2 * static_cast<size_t>(l.ctas) * 4;
+  l.part_ml = round_up(rows * 128 * sizeof(float), 256);
+  l.bytes = l.part_ml + rows * sizeof(float2);
+  return l;
+}
+
 size_t pool_bytes(const gqa_paged* g) {
   const PagedPool& p = g->pool;
   return (reach(p.n_pages, p.page) + reach(p.page_size, p.pos) + reach(g->n_kv, p.head) + 128) *
@@ -73,7 +107,9 @@ gqa_status gqa::check_paged(gqa_ctx* c, const gqa_paged* g, int max_pages) {
   return GQA_OK;
 }
 
-gqa_status gqa::reserve_paged_attn(gqa_ctx*, cudaStream_t) { return GQA_OK; }
+gqa_status gqa::reserve_paged_attn(gqa_ctx* c, cudaStream_t s) {
+  return ensure_buffer(c, c->cache_ws, paged_scratch(c).bytes, s);
+}
 
 gqa_status gqa::run_paged_append(gqa_ctx* c, const gqa_paged* g, const PagedAppendCall& a, cudaStream_t s) {
   PagedAppendParams p{};
@@ -100,6 +136,9 @@ gqa_status gqa::run_paged_append(gqa_ctx* c, const gqa_paged* g, const PagedAppe
 
 gqa_status gqa::run_paged_attn(gqa_ctx* c, const gqa_paged* g, const void* q, int B, const int* page_table,
                                int max_pages, const int* kv_len, int n_new, void* h, cudaStream_t s) {
+  const PagedScratch l = paged_scratch(c);
+  gqa_status st = ensure_buffer(c, c->cache_ws, l.bytes, s);
+  if (st != GQA_OK) return st;
   PagedAttnParams p{};
   p.B = B;
   p.n_kv = c->n_kv;
@@ -110,10 +149,21 @@ gqa_status gqa::run_paged_attn(gqa_ctx* c, const gqa_paged* g, const void* q, in
   p.page_table = page_table;
   p.kv_len = kv_len;
   p.h = h;
+  p.S_max = max_pages * g->pool.page_size;
+  p.log_box = g->log_box;
+  p.unit_cost = kUnitCostDecode;
+  p.part_o = reinterpret_cast<float*>(c->cache_ws.p + l.part_o);
+  p.part_ml = reinterpret_cast<float2*>(c->cache_ws.p + l.part_ml);
+  p.counters = c->counters;
   p.status = c->status;
   p.scale_log2 = kScaleLog2;
+  p.fault = take_fault(c, GQA_KERNEL_PAGED_ATTN);
+  // as many CTAs as fit, or as the longest sequences that the table allows have places for
+  const size_t tiles = (static_cast<size_t>(p.S_max) + kKvTile - 1) / kKvTile;
+  const size_t places = static_cast<size_t>(B) * c->n_kv * (tiles + p.unit_cost);
+  const int ctas = static_cast<int>(std::min<size_t>(l.ctas, places));
   ProfScope ps(c, GQA_KERNEL_PAGED_ATTN, s);
-  GQA_CUDA(launch_paged_attn(p, g->dtype, s));
+  GQA_CUDA(launch_paged_attn(g->map_k, g->map_v, p, g->dtype, ctas, s));
   return GQA_OK;
 }
 
@@ -233,6 +283,11 @@ gqa_status attn_paged_create(gqa_ctx* c, void* k_pages, void* v_pages, int n_pag
              v_pages,
              k_scale,
              v_scale};
+  for (g->log_box = 3; g->log_box < 6 && page_size % (2 << g->log_box) == 0;) ++g->log_box;
+  if (!map_pool(&g->map_k, k_pages, g) || !map_pool(&g->map_v, v_pages, g)) {
+    delete g;
+    return cuda_fail(cudaErrorInvalidValue);
+  }
   *out = g;
   return GQA_OK;
 }

@@ -1,95 +1,571 @@
-// paged_attn.cuh — attention of one new token per sequence over a paged cache.
+// paged_attn.cuh — attention of one new token per sequence over a paged cache (bf16 or e4m3), split over
+// the cache's length and joined.
 //
-// A CTA per (sequence, kv head); a warp takes every eighth key, a lane four elements of it.  The
-// four query heads of the kv head share each key and value; online softmax in fp32, the warps'
-// results joined through shared memory.
+// The four query heads of kv head g share its keys and values, so a byte of the cache is read once for all of
+// them, and reading it is what bounds the kernel.  Persistent CTAs, two per SM, each take an equal share of all
+// sequences' 128-key tiles (kv_sched.h: found on the device from the lengths, so one long sequence and
+// a ragged batch both fill the GPU).
+//
+//   warps 0..3  consumers: each takes a quarter of the keys of every stage; S = q K^T and O += P V with
+//               mma.sync m16n8k16, rows 0..3 being the heads; online softmax in fp32
+//   warp 4      producer: a TMA box is the largest power of two of slots that divides the page (at most 64), so
+//               that a box never leaves its page.  Lane i knows the page of box i of the next 32 (read
+//               ahead while the boxes before are copied) and copies that box of K and of V itself.
+//
+// A piece of a unit (sequence, kv head) that a CTA does not have to itself leaves an unnormalised partial
+// (O, maximum m, sum l) behind; the last CTA of the unit to arrive joins the pieces in their order, so
+// results do not depend on which one is last.
+//
+// e4m3: numbers become fp16, which holds all of them, NaN included (bf16 would as well, but there is no
+// instruction to it).  The queries are brought to fp16 with the exponent of their row's largest element taken
+// out (exact down to 2^-14 of it, to 2^-25 of it below), which goes into the scale of the scores with k_scale;
+// weights are 2^(c s - m + 15), so that they keep fp16's full precision down to 2^-29 of the largest and a million
+// small ones are not lost.  v_scale is applied to the joined result.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
+#include "kv_sched.h"
 #include "params.h"
 #include "ptx.cuh"
 
 namespace gqa {
 
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
-  return make_float4(bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y), bf16hi_to_f32(v.y));
+template <typename E>
+struct PagedTile;
+template <>
+struct PagedTile<__nv_bfloat16> {
+  static constexpr int kKeys = 64;        // of a stage
+  static constexpr float kShift = 0.f;    // of the weights' exponent
+};
+template <>
+struct PagedTile<uint8_t> {
+  static constexpr int kKeys = 128;
+  static constexpr float kShift = 15.f;
+};
+
+constexpr int kPagedStages = 3;
+constexpr int kPagedThreads = 160;
+
+struct PagedSmem {
+  static constexpr int kHalf = 64 * 128 * 2;  // K or V of a stage: 64 keys of bf16 or 128 of e4m3
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kRed = kPagedStages * kStage;  // the consumers' results: [4 warps][4 heads][128], then (m, l)
+  static constexpr int kRedBytes = 4 * 4 * 128 * 4 + 4 * 4 * 8;
+  static constexpr int kBar = kRed + kRedBytes;
+  static constexpr int kRange = kBar + 128;
+  static constexpr int kBytes = kRange + 64 + 1024;
+};
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1,
+                                          __nv_bfloat16) {
+  mma_bf16_16816(d, a0, 0u, a2, 0u, b0, b1);
 }
-__device__ __forceinline__ float4 load4(const uint8_t* p) {
-  const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(p));
-  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xFFFF), __NV_E4M3);
-  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v >> 16), __NV_E4M3);
-  const float2 x = __half22float2(__half2(a)), y = __half22float2(__half2(b));
-  return make_float4(x.x, x.y, y.x, y.y);
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1, uint8_t) {
+  mma_f16_16816(d, a0, 0u, a2, 0u, b0, b1);
+}
+
+// Two e4m3 numbers as fp16.
+__device__ __forceinline__ uint32_t halves_of(uint32_t e4m3x2) {
+  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(e4m3x2), __NV_E4M3);
+  return static_cast<uint32_t>(r.x) | static_cast<uint32_t>(r.y) << 16;
+}
+
+// What the consumers read of a stage.  Of a 16-key block starting at key k0, keys(kk) gives the B operands of
+// S += q K^T for the block's keys 0..7 and 8..15 and 16 of the 128 elements; values(i) those of O += P V
+// for all 16 keys and two sets of eight columns of O.
+template <typename E>
+struct PagedReader;
+
+// A box of R slots is two halves of 64 elements, [half][slot][128 bytes], 128-byte swizzle.
+template <>
+struct PagedReader<__nv_bfloat16> {
+  uint32_t half;               // bytes from a box's first half to its second
+  uint32_t k_row, v_row;       // this lane's rows, from the stage's start
+  uint32_t k_swz, v_swz, k_sub, v_sub;
+  __device__ __forceinline__ PagedReader(int lane, int k0, int log_box) {
+    const int mi = lane >> 3;
+    half = 128u << log_box;
+    auto row = [&](int key) { return ((key >> log_box) << (8 + log_box)) + (key & ((1 << log_box) - 1)) * 128; };
+    const int kk = k0 + (mi >> 1) * 8 + (lane & 7), kv = k0 + (mi & 1) * 8 + (lane & 7);
+    k_row = row(kk);
+    v_row = row(kv);
+    k_swz = kk & 7;
+    v_swz = kv & 7;
+    k_sub = mi & 1;
+    v_sub = mi >> 1;
+  }
+  __device__ __forceinline__ void keys(uint32_t k, int kk, uint32_t (&b)[2][2]) const {
+    const uint32_t cd = 2 * kk + k_sub;
+    ldsm_x4(k + k_row + (cd >> 3) * half + (((cd & 7) ^ k_swz) << 4), b[0][0], b[0][1], b[1][0], b[1][1]);
+  }
+  template <bool kTail>
+  __device__ __forceinline__ void values(uint32_t v, int i, const uint32_t (&seen)[2], uint32_t (&b)[2][2]) const {
+    const uint32_t cd = 2 * i + v_sub;
+    ldsm_x4_t(v + v_row + (cd >> 3) * half + (((cd & 7) ^ v_swz) << 4), b[0][0], b[0][1], b[1][0], b[1][1]);
+    if (kTail) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        b[s][0] &= seen[0];
+        b[s][1] &= seen[1];
+      }
+    }
+  }
+  // d of column n of set s of values(i)
+  static __device__ __forceinline__ int column(int i, int s, int n) { return 16 * i + 8 * s + n; }
+};
+
+// A row is 128 bytes, 128-byte swizzle.  A 4-byte register of ldmatrix holds elements 4 c .. 4 c + 3 (c = lane & 3)
+// of its 16: they take the places 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of the product's sum, and the queries the same.
+// Transposed, it holds elements 2 n, 2 n + 1 of keys 2 c and 2 c + 1: set 0 is the even elements, set 1 the odd ones.
+template <>
+struct PagedReader<uint8_t> {
+  uint32_t row, swz, sub;
+  __device__ __forceinline__ PagedReader(int lane, int k0, int) {
+    const int mi = lane >> 3;
+    const int key = k0 + (mi & 1) * 8 + (lane & 7);
+    row = key * 128;
+    swz = key & 7;
+    sub = mi >> 1;
+  }
+  // two steps of 16 elements at once: kk even, b[step][keys 0..7, 8..15][2]
+  __device__ __forceinline__ void keys2(uint32_t k, int kk, uint32_t (&b)[2][2][2]) const {
+    uint32_t r[4];
+    ldsm_x4(k + row + (((kk + sub) ^ swz) << 4), r[0], r[1], r[2], r[3]);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        b[s][n][0] = halves_of(r[2 * s + n] & 0xFFFFu);
+        b[s][n][1] = halves_of(r[2 * s + n] >> 16);
+      }
+  }
+  template <bool kTail>
+  __device__ __forceinline__ void values2(uint32_t v, int i, const uint32_t (&seen)[2], uint32_t (&b)[2][2][2]) const {
+    uint32_t r[4];
+    ldsm_x4_t(v + row + (((i + sub) ^ swz) << 4), r[0], r[1], r[2], r[3]);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {  // keys 0..7, 8..15
+        const uint32_t x = __byte_perm(kTail ? r[2 * s + n] & seen[n] : r[2 * s + n], 0u, 0x3120);
+        b[s][0][n] = halves_of(x & 0xFFFFu);
+        b[s][1][n] = halves_of(x >> 16);
+      }
+  }
+  static __device__ __forceinline__ int column(int i, int s, int n) { return 16 * i + 2 * n + s; }
+};
+
+// A worker's share of the places (kv_sched.h): thread i sums those of sequences i per .. i per + per - 1;
+// a scan over the CTA gives the total and finds where the share starts.
+struct PagedRange {
+  int* at;  // [5] per-warp sums, then total, workers, first place, places, sequence, offset in it, its length
+  __device__ __forceinline__ int total() const { return at[8]; }
+  __device__ __forceinline__ int workers() const { return at[9]; }
+  __device__ __forceinline__ KvWalk walk(const PagedAttnParams& p) const {
+    KvWalk w;
+    w.n = 0;
+    if (at[11] > 0) w.start(p.unit_cost, at[12], at[13], at[14], p.n_new, p.S_max, at[10], at[11]);
+    return w;
+  }
+  __device__ __forceinline__ void find(const PagedAttnParams& p) const {
+    constexpr int kWarps = kPagedThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = (p.B + kPagedThreads - 1) / kPagedThreads, b0 = threadIdx.x * per, b1 = min(b0 + per, p.B);
+    auto places = [&](int len) { return (kv_tiles(kv_end(len, p.n_new, p.S_max)) + p.unit_cost) * p.n_kv; };
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) mine += places(__ldcg(p.kv_len + b));
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) at[warp] = x;
+    __syncthreads();
+    int before = x - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += at[w];
+      all += at[w];
+    }
+    const int n = range_workers(all, gridDim.x), c = blockIdx.x;
+    const int lo = c < n ? range_start(all, n, c) : all, hi = c < n ? range_start(all, n, c + 1) : all;
+    if (threadIdx.x == 0) {
+      at[8] = all;
+      at[9] = n;
+      at[10] = lo;
+      at[11] = hi - lo;
+    }
+    if (lo >= before && lo < before + mine) {
+      int b = b0, from = before, len = __ldcg(p.kv_len + b);
+      while (lo >= from + places(len)) {
+        from += places(len);
+        len = __ldcg(p.kv_len + ++b);
+      }
+      at[12] = b;
+      at[13] = lo - from;
+      at[14] = len;
+    }
+    __syncthreads();
+  }
+};
+
+// Keys of a piece: from its first tile to the end of its last or of the sequence.
+__device__ __forceinline__ int piece_keys(const KvWalk& w, int end) {
+  return max(0, min(end, (w.first + w.n) * kKvTile) - w.first * kKvTile);
 }
 
 template <typename E>
-__global__ void __launch_bounds__(256) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
-  __shared__ float4 red_o[8][4][32];
-  __shared__ float2 red_ml[8][4];
+__global__ void __launch_bounds__(kPagedThreads, 2)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ PagedAttnParams p) {
+  constexpr bool k8 = sizeof(E) == 1;
+  constexpr int kKeys = PagedTile<E>::kKeys;
+  constexpr int kRow = 128 * sizeof(E);
+  using L = PagedSmem;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* empty_bar = full_bar + kPagedStages;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty_bar + kPagedStages);
+  volatile int* last_flag = abort_flag + 1;
+  volatile int* bad_page = abort_flag + 2;  // [kPagedStages] a page of the stage's keys is out of range
+  const PagedRange range{reinterpret_cast<int*>(smem + L::kRange)};
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPagedStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
   griddep_launch_dependents();
-  griddep_wait();
-  const int g = blockIdx.x, b = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = __ldcg(p.kv_len + b);
-  const bool in_range = len >= 0 && len <= p.max_pages * p.pool.page_size - p.n_new;
-  const int end = in_range ? len + p.n_new : 0;
-  const float ks = p.scale_log2 * (p.pool.k_scale ? __ldg(p.pool.k_scale + g) : 1.f);
-  float4 q[4], o[4];
-  float m[4], l[4];
-#pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    q[h] = load4(static_cast<const __nv_bfloat16*>(p.q) + (static_cast<size_t>(b) * p.n_kv * 4 + g * 4 + h) * 128 + 4 * lane);
-    o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-    m[h] = -INFINITY;
-    l[h] = 0.f;
-  }
-  bool bad = !in_range;
-  for (int s = warp; s < end; s += 8) {
-    const int n = s / p.pool.page_size;
-    const int page = __ldcg(p.page_table + static_cast<size_t>(b) * p.max_pages + n);
-    if (page < 0 || page >= p.pool.n_pages) {
-      bad = true;
-      break;
+  griddep_wait();  // lengths, queries and the new cache entries; the scratch of the call before
+  range.find(p);
+  KvWalk w = range.walk(p);
+  auto len_of = [&](int b) { return __ldcg(p.kv_len + b); };
+
+  if (warp == 4) {
+    // ------------------------------------------------------------------ producer
+    const int box = 1 << p.log_box;
+    const int per_page = p.pool.page_size >> p.log_box;  // boxes
+    const int per_stage = kKeys >> p.log_box;
+    // test hook: the last worker issues no loads, so its consumers wait out and abort
+    const bool no_loads = p.fault && static_cast<int>(blockIdx.x) == range.workers() - 1;
+    int issued = 0;
+    bool ok = !no_loads;
+    for (; ok && !w.done(); w.next(p.n_kv, p.n_new, p.S_max, len_of)) {
+      const int end = kv_end(w.len, p.n_new, p.S_max);
+      const int keys = piece_keys(w, end);
+      const int* table = p.page_table + static_cast<size_t>(w.b) * p.max_pages;
+      const int first = w.first * (kKvTile >> p.log_box);  // box of the sequence
+      const int boxes = (keys + box - 1) >> p.log_box;
+      // page and slot of this lane's box of 32 boxes from `from` on
+      auto look = [&](int from, int& page, int& slot) {
+        const int i = from + lane;
+        page = -1;
+        if (i < boxes) {
+          const int n = (first + i) / per_page;
+          slot = (first + i - n * per_page) << p.log_box;
+          page = __ldcg(table + n);
+        }
+      };
+      int page = 0, slot = 0, next_page = 0, next_slot = 0;
+      look(0, next_page, next_slot);
+      for (int k0 = 0, i = 0; ok && k0 < keys; k0 += kKeys, i += per_stage, ++issued) {
+        if ((i & 31) == 0) {
+          page = next_page;
+          slot = next_slot;
+          look(i + 32, next_page, next_slot);
+        }
+        const int s = issued % kPagedStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[s], ((issued / kPagedStages) & 1) ^ 1, abort_flag, p.status));
+        if (!ok) break;
+        const int j = lane - (i & 31);  // box of the stage
+        const bool mine = j >= 0 && j < per_stage && i + j < boxes;
+        const bool fits = page >= 0 && page < p.pool.n_pages;
+        const uint32_t copies = __ballot_sync(0xffffffffu, mine && fits);
+        const uint32_t wrong = __ballot_sync(0xffffffffu, mine && !fits);
+        if (lane == 0) {
+          bad_page[s] = wrong != 0;
+          if (wrong) atomicOr(p.status, kDevErrRange);
+          mbar_arrive_expect_tx(&full_bar[s], static_cast<uint32_t>(__popc(copies)) * 2 * box * kRow);
+        }
+        __syncwarp();
+        if (mine && fits) {
+          uint8_t* dst = smem + s * L::kStage + j * box * kRow;
+          if constexpr (k8) {
+            tma_load_4d(dst, &tmK, &full_bar[s], 0, slot, w.u, page);
+            tma_load_4d(dst + L::kHalf, &tmV, &full_bar[s], 0, slot, w.u, page);
+          } else {
+            tma_load_5d(dst, &tmK, &full_bar[s], 0, slot, 0, w.u, page);
+            tma_load_5d(dst + L::kHalf, &tmV, &full_bar[s], 0, slot, 0, w.u, page);
+          }
+        }
+      }
     }
-    const long long at = page * p.pool.page + (s - n * p.pool.page_size) * p.pool.pos + g * p.pool.head + 4 * lane;
-    const float4 k = load4(static_cast<const E*>(p.pool.k) + at), v = load4(static_cast<const E*>(p.pool.v) + at);
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      float x = q[h].x * k.x + q[h].y * k.y + q[h].z * k.z + q[h].w * k.w;
-#pragma unroll
-      for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
-      x *= ks;
-      const float top = fmaxf(m[h], x), base = top == -INFINITY ? 0.f : top;
-      const float a = fast_exp2(m[h] - base), e = fast_exp2(x - base);
-      m[h] = top;
-      l[h] = l[h] * a + e;
-      o[h] = make_float4(o[h].x * a + e * v.x, o[h].y * a + e * v.y, o[h].z * a + e * v.z, o[h].w * a + e * v.w);
+    if (*abort_flag) {
+      for (int i = (issued > kPagedStages ? issued - kPagedStages : 0); i < issued; ++i)
+        mbar_wait_drain(&full_bar[i % kPagedStages], (i / kPagedStages) & 1);
     }
+    return;
   }
+
+  // -------------------------------------------------------------------- consumers
+  constexpr int kBlocks = kKeys / 64;  // 16-key blocks of a warp in a stage
+  const int r0 = lane >> 2, c2 = (lane & 3) * 2;
+  const bool live = r0 < 4;
+  float* red_o = reinterpret_cast<float*>(smem + L::kRed);     // [4 warps][4 heads][128]
+  float2* red_ml = reinterpret_cast<float2*>(red_o + 4 * 512);  // [4 warps][4 heads]
+  const PagedReader<E> rd0(lane, warp * 16 * kBlocks, p.log_box);
+  int item = 0;
+  for (; !w.done(); w.next(p.n_kv, p.n_new, p.S_max, len_of)) {
+    const int end = kv_end(w.len, p.n_new, p.S_max);
+    const int keys = piece_keys(w, end);
+    const int g = w.u;
+    float scale = p.scale_log2 * (k8 && p.pool.k_scale ? __ldcg(p.pool.k_scale + g) : 1.f);
+
+    // A operand: rows r0 (heads), all 128 elements in the order that the keys' registers have
+    uint32_t qa[8][2];
+    {
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
+                               (static_cast<size_t>(w.b) * p.n_kv * 4 + g * 4 + (live ? r0 : 0)) * 128;
+      const uint32_t* qw = reinterpret_cast<const uint32_t*>(q);
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    red_o[warp][h][lane] = o[h];
-    if (lane == 0) red_ml[warp][h] = make_float2(m[h], l[h]);
+      for (int kk = 0; kk < 8; ++kk) {
+        const int at = k8 ? kk * 8 + c2 : kk * 8 + c2 / 2;  // pairs of elements
+        qa[kk][0] = live ? ld_behind_wait(qw + at) : 0u;
+        qa[kk][1] = live ? ld_behind_wait(qw + at + (k8 ? 1 : 4)) : 0u;
+      }
+      if constexpr (k8) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) top = max(top, max(qa[kk][i] << 16 & 0x7F800000u, qa[kk][i] & 0x7F800000u));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = min(max(top, 1u << 23), 253u << 23);             // exponent field e
+        const float down = __uint_as_float((254u << 23) - top);  // 2^(127 - e)
+        scale *= __uint_as_float(top);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const __half2 v = __floats2half2_rn(bf16lo_to_f32(qa[kk][i]) * down, bf16hi_to_f32(qa[kk][i]) * down);
+            qa[kk][i] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+      }
+    }
+
+    float o[16][4];  // [set of eight columns]: rows r0 (0, 1) and r0 + 8 (2, 3: nothing)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m = -INFINITY, l = 0.f;  // l: of this lane's columns
+
+    // One stage, whose first key is k0 of the piece; kTail: keys past the last one are left out.
+    auto stage = [&](auto tail, uint32_t k_addr, uint32_t v_addr, int last) {
+      constexpr bool kTail = decltype(tail)::value;
+      float sc[kBlocks][2][4];
+#pragma unroll
+      for (int blk = 0; blk < kBlocks; ++blk) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) sc[blk][n][0] = sc[blk][n][1] = sc[blk][n][2] = sc[blk][n][3] = 0.f;
+        const uint32_t ka = k_addr + blk * 16 * kRow;  // (boxes of 16 and more slots, or rows of 128 bytes)
+        if constexpr (k8) {
+#pragma unroll
+          for (int kk = 0; kk < 8; kk += 2) {
+            uint32_t b[2][2][2];
+            rd0.keys2(ka, kk, b);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int n = 0; n < 2; ++n) mma_16816(sc[blk][n], qa[kk + s][0], qa[kk + s][1], b[s][n][0], b[s][n][1], E());
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            uint32_t b[2][2];
+            rd0.keys(ka, kk, b);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) mma_16816(sc[blk][n], qa[kk][0], qa[kk][1], b[n][0], b[n][1], E());
+          }
+        }
+      }
+      // this lane's columns are keys kb + 8 n + c2, + 1 of each block
+      const int kb = warp * 16 * kBlocks;
+      if (kTail) {
+#pragma unroll
+        for (int blk = 0; blk < kBlocks; ++blk)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (kb + blk * 16 + n * 8 + c2 + e >= last) sc[blk][n][e] = -INFINITY;
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int blk = 0; blk < kBlocks; ++blk)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) mx = max3f(mx, sc[blk][n][0], sc[blk][n][1]);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float m_new = fmaxf(m, mx * scale);
+      const float mu = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = fast_exp2(m - mu);
+      m = m_new;
+      l *= alpha;
+      uint32_t pa[kBlocks][2];
+#pragma unroll
+      for (int blk = 0; blk < kBlocks; ++blk)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float x = fast_exp2(fmaf(sc[blk][n][0], scale, PagedTile<E>::kShift - mu));
+          const float y = fast_exp2(fmaf(sc[blk][n][1], scale, PagedTile<E>::kShift - mu));
+          l += x + y;
+          if constexpr (k8) {
+            const __half2 v = __floats2half2_rn(x, y);
+            pa[blk][n] = *reinterpret_cast<const uint32_t*>(&v);
+          } else {
+            pa[blk][n] = pack_bf16x2(x, y);
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        o[i][0] *= alpha;
+        o[i][1] *= alpha;
+      }
+#pragma unroll
+      for (int blk = 0; blk < kBlocks; ++blk) {
+        const uint32_t va = v_addr + blk * 16 * kRow;
+        uint32_t seen[2] = {~0u, ~0u};  // of values of keys 2 c and 2 c + 1, and those 8 further on: 0 x NaN is not 0
+        if (kTail) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int left = last - (kb + blk * 16 + n * 8 + c2);
+            seen[n] = left >= 2 ? ~0u : left == 1 ? 0xFFFFu : 0u;
+          }
+        }
+        if constexpr (k8) {
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            uint32_t b[2][2][2];
+            rd0.template values2<kTail>(va, i, seen, b);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int n = 0; n < 2; ++n) mma_16816(o[2 * (i + s) + n], pa[blk][0], pa[blk][1], b[s][n][0], b[s][n][1], E());
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t b[2][2];
+            rd0.template values<kTail>(va, i, seen, b);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) mma_16816(o[2 * i + n], pa[blk][0], pa[blk][1], b[n][0], b[n][1], E());
+          }
+        }
+      }
+    };
+
+    bool ok = true;
+    for (int k0 = 0; k0 < keys; k0 += kKeys, ++item) {
+      const int s = item % kPagedStages;
+      ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[s], (item / kPagedStages) & 1, abort_flag, p.status));
+      if (!ok) break;
+      const uint32_t k_addr = smem_u32(smem + s * L::kStage), v_addr = k_addr + L::kHalf;
+      if (k0 + kKeys <= keys)
+        stage(std::false_type{}, k_addr, v_addr, 0);
+      else
+        stage(std::true_type{}, k_addr, v_addr, keys - k0);
+      if (bad_page[s]) l = __int_as_float(0x7fc00000);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty_bar[s]);
+    }
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+
+    // ---------------------------------------------------------- the warps' results
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) red_o[(warp * 4 + r0) * 128 + PagedReader<E>::column(i >> 1, i & 1, c2 + e)] = o[i][e];
+      if ((lane & 3) == 0) red_ml[warp * 4 + r0] = make_float2(m, l);
+    }
+    // one decision for all 128 consumer threads
+    if (!bar1_and_128(ok && !*abort_flag)) break;
+    const int d0 = lane * 4;  // of head `warp`
+    float M = -INFINITY, Ls = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) M = fmaxf(M, red_ml[v * 4 + warp].x);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const float2 ml = red_ml[v * 4 + warp];
+      const float f = fast_exp2(ml.x - (M == -INFINITY ? 0.f : M));
+      const float4 x = *reinterpret_cast<const float4*>(red_o + (v * 4 + warp) * 128 + d0);
+      Ls += f * ml.y;
+      acc = make_float4(acc.x + f * x.x, acc.y + f * x.y, acc.z + f * x.z, acc.w + f * x.w);
+    }
+    bool write = w.whole();
+    if (!write) {
+      const int slot = partial_slot(blockIdx.x, w.first > 0);
+      reinterpret_cast<float4*>(p.part_o)[(static_cast<size_t>(slot) * 4 + warp) * 32 + lane] = acc;
+      if (lane == 0) p.part_ml[slot * 4 + warp] = make_float2(M, Ls);
+      const int from = range_owner(range.total(), range.workers(), w.place(0));
+      const int to = range_owner(range.total(), range.workers(), w.place(w.tiles - 1));
+      int* counter = p.counters + w.b * p.n_kv + g;
+      __threadfence();
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (threadIdx.x == 0) *last_flag = atomicAdd(counter, 1) == to - from;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (*last_flag) {
+        // the unit's last piece to arrive joins them: lanes take the pieces' maxima and sums, then all their O
+        __threadfence();
+        write = true;
+        if (threadIdx.x == 0) *counter = 0;  // ready for the next call
+        auto at = [&](int v) { return partial_slot(v, v > from); };
+        M = -INFINITY;
+        for (int v = from + lane; v <= to; v += 32) M = fmaxf(M, __ldcg(&p.part_ml[at(v) * 4 + warp].x));
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
+        const float base = M == -INFINITY ? 0.f : M;
+        Ls = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int v = from; v <= to; ++v) {
+          const float2 ml = __ldcg(&p.part_ml[at(v) * 4 + warp]);
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (static_cast<size_t>(at(v)) * 4 + warp) * 32 + lane);
+          const float f = fast_exp2(ml.x - base);
+          Ls += f * ml.y;
+          acc = make_float4(acc.x + f * x.x, acc.y + f * x.y, acc.z + f * x.z, acc.w + f * x.w);
+        }
+      }
+    }
+    if (write) {
+      float inv = (k8 && p.pool.v_scale ? __ldcg(p.pool.v_scale + g) : 1.f) / Ls;
+      if (end == 0) inv = 0.f;
+      if (end < 0) {
+        inv = __int_as_float(0x7fc00000);
+        if (threadIdx.x == 0) atomicOr(p.status, kDevErrRange);
+      }
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.h) +
+                                (static_cast<size_t>(w.b) * p.n_kv * 4 + g * 4 + warp) * 128 + d0) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");  // the results' room is free for the next piece
   }
-  bad = __syncthreads_or(bad);
-  if (bad && threadIdx.x == 0) atomicOr(p.status, kDevErrRange);
-  if (warp >= 4) return;
-  float M = -INFINITY, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, red_ml[w][warp].x);
-  const float base = M == -INFINITY ? 0.f : M;
-  for (int w = 0; w < 8; ++w) {
-    const float f = fast_exp2(red_ml[w][warp].x - base);
-    const float4 v = red_o[w][warp][lane];
-    L += f * red_ml[w][warp].y;
-    acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
-  }
-  float inv = end == 0 ? 0.f : (p.pool.v_scale ? __ldg(p.pool.v_scale + g) : 1.f) / L;
-  if (bad) inv = __int_as_float(0x7fc00000);
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.h) + (static_cast<size_t>(b) * p.n_kv * 4 + g * 4 + warp) * 128 +
-                            4 * lane) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 }  // namespace gqa

@@ -12,6 +12,8 @@
 struct gqa_paged {
   int device, n_kv, dtype;
   gqa::PagedPool pool;
+  int log_box;             // slots of the maps' boxes: a power of two, at most 64, that divides the page
+  CUtensorMap map_k, map_v;
 };
 
 namespace gqa {

@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
     const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + src;
     const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + src;
     const uint4 ka = ld16(k + 8 * at.a), kb = ld16(k + 8 * at.b), va = ld16(v + 8 * at.a), vb = ld16(v + 8 * at.b);
-    const float ik = p.pool.k_scale ? 1.f / __ldg(p.pool.k_scale + g) : 1.f;
-    const float iv = p.pool.v_scale ? 1.f / __ldg(p.pool.v_scale + g) : 1.f;
+    const float ik = p.pool.k_scale ? 1.f / __ldcg(p.pool.k_scale + g) : 1.f;
+    const float iv = p.pool.v_scale ? 1.f / __ldcg(p.pool.v_scale + g) : 1.f;
     E* dk = static_cast<E*>(p.pool.k) + row + g * p.pool.head;
     E* dv = static_cast<E*>(p.pool.v) + row + g * p.pool.head;
     float x[8], y[8];

@@ -210,7 +210,14 @@ struct PagedAttnParams {
   const int* page_table;   // [B, max_pages]
   const int* kv_len;       // [B]
   void* h;                 // [B, 512 n_kv] bf16
+  int S_max;               // max_pages x page_size
+  int log_box;             // slots of a copy, a power of two that divides the page
+  int unit_cost;           // empty places of a unit in the CTAs' shares (kv_sched.h)
+  float* part_o;           // partial results of cut units: [2 CTAs][4 heads][128]
+  float2* part_ml;         // their (maximum, sum): [2 CTAs][4]
+  int* counters;           // [B n_kv] pieces of a unit that have arrived (zero between calls)
   int* status;
+  int fault;               // test hook: the last worker issues no loads (its waits run out)
   float scale_log2;        // log2(e) / sqrt(128)
 };
 
