@@ -24,8 +24,6 @@
 #pragma once
 
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
 #include <type_traits>
 
 #include "kv_sched.h"
@@ -68,10 +66,12 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
   mma_f16_16816(d, a0, 0u, a2, 0u, b0, b1);
 }
 
-// Two e4m3 numbers as fp16.
-__device__ __forceinline__ uint32_t halves_of(uint32_t e4m3x2) {
-  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(e4m3x2), __NV_E4M3);
-  return static_cast<uint32_t>(r.x) | static_cast<uint32_t>(r.y) << 16;
+// Four e4m3 numbers as fp16: the lower two and the upper two.
+__device__ __forceinline__ void halves_of(uint32_t e4m3x4, uint32_t& lower, uint32_t& upper) {
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+      : "=r"(lower), "=r"(upper)
+      : "r"(e4m3x4));
 }
 
 // What the consumers read of a stage.  Of a 16-key block starting at key k0, keys(kk) gives the B operands of
@@ -138,10 +138,7 @@ struct PagedReader<uint8_t> {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        b[s][n][0] = halves_of(r[2 * s + n] & 0xFFFFu);
-        b[s][n][1] = halves_of(r[2 * s + n] >> 16);
-      }
+      for (int n = 0; n < 2; ++n) halves_of(r[2 * s + n], b[s][n][0], b[s][n][1]);
   }
   template <bool kTail>
   __device__ __forceinline__ void values2(uint32_t v, int i, const uint32_t (&seen)[2], uint32_t (&b)[2][2][2]) const {
@@ -152,8 +149,7 @@ struct PagedReader<uint8_t> {
 #pragma unroll
       for (int n = 0; n < 2; ++n) {  // keys 0..7, 8..15
         const uint32_t x = __byte_perm(kTail ? r[2 * s + n] & seen[n] : r[2 * s + n], 0u, 0x3120);
-        b[s][0][n] = halves_of(x & 0xFFFFu);
-        b[s][1][n] = halves_of(x >> 16);
+        halves_of(x, b[s][0][n], b[s][1][n]);
       }
   }
   static __device__ __forceinline__ int column(int i, int s, int n) { return 16 * i + 2 * n + s; }
