@@ -103,9 +103,10 @@ inline EncodeTiledFn encode_fn() {
 }
 
 // Tensor map (bf16 unless `type` says otherwise) with 128-byte swizzle; dims[0] innermost; strides in
-// bytes for dims 1..
+// bytes for dims 1..; `fetch`: bytes of a row that a miss brings to L2 together.
 inline bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-              const uint32_t* box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
+              const uint32_t* box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              CUtensorMapL2promotion fetch = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t d[5], s[4];
@@ -117,7 +118,7 @@ inline bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t*
   }
   for (int i = 0; i < rank - 1; ++i) s[i] = strides[i];
   return fn(m, type, rank, const_cast<void*>(base), d, s, b, e,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, fetch,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

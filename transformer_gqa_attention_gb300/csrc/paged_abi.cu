@@ -69,7 +69,7 @@ bool map_pool(CUtensorMap* m, const void* base, const gqa_paged* g) {
     const uint64_t dims[4] = {128, slots, heads, n_pages};
     const uint64_t strides[3] = {static_cast<uint64_t>(p.pos), static_cast<uint64_t>(p.head), static_cast<uint64_t>(p.page)};
     const uint32_t shape[4] = {128, box, 1, 1};
-    return make_map(m, base, 4, dims, strides, shape, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+    return make_map(m, base, 4, dims, strides, shape, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
   }
   const uint64_t dims[5] = {64, slots, 2, heads, n_pages};
   const uint64_t strides[4] = {2 * static_cast<uint64_t>(p.pos), 128, 2 * static_cast<uint64_t>(p.head),

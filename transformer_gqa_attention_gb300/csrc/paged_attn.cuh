@@ -170,10 +170,16 @@ struct PagedRange {
   __device__ __forceinline__ void find(const PagedAttnParams& p) const {
     constexpr int kWarps = kPagedThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = (p.B + kPagedThreads - 1) / kPagedThreads, b0 = threadIdx.x * per, b1 = min(b0 + per, p.B);
-    auto places = [&](int len) { return (kv_tiles(kv_end(len, p.n_new, p.S_max)) + p.unit_cost) * p.n_kv; };
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) mine += places(__ldcg(p.kv_len + b));
+    constexpr int kMost = (1024 + kPagedThreads - 1) / kPagedThreads;  // sequences of a thread
+    const int per = (p.B + kPagedThreads - 1) / kPagedThreads, b0 = threadIdx.x * per;
+    int lens[kMost], places[kMost], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) lens[i] = i < per && b0 + i < p.B ? __ldcg(p.kv_len + b0 + i) : 0;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      places[i] = i < per && b0 + i < p.B ? (kv_tiles(kv_end(lens[i], p.n_new, p.S_max)) + p.unit_cost) * p.n_kv : 0;
+      mine += places[i];
+    }
     int x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -196,15 +202,15 @@ struct PagedRange {
       at[10] = lo;
       at[11] = hi - lo;
     }
-    if (lo >= before && lo < before + mine) {
-      int b = b0, from = before, len = __ldcg(p.kv_len + b);
-      while (lo >= from + places(len)) {
-        from += places(len);
-        len = __ldcg(p.kv_len + ++b);
+    int from = before;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      if (lo >= from && lo < from + places[i]) {
+        at[12] = b0 + i;
+        at[13] = lo - from;
+        at[14] = lens[i];
       }
-      at[12] = b;
-      at[13] = lo - from;
-      at[14] = len;
+      from += places[i];
     }
     __syncthreads();
   }
@@ -329,6 +335,9 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     const int end = kv_end(w.len, p.n_new, p.S_max);
     const int keys = piece_keys(w, end);
     const int g = w.u;
+    const bool whole = w.whole();
+    const int from = whole ? 0 : range_owner(range.total(), range.workers(), w.place(0));
+    const int to = whole ? 0 : range_owner(range.total(), range.workers(), w.place(w.tiles - 1));
     float scale = p.scale_log2 * (k8 && p.pool.k_scale ? __ldcg(p.pool.k_scale + g) : 1.f);
 
     // A operand: rows r0 (heads), all 128 elements in the order that the keys' registers have
@@ -514,38 +523,50 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
       Ls += f * ml.y;
       acc = make_float4(acc.x + f * x.x, acc.y + f * x.y, acc.z + f * x.z, acc.w + f * x.w);
     }
-    bool write = w.whole();
-    if (!write) {
+    bool write = whole;
+    if (!whole) {
       const int slot = partial_slot(blockIdx.x, w.first > 0);
       reinterpret_cast<float4*>(p.part_o)[(static_cast<size_t>(slot) * 4 + warp) * 32 + lane] = acc;
       if (lane == 0) p.part_ml[slot * 4 + warp] = make_float2(M, Ls);
-      const int from = range_owner(range.total(), range.workers(), w.place(0));
-      const int to = range_owner(range.total(), range.workers(), w.place(w.tiles - 1));
-      int* counter = p.counters + w.b * p.n_kv + g;
-      __threadfence();
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (threadIdx.x == 0) *last_flag = atomicAdd(counter, 1) == to - from;
+      // (releases what the barrier has gathered, and acquires what the pieces before have released)
+      int* counter = p.counters + w.b * p.n_kv + g;
+      if (threadIdx.x == 0) *last_flag = atomic_add_acq_rel(counter, 1) == to - from;
       asm volatile("bar.sync 1, 128;" ::: "memory");
       if (*last_flag) {
-        // the unit's last piece to arrive joins them: lanes take the pieces' maxima and sums, then all their O
-        __threadfence();
+        // the unit's last piece to arrive joins them, eight pieces' loads in flight together
         write = true;
         if (threadIdx.x == 0) *counter = 0;  // ready for the next call
-        auto at = [&](int v) { return partial_slot(v, v > from); };
+        constexpr int kAtOnce = 8;
         M = -INFINITY;
-        for (int v = from + lane; v <= to; v += 32) M = fmaxf(M, __ldcg(&p.part_ml[at(v) * 4 + warp].x));
-#pragma unroll
-        for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
-        const float base = M == -INFINITY ? 0.f : M;
         Ls = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int v = from; v <= to; ++v) {
-          const float2 ml = __ldcg(&p.part_ml[at(v) * 4 + warp]);
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (static_cast<size_t>(at(v)) * 4 + warp) * 32 + lane);
-          const float f = fast_exp2(ml.x - base);
-          Ls += f * ml.y;
-          acc = make_float4(acc.x + f * x.x, acc.y + f * x.y, acc.z + f * x.z, acc.w + f * x.w);
+        for (int v0 = from; v0 <= to; v0 += kAtOnce) {
+          float2 ml[kAtOnce];
+          float4 x[kAtOnce];
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const int v = min(v0 + i, to);
+            const size_t row = static_cast<size_t>(partial_slot(v, v > from)) * 4 + warp;
+            ml[i] = __ldcg(p.part_ml + row);
+            x[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + row * 32 + lane);
+          }
+          float top = M;
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, ml[i].x);
+          const float base = top == -INFINITY ? 0.f : top;
+          const float f0 = fast_exp2(M - base);
+          M = top;
+          Ls *= f0;
+          acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const float f = fast_exp2(ml[i].x - base);
+            if (v0 + i <= to) {  // (the others read the last one again, NaN or not)
+              Ls += f * ml[i].y;
+              acc = make_float4(acc.x + f * x[i].x, acc.y + f * x[i].y, acc.z + f * x[i].z, acc.w + f * x[i].w);
+            }
+          }
         }
       }
     }
