@@ -396,9 +396,10 @@ def attn_rope_init(layout, rot_dim, theta, scaling=None, factor=0.0, low=0.0, hi
 def attn_rope_apply(ctx, rope, x, n_tok, n_heads, stride, positions, out, out_stride, stream=None):
     """Rotate n_heads heads of n_tok tokens by positions [n_tok] int32; strides in elements between
     tokens; out may be x."""
-    _check("attn_rope_apply",
-           lib().attn_rope_apply(ctx, rope, _ptr(x), int(n_tok), int(n_heads), int(stride), _ptr(positions), _ptr(out),
-                                 int(out_stride), _stream(stream)))
+    st = (_lib or lib()).attn_rope_apply(ctx, rope, _ptr(x), n_tok, n_heads, stride, _ptr(positions), _ptr(out), out_stride,
+                                         _stream(stream))
+    if st:
+        _check("attn_rope_apply", st)
 
 
 def attn_rope_table(ctx, rope, positions, n_tok, R, stream=None):
@@ -428,18 +429,19 @@ def attn_paged_append(ctx, paged, k, v, B, T, stride_b, stride_t, rope, rope_pos
                       n_new=None, stream=None):
     """Write n_new[b] (None: T) keys, rotated by rope (None: as they are), and values behind kv_len[b];
     strides of k and v in elements between sequences and between tokens."""
-    _check("attn_paged_append",
-           lib().attn_paged_append(ctx, paged, _ptr(k), _ptr(v), int(B), int(T), int(stride_b), int(stride_t), rope,
-                                   _ptr(rope_pos), _ptr(page_table), int(max_pages), _ptr(kv_len), _ptr(n_new),
-                                   _stream(stream)))
+    st = (_lib or lib()).attn_paged_append(ctx, paged, _ptr(k), _ptr(v), B, T, stride_b, stride_t, rope, _ptr(rope_pos),
+                                           _ptr(page_table), max_pages, _ptr(kv_len), _ptr(n_new), _stream(stream))
+    if st:
+        _check("attn_paged_append", st)
 
 
 def attn_paged_decode_attention(ctx, paged, q_r, B, page_table, max_pages, kv_len, h, stream=None):
     """Attention of one token per sequence over keys 0 .. kv_len[b]-1 of a paged cache; page_table
     [B, max_pages] and kv_len [B] int32 on the device."""
-    _check("attn_paged_decode_attention",
-           lib().attn_paged_decode_attention(ctx, paged, _ptr(q_r), int(B), _ptr(page_table), int(max_pages),
-                                             _ptr(kv_len), _ptr(h), _stream(stream)))
+    st = (_lib or lib()).attn_paged_decode_attention(ctx, paged, _ptr(q_r), B, _ptr(page_table), max_pages, _ptr(kv_len),
+                                                     _ptr(h), _stream(stream))
+    if st:
+        _check("attn_paged_decode_attention", st)
 
 
 def attn_decode_paged(ctx, paged, x, B, R, page_table, max_pages, kv_len, delta, stream=None):

@@ -40,12 +40,27 @@ struct RopeLane {
   }
 };
 
-// cos and sin of a turning thread's eight pairs.
-__device__ __forceinline__ void rope_coefficients(const gqa_rope& r, const RopeLane& at, int i, int pos,
-                                                  float2 (&cs)[8]) {
-  if (!at.turns) return;
+// cos and sin of the eight pairs of threads i: kSubs threads with the same i, one for each of as many heads, lie
+// eight lanes apart and compute 8 / kSubs pairs each.  Called by whole warps.
+template <int kSubs>
+__device__ __forceinline__ void rope_coefficients(const gqa_rope& r, int pos, float2 (&cs)[8]) {
+  constexpr int kOwn = 8 / kSubs;
+  const int i = threadIdx.x & 7, sub = (threadIdx.x >> 3) & (kSubs - 1);
+  float2 own[kOwn];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) cs[j] = rope_cos_sin(r, 8 * i + j, pos);
+  for (int j = 0; j < kOwn; ++j) own[j] = rope_cos_sin(r, 8 * i + sub * kOwn + j, pos);
+  if constexpr (kSubs == 1) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cs[j] = own[j];
+    return;
+  }
+  // (lanes of this token begin at the last multiple of 8 kSubs)
+  const int from = (threadIdx.x & 31 & ~(8 * kSubs - 1)) + i;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    cs[j].x = __shfl_sync(0xffffffffu, own[j % kOwn].x, from + 8 * (j / kOwn));
+    cs[j].y = __shfl_sync(0xffffffffu, own[j % kOwn].y, from + 8 * (j / kOwn));
+  }
 }
 
 __device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
