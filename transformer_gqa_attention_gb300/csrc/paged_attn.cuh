@@ -55,7 +55,9 @@ struct PagedSmem {
   static constexpr int kRedBytes = 4 * 4 * 128 * 4 + 4 * 4 * 8;
   static constexpr int kBar = kRed + kRedBytes;
   static constexpr int kRange = kBar + 128;
-  static constexpr int kBytes = kRange + 64 + 1024;
+  static constexpr int kQ = kRange + 64;                // [stages] the queries of the piece that begins in the stage
+  static constexpr int kQBytes = 4 * 128 * 2;
+  static constexpr int kBytes = kQ + kPagedStages * kQBytes + 1024;
 };
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1,
@@ -301,7 +303,11 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         if (lane == 0) {
           bad_page[s] = wrong != 0;
           if (wrong) atomicOr(p.status, kDevErrRange);
-          mbar_arrive_expect_tx(&full_bar[s], static_cast<uint32_t>(__popc(copies)) * 2 * box * kRow);
+          mbar_arrive_expect_tx(&full_bar[s], static_cast<uint32_t>(__popc(copies)) * 2 * box * kRow + (k0 == 0 ? L::kQBytes : 0));
+          if (k0 == 0)  // the four heads' rows lie together
+            bulk_load(smem + L::kQ + s * L::kQBytes,
+                      static_cast<const __nv_bfloat16*>(p.q) + (static_cast<size_t>(w.b) * p.n_kv + w.u) * 512, L::kQBytes,
+                      &full_bar[s]);
         }
         __syncwarp();
         if (mine && fits) {
@@ -342,15 +348,13 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
 
     // A operand: rows r0 (heads), all 128 elements in the order that the keys' registers have
     uint32_t qa[8][2];
-    {
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
-                               (static_cast<size_t>(w.b) * p.n_kv * 4 + g * 4 + (live ? r0 : 0)) * 128;
-      const uint32_t* qw = reinterpret_cast<const uint32_t*>(q);
+    auto queries = [&](int s) {
+      const uint32_t* qw = reinterpret_cast<const uint32_t*>(smem + L::kQ + s * L::kQBytes) + (live ? r0 : 0) * 64;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         const int at = k8 ? kk * 8 + c2 : kk * 8 + c2 / 2;  // pairs of elements
-        qa[kk][0] = live ? ld_behind_wait(qw + at) : 0u;
-        qa[kk][1] = live ? ld_behind_wait(qw + at + (k8 ? 1 : 4)) : 0u;
+        qa[kk][0] = live ? qw[at] : 0u;
+        qa[kk][1] = live ? qw[at + (k8 ? 1 : 4)] : 0u;
       }
       if constexpr (k8) {
         uint32_t top = 0;
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
             qa[kk][i] = *reinterpret_cast<const uint32_t*>(&v);
           }
       }
-    }
+    };
 
     float o[16][4];  // [set of eight columns]: rows r0 (0, 1) and r0 + 8 (2, 3: nothing)
 #pragma unroll
@@ -488,6 +492,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
       const int s = item % kPagedStages;
       ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[s], (item / kPagedStages) & 1, abort_flag, p.status));
       if (!ok) break;
+      if (k0 == 0) queries(s);
       const uint32_t k_addr = smem_u32(smem + s * L::kStage), v_addr = k_addr + L::kHalf;
       if (k0 + kKeys <= keys)
         stage(std::false_type{}, k_addr, v_addr, 0);
@@ -534,18 +539,18 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
       if (threadIdx.x == 0) *last_flag = atomic_add_acq_rel(counter, 1) == to - from;
       asm volatile("bar.sync 1, 128;" ::: "memory");
       if (*last_flag) {
-        // the unit's last piece to arrive joins them, eight pieces' loads in flight together
+        // the unit's last piece to arrive joins them, eight or sixteen pieces' loads in flight together
         write = true;
         if (threadIdx.x == 0) *counter = 0;  // ready for the next call
-        constexpr int kAtOnce = 8;
         M = -INFINITY;
         Ls = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int v0 = from; v0 <= to; v0 += kAtOnce) {
+        auto join = [&](auto at_once, int v0) {
+          constexpr int kAtOnce = decltype(at_once)::value;
           float2 ml[kAtOnce];
           float4 x[kAtOnce];
 #pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) {
+          for (int i = 0; i < kAtOnce; ++i) {  // (past the last one: that one again)
             const int v = min(v0 + i, to);
             const size_t row = static_cast<size_t>(partial_slot(v, v > from)) * 4 + warp;
             ml[i] = __ldcg(p.part_ml + row);
@@ -560,14 +565,17 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
           Ls *= f0;
           acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
 #pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) {
-            const float f = fast_exp2(ml[i].x - base);
-            if (v0 + i <= to) {  // (the others read the last one again, NaN or not)
+          for (int i = 0; i < kAtOnce; ++i)
+            if (v0 + i <= to) {
+              const float f = fast_exp2(ml[i].x - base);
               Ls += f * ml[i].y;
               acc = make_float4(acc.x + f * x[i].x, acc.y + f * x[i].y, acc.z + f * x[i].z, acc.w + f * x[i].w);
             }
-          }
-        }
+        };
+        if (to - from < 8)
+          join(std::integral_constant<int, 8>{}, from);
+        else
+          for (int v0 = from; v0 <= to; v0 += 16) join(std::integral_constant<int, 16>{}, v0);
       }
     }
     if (write) {
