@@ -158,12 +158,11 @@ gqa_status gqa::run_paged_attn(gqa_ctx* c, const gqa_paged* g, const void* q, in
   p.status = c->status;
   p.scale_log2 = kScaleLog2;
   p.fault = take_fault(c, GQA_KERNEL_PAGED_ATTN);
-  // as many CTAs as fit, or as the longest sequences that the table allows have places for
+  // a CTA per range and kv head: as many as fit, or as the longest sequences that the table allows have places for
   const size_t tiles = (static_cast<size_t>(p.S_max) + kKvTile - 1) / kKvTile;
-  const size_t places = static_cast<size_t>(B) * c->n_kv * (tiles + p.unit_cost);
-  const int ctas = static_cast<int>(std::min<size_t>(l.ctas, places));
+  const int ranges = static_cast<int>(std::min<size_t>(l.ctas / c->n_kv, static_cast<size_t>(B) * (tiles + p.unit_cost)));
   ProfScope ps(c, GQA_KERNEL_PAGED_ATTN, s);
-  GQA_CUDA(launch_paged_attn(g->map_k, g->map_v, p, g->dtype, ctas, s));
+  GQA_CUDA(launch_paged_attn(g->map_k, g->map_v, p, g->dtype, ranges * c->n_kv, s));
   return GQA_OK;
 }
 

@@ -157,7 +157,7 @@ struct PagedReader<uint8_t> {
   static __device__ __forceinline__ int column(int i, int s, int n) { return 16 * i + 2 * n + s; }
 };
 
-// A worker's share of the places (kv_sched.h): thread i sums those of sequences i per .. i per + per - 1;
+// A worker's range of the places (kv_sched.h, one unit a sequence): thread i sums those of sequences i per .. i per + per - 1;
 // a scan over the CTA gives the total and finds where the share starts.
 struct PagedRange {
   int* at;  // [5] per-warp sums, then total, workers, first place, places, sequence, offset in it, its length
@@ -179,7 +179,7 @@ struct PagedRange {
     for (int i = 0; i < kMost; ++i) lens[i] = i < per && b0 + i < p.B ? __ldcg(p.kv_len + b0 + i) : 0;
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
-      places[i] = i < per && b0 + i < p.B ? (kv_tiles(kv_end(lens[i], p.n_new, p.S_max)) + p.unit_cost) * p.n_kv : 0;
+      places[i] = i < per && b0 + i < p.B ? kv_tiles(kv_end(lens[i], p.n_new, p.S_max)) + p.unit_cost : 0;
       mine += places[i];
     }
     int x = mine;
@@ -196,7 +196,7 @@ struct PagedRange {
       if (w < warp) before += at[w];
       all += at[w];
     }
-    const int n = range_workers(all, gridDim.x), c = blockIdx.x;
+    const int n = range_workers(all, gridDim.x / p.n_kv), c = blockIdx.x / p.n_kv;
     const int lo = c < n ? range_start(all, n, c) : all, hi = c < n ? range_start(all, n, c + 1) : all;
     if (threadIdx.x == 0) {
       at[8] = all;
@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
   range.find(p);
   KvWalk w = range.walk(p);
   auto len_of = [&](int b) { return __ldcg(p.kv_len + b); };
+  const int g = blockIdx.x % p.n_kv;  // kv head: the CTAs of a range read the same pages at the same time
 
   if (warp == 4) {
     // ------------------------------------------------------------------ producer
@@ -265,10 +266,10 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     const int per_page = p.pool.page_size >> p.log_box;  // boxes
     const int per_stage = kKeys >> p.log_box;
     // test hook: the last worker issues no loads, so its consumers wait out and abort
-    const bool no_loads = p.fault && static_cast<int>(blockIdx.x) == range.workers() - 1;
+    const bool no_loads = p.fault && static_cast<int>(blockIdx.x) == range.workers() * p.n_kv - 1;
     int issued = 0;
     bool ok = !no_loads;
-    for (; ok && !w.done(); w.next(p.n_kv, p.n_new, p.S_max, len_of)) {
+    for (; ok && !w.done(); w.next(1, p.n_new, p.S_max, len_of)) {
       const int end = kv_end(w.len, p.n_new, p.S_max);
       const int keys = piece_keys(w, end);
       const int* table = p.page_table + static_cast<size_t>(w.b) * p.max_pages;
@@ -306,18 +307,18 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
           mbar_arrive_expect_tx(&full_bar[s], static_cast<uint32_t>(__popc(copies)) * 2 * box * kRow + (k0 == 0 ? L::kQBytes : 0));
           if (k0 == 0)  // the four heads' rows lie together
             bulk_load(smem + L::kQ + s * L::kQBytes,
-                      static_cast<const __nv_bfloat16*>(p.q) + (static_cast<size_t>(w.b) * p.n_kv + w.u) * 512, L::kQBytes,
+                      static_cast<const __nv_bfloat16*>(p.q) + (static_cast<size_t>(w.b) * p.n_kv + g) * 512, L::kQBytes,
                       &full_bar[s]);
         }
         __syncwarp();
         if (mine && fits) {
           uint8_t* dst = smem + s * L::kStage + j * box * kRow;
           if constexpr (k8) {
-            tma_load_4d(dst, &tmK, &full_bar[s], 0, slot, w.u, page);
-            tma_load_4d(dst + L::kHalf, &tmV, &full_bar[s], 0, slot, w.u, page);
+            tma_load_4d(dst, &tmK, &full_bar[s], 0, slot, g, page);
+            tma_load_4d(dst + L::kHalf, &tmV, &full_bar[s], 0, slot, g, page);
           } else {
-            tma_load_5d(dst, &tmK, &full_bar[s], 0, slot, 0, w.u, page);
-            tma_load_5d(dst + L::kHalf, &tmV, &full_bar[s], 0, slot, 0, w.u, page);
+            tma_load_5d(dst, &tmK, &full_bar[s], 0, slot, 0, g, page);
+            tma_load_5d(dst + L::kHalf, &tmV, &full_bar[s], 0, slot, 0, g, page);
           }
         }
       }
@@ -337,10 +338,9 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
   float2* red_ml = reinterpret_cast<float2*>(red_o + 4 * 512);  // [4 warps][4 heads]
   const PagedReader<E> rd0(lane, warp * 16 * kBlocks, p.log_box);
   int item = 0;
-  for (; !w.done(); w.next(p.n_kv, p.n_new, p.S_max, len_of)) {
+  for (; !w.done(); w.next(1, p.n_new, p.S_max, len_of)) {
     const int end = kv_end(w.len, p.n_new, p.S_max);
     const int keys = piece_keys(w, end);
-    const int g = w.u;
     const bool whole = w.whole();
     const int from = whole ? 0 : range_owner(range.total(), range.workers(), w.place(0));
     const int to = whole ? 0 : range_owner(range.total(), range.workers(), w.place(w.tiles - 1));
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     }
     bool write = whole;
     if (!whole) {
-      const int slot = partial_slot(blockIdx.x, w.first > 0);
+      const int slot = partial_slot(blockIdx.x / p.n_kv, w.first > 0) * p.n_kv + g;
       reinterpret_cast<float4*>(p.part_o)[(static_cast<size_t>(slot) * 4 + warp) * 32 + lane] = acc;
       if (lane == 0) p.part_ml[slot * 4 + warp] = make_float2(M, Ls);
       asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
 #pragma unroll
           for (int i = 0; i < kAtOnce; ++i) {  // (past the last one: that one again)
             const int v = min(v0 + i, to);
-            const size_t row = static_cast<size_t>(partial_slot(v, v > from)) * 4 + warp;
+            const size_t row = static_cast<size_t>(partial_slot(v, v > from) * p.n_kv + g) * 4 + warp;
             ml[i] = __ldcg(p.part_ml + row);
             x[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + row * 32 + lane);
           }
