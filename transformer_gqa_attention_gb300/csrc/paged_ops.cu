@@ -11,7 +11,7 @@
 namespace gqa {
 
 namespace {
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
 __device__ __forceinline__ uint4 ld16(const void* p) { return ld_behind_wait(static_cast<const uint4*>(p)); }
@@ -22,7 +22,7 @@ __device__ __forceinline__ uint4 ld16(const void* p) { return ld_behind_wait(sta
 // per head, kAhead times four heads at a time, whose angles are the same.  The first heads are loaded
 // while sine and cosine are computed.
 template <int kAhead>
-__global__ void __launch_bounds__(kThreads, 4) rope_apply_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) rope_apply_kernel(const __grid_constant__ RopeParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
