@@ -453,6 +453,20 @@ def test_queries_of_any_size_against_e4m3_keys():
         check(c, q, t, lens, h)
 
 
+@pytest.mark.parametrize("scale", [1e-30, 1e-7, 1.0])
+def test_queries_of_nothing_against_e4m3_keys(scale):
+    """Scores that are all the same however small the scale: the mean of the values, also behind keys that are left out."""
+    c = Cache(8, 32, 2, True, seed=12)
+    t, lens = np.arange(8, dtype=np.int32).reshape(2, 4), [100, 37]
+    scrub(c, t, lens)
+    c.scales[0].fill_(scale)
+    for size in (0.0, 1e-38):
+        q = query(2, 2, size=size)
+        h = attend(c, q, t, lens)
+        assert not reported(c.ctx)
+        check(c, q, t, lens, h)
+
+
 def test_pools_past_two_to_the_32():
     """Pages whose byte offsets (and element offsets) pass 2^32."""
     n_pages, page = 36000, 128

@@ -140,6 +140,31 @@ def test_decode_step_against_the_oracle():
         blk.close()
 
 
+@pytest.mark.parametrize("n_kv,first", [(2, 4), (1, 7), (3, 0)])
+def test_decode_step_of_a_head_shard(n_kv, first):
+    """The shard's partial Delta over pages against its Delta over a dense cache."""
+    B, T, page = 3, 29, 16
+    inp = gin.make_custom(seed=960 + n_kv, B=B, T=T)
+    rows = lambda w, n: w[n * first:n * (first + n_kv)].contiguous().to(DEV)  # noqa: E731
+    ctx = abi.attn_create_shard(rows(inp.wq, 512), rows(inp.wk, 128), rows(inp.wv, 128),
+                                inp.wo[:, 512 * first:512 * (first + n_kv)].contiguous().to(DEV), n_kv)
+    try:
+        dense = [torch.zeros(B, T + 1, n_kv, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        delta = torch.empty(B, T, 4096, device=DEV)
+        abi.attn_prefill(ctx, inp.x.to(DEV), B, T, inp.R.to(DEV), True, *dense, T + 1, 0, delta)
+        pools = Pools(ctx, 8, page, n_kv=n_kv)
+        table = ints([[5, 2], [0, 7], [3, 1]])
+        abi.attn_paged_append(ctx, pools.p, *dense, B, T, (T + 1) * n_kv * 128, n_kv * 128, None, None, table, 2, ints([0] * B))
+        x, R1 = inp.x[:, :1].contiguous().to(DEV), gin.rope_table([T]).to(DEV)
+        got, want = torch.empty(B, 1, 4096, device=DEV), torch.empty(B, 1, 4096, device=DEV)
+        abi.attn_decode_paged(ctx, pools.p, x, B, R1.expand(B, 64, 2).contiguous(), table, 2, ints([T] * B), got)
+        abi.attn_decode(ctx, x, B, T, R1, *dense, T + 1, want)
+        abi.attn_sync_status(ctx)
+        gu.assert_close(gu.np64(got), gu.np64(want))
+    finally:
+        abi.attn_destroy(ctx)
+
+
 def _zero_context(n_kv):
     z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
     ctx = abi.attn_create_shard(z(512 * n_kv, 4096), z(128 * n_kv, 4096), z(128 * n_kv, 4096), z(4096, 512 * n_kv), n_kv)

@@ -366,7 +366,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         top = min(max(top, 1u << 23), 253u << 23);             // exponent field e
         const float down = __uint_as_float((254u << 23) - top);  // 2^(127 - e)
-        scale *= __uint_as_float(top);
+        // (a row of zeros or tiny numbers: not a scale of 0, which a key that is left out, -inf, would make NaN)
+        scale = fmaxf(scale * __uint_as_float(top), 0x1p-126f);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
 #pragma unroll

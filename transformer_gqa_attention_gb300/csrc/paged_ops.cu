@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
   if (live) {
     n = p.n_new ? __ldcg(p.n_new + b) : p.T;
     len = __ldcg(p.kv_len + b);
-    pos = (p.rope_pos ? __ldcg(p.rope_pos + b) : len) + t;
+    pos = static_cast<int>(static_cast<unsigned>(p.rope_pos ? __ldcg(p.rope_pos + b) : len) + t);  // (wraps)
     if (n < 0 || n > p.T || len < 0 || len > p.max_pages * p.pool.page_size - n) {
       if (t == 0 && g0 == 0 && i == 0) atomicOr(p.status, kDevErrRange);
       live = false;
