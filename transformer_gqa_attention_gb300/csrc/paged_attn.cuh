@@ -254,6 +254,13 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     tma_prefetch_desc(&tmV);
   }
   griddep_launch_dependents();
+  // The lengths and a table of at most 512 KB, which the cache has pushed out of L2 since the call before, are on their
+  // way there while the kernel in front ends: nothing is read yet that it may still write.
+  {
+    const int at = blockIdx.x * kPagedThreads + threadIdx.x, table_lines = static_cast<int>((4ll * p.B * p.max_pages + 127) >> 7);
+    if (at < table_lines && table_lines <= 4096) prefetch_l2(reinterpret_cast<const char*>(p.page_table) + at * 128);
+    if (threadIdx.x < (4 * p.B + 127) >> 7) prefetch_l2(reinterpret_cast<const char*>(p.kv_len) + threadIdx.x * 128);
+  }
   griddep_wait();  // lengths, queries and the new cache entries; the scratch of the call before
   range.find(p);
   KvWalk w = range.walk(p);
@@ -334,6 +341,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
   constexpr int kBlocks = kKeys / 64;  // 16-key blocks of a warp in a stage
   const int r0 = lane >> 2, c2 = (lane & 3) * 2;
   const bool live = r0 < 4;
+  const float k_scale = k8 && p.pool.k_scale ? __ldcg(p.pool.k_scale + g) : 1.f;
+  const float v_scale = k8 && p.pool.v_scale ? __ldcg(p.pool.v_scale + g) : 1.f;
   float* red_o = reinterpret_cast<float*>(smem + L::kRed);     // [4 warps][4 heads][128]
   float2* red_ml = reinterpret_cast<float2*>(red_o + 4 * 512);  // [4 warps][4 heads]
   const PagedReader<E> rd0(lane, warp * 16 * kBlocks, p.log_box);
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     const bool whole = w.whole();
     const int from = whole ? 0 : range_owner(range.total(), range.workers(), w.place(0));
     const int to = whole ? 0 : range_owner(range.total(), range.workers(), w.place(w.tiles - 1));
-    float scale = p.scale_log2 * (k8 && p.pool.k_scale ? __ldcg(p.pool.k_scale + g) : 1.f);
+    float scale = p.scale_log2 * k_scale;
 
     // A operand: rows r0 (heads), all 128 elements in the order that the keys' registers have
     uint32_t qa[8][2];
@@ -580,7 +589,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
       }
     }
     if (write) {
-      float inv = (k8 && p.pool.v_scale ? __ldcg(p.pool.v_scale + g) : 1.f) / Ls;
+      float inv = v_scale / Ls;
       if (end == 0) inv = 0.f;
       if (end < 0) {
         inv = __int_as_float(0x7fc00000);
