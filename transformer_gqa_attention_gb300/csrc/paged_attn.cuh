@@ -51,8 +51,9 @@ constexpr int kPagedThreads = 160;
 struct PagedSmem {
   static constexpr int kHalf = 64 * 128 * 2;  // K or V of a stage: 64 keys of bf16 or 128 of e4m3
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kRed = kPagedStages * kStage;  // the consumers' results: [4 warps][4 heads][128], then (m, l)
-  static constexpr int kRedBytes = 4 * 4 * 128 * 4 + 4 * 4 * 8;
+  static constexpr int kRed = kPagedStages * kStage;  // the consumers' results: [4 warps][4 heads][kRedRow], then (m, l)
+  static constexpr int kRedRow = 136;  // floats: heads lie 8 banks apart
+  static constexpr int kRedBytes = 4 * 4 * kRedRow * 4 + 4 * 4 * 8;
   static constexpr int kBar = kRed + kRedBytes;
   static constexpr int kRange = kBar + 128;
   static constexpr int kQ = kRange + 64;                // [stages] the queries of the piece that begins in the stage
@@ -116,8 +117,11 @@ struct PagedReader<__nv_bfloat16> {
       }
     }
   }
-  // d of column n of set s of values(i)
-  static __device__ __forceinline__ int column(int i, int s, int n) { return 16 * i + 8 * s + n; }
+  // the four results of a lane's sets 2 i and 2 i + 1 (of columns 16 i + c2, + 1 and 8 further on) into a head's row
+  static __device__ __forceinline__ void put(float* row, int i, int c2, const float (&x)[4], const float (&y)[4]) {
+    *reinterpret_cast<float2*>(row + 16 * i + c2) = make_float2(x[0], x[1]);
+    *reinterpret_cast<float2*>(row + 16 * i + 8 + c2) = make_float2(y[0], y[1]);
+  }
 };
 
 // A row is 128 bytes, 128-byte swizzle.  A 4-byte register of ldmatrix holds elements 4 c .. 4 c + 3 (c = lane & 3)
@@ -154,7 +158,9 @@ struct PagedReader<uint8_t> {
         halves_of(x, b[s][0][n], b[s][1][n]);
       }
   }
-  static __device__ __forceinline__ int column(int i, int s, int n) { return 16 * i + 2 * n + s; }
+  static __device__ __forceinline__ void put(float* row, int i, int c2, const float (&x)[4], const float (&y)[4]) {
+    *reinterpret_cast<float4*>(row + 16 * i + 2 * c2) = make_float4(x[0], y[0], x[1], y[1]);
+  }
 };
 
 // A worker's range of the places (kv_sched.h, one unit a sequence): thread i sums those of sequences i per .. i per + per - 1;
@@ -343,8 +349,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
   const bool live = r0 < 4;
   const float k_scale = k8 && p.pool.k_scale ? __ldcg(p.pool.k_scale + g) : 1.f;
   const float v_scale = k8 && p.pool.v_scale ? __ldcg(p.pool.v_scale + g) : 1.f;
-  float* red_o = reinterpret_cast<float*>(smem + L::kRed);     // [4 warps][4 heads][128]
-  float2* red_ml = reinterpret_cast<float2*>(red_o + 4 * 512);  // [4 warps][4 heads]
+  float* red_o = reinterpret_cast<float*>(smem + L::kRed);               // [4 warps][4 heads][kRedRow]
+  float2* red_ml = reinterpret_cast<float2*>(red_o + 16 * L::kRedRow);  // [4 warps][4 heads]
   const PagedReader<E> rd0(lane, warp * 16 * kBlocks, p.log_box);
   int item = 0;
   for (; !w.done(); w.next(1, p.n_new, p.S_max, len_of)) {
@@ -518,9 +524,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     // ---------------------------------------------------------- the warps' results
     if (live) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) red_o[(warp * 4 + r0) * 128 + PagedReader<E>::column(i >> 1, i & 1, c2 + e)] = o[i][e];
+      for (int i = 0; i < 8; ++i) PagedReader<E>::put(red_o + (warp * 4 + r0) * L::kRedRow, i, c2, o[2 * i], o[2 * i + 1]);
       if ((lane & 3) == 0) red_ml[warp * 4 + r0] = make_float2(m, l);
     }
     // one decision for all 128 consumer threads
@@ -534,7 +538,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     for (int v = 0; v < 4; ++v) {
       const float2 ml = red_ml[v * 4 + warp];
       const float f = fast_exp2(ml.x - (M == -INFINITY ? 0.f : M));
-      const float4 x = *reinterpret_cast<const float4*>(red_o + (v * 4 + warp) * 128 + d0);
+      const float4 x = *reinterpret_cast<const float4*>(red_o + (v * 4 + warp) * L::kRedRow + d0);
       Ls += f * ml.y;
       acc = make_float4(acc.x + f * x.x, acc.y + f * x.y, acc.z + f * x.z, acc.w + f * x.w);
     }
