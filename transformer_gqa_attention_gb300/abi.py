@@ -172,9 +172,7 @@ def _stream(stream) -> int | None:
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is None:
             return torch.cuda.current_stream().cuda_stream
-        if not torch.cuda.is_initialized():
-            torch.cuda.init()
-        return raw(torch.cuda.current_device())
+        return raw(torch.cuda.current_device())  # (which initialises CUDA)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

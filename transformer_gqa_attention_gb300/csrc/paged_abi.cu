@@ -151,6 +151,7 @@ gqa_status gqa::run_paged_attn(gqa_ctx* c, const gqa_paged* g, const void* q, in
   p.h = h;
   p.S_max = max_pages * g->pool.page_size;
   p.log_box = g->log_box;
+  // (with 0, 1, 2 and 4, us: 16 sequences of up to 4096 keys 29.4, 28.4, 27.5, 27.6; 64 of up to 8192 e4m3 97, 92, 89, 90)
   p.unit_cost = kUnitCostDecode;
   p.part_o = reinterpret_cast<float*>(c->cache_ws.p + l.part_o);
   p.part_ml = reinterpret_cast<float2*>(c->cache_ws.p + l.part_ml);
@@ -344,10 +345,8 @@ gqa_status attn_paged_decode_attention(gqa_ctx* c, const gqa_paged* g, const voi
   if (overlap(h, heads, q_r, heads) || overlap(h, heads, kv_len, 4 * static_cast<size_t>(B)) ||
       overlap(h, heads, page_table, 4 * static_cast<size_t>(B) * max_pages))
     return GQA_ERR_INVALID_ARG;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((st = reserve_paged_attn(c, s)) != GQA_OK) return st;
   CallRange range("gqa.attn_paged_decode_attention");
-  return run_paged_attn(c, g, q_r, B, page_table, max_pages, kv_len, 0, h, s);
+  return run_paged_attn(c, g, q_r, B, page_table, max_pages, kv_len, 0, h, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
