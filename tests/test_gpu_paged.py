@@ -376,6 +376,57 @@ def test_attention_of_the_most_sequences():
     check(c, q, t, lens, h)
 
 
+@pytest.mark.parametrize("order", [(2, 0, 1), (1, 0, 2), (1, 2, 0), (2, 1, 0)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_pools_in_other_orders(order, e4m3):
+    """Pages, slots and heads in any order in memory, with room between them: append, then attend."""
+    n_pages, page, n_kv, B = 7, 24, 3, 3
+    rng = np.random.default_rng(sum(order) + 4 * e4m3)
+    kind = torch.uint8 if e4m3 else torch.bfloat16
+    extent = (n_pages, page, n_kv)
+    place = [extent[i] + (2 if i == order[1] else 0) for i in order]  # two more of the middle extent than are used
+    c = Cache.__new__(Cache)
+    c.n_pages, c.page, c.n_kv, c.e4m3, c.heads_first, c.ctx = n_pages, page, n_kv, e4m3, False, context(n_kv)
+    whole = [torch.full((*place, 144), 0x7F if e4m3 else NAN, dtype=kind, device=DEV) for _ in range(2)]
+    back = [order.index(i) for i in range(3)]
+    c.k, c.v = (w.permute(*back, 3)[:n_pages, :page, :n_kv, :128] for w in whole)
+    c.scales = (torch.full((8,), 0.03, device=DEV), torch.full((8,), 0.02, device=DEV)) if e4m3 else (None, None)
+    c.p = abi.attn_paged_create(c.ctx, c.k, c.v, n_pages, page, "e4m3" if e4m3 else "bf16", *c.k.stride()[:3], *c.scales)
+    lens, t = [70, 24, 1], np.array([[4, 0, 6], [2, -1, -1], [5, 9, 9]], dtype=np.int32)
+    new = torch.from_numpy(rng.standard_normal((2, B, 70, n_kv, 128))).to(torch.bfloat16).to(DEV)
+    abi.attn_paged_append(c.ctx, c.p, new[0], new[1], B, 70, new.stride(1), new.stride(2), None, None, ints(t), 3, ints([0] * B),
+                          ints(lens))
+    assert not reported(c.ctx)
+    q = query(B, n_kv)
+    h = attend(c, q, t, lens)
+    assert not reported(c.ctx)
+    check(c, q, t, lens, h)
+    held = [c.k.clone(), c.v.clone()]
+    for i, pool in enumerate((c.k, c.v)):  # what is not a held slot is as it was
+        for b, n in enumerate(lens):
+            at = np.arange(n)
+            pool[torch.from_numpy(t[b, at // page].astype(np.int64)), torch.from_numpy(at % page)] = 0x7F if e4m3 else NAN
+        assert torch.equal(whole[i].view(torch.uint8), torch.full_like(whole[i], 0x7F if e4m3 else NAN).view(torch.uint8))
+        assert not torch.equal(held[i].view(torch.uint8), pool.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn_geometries(seed):
+    rng = np.random.default_rng(1000 + seed)
+    n_kv, page = int(rng.choice([1, 2, 3, 4, 5, 7, 8])), 8 * int(rng.choice([1, 2, 3, 4, 5, 8, 11, 16, 32, 40]))
+    e4m3, B = bool(rng.integers(0, 2)), int(rng.choice([1, 2, 3, 7, 20, 45]))
+    top = int(rng.choice([10, 130, 700, 2500, 9000 if B < 4 else 900]))
+    lens = [int(n) for n in rng.integers(0, top + 1, B)]
+    n_pages = sum(-(-n // page) for n in lens) + 1
+    c = Cache(n_pages, page, n_kv, e4m3, bool(rng.integers(0, 2)), bool(rng.integers(0, 2)), seed=seed)
+    t = tables(lens, page, n_pages, seed=seed, room=int(rng.integers(0, 5)))
+    scrub(c, t, lens)
+    q = query(B, n_kv, seed)
+    h = attend(c, q, t, lens)
+    assert not reported(c.ctx)
+    check(c, q, t, lens, h)
+
+
 def test_sequences_that_share_pages():
     c = Cache(12, 64, 8, True, seed=5)
     t = np.array([[3, 4, 5], [3, 4, 6], [3, 3, 3], [9, 4, 3]], dtype=np.int32)
