@@ -553,6 +553,85 @@ def test_pools_past_two_to_the_32():
         assert np.all(np.abs(gu.np64(h[b]).reshape(8, 4, 128) - ref) <= tol)
 
 
+# ------------------------------------------------------------------------------- the largest calls
+def test_the_most_tokens():
+    n = 262144
+    rope, w, gain = turn("halves", 32, "bands")
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(n, 256, generator=gen, device=DEV).to(torch.bfloat16)
+    pos = torch.randint(-1000000, 1000000, (n,), generator=gen, device=DEV, dtype=torch.int32)
+    out = torch.full((n + 1, 256), NAN, dtype=torch.bfloat16, device=DEV)
+    abi.attn_rope_apply(context(), rope, x, n, 2, 256, pos, out, 256)
+    R = torch.full((n + 1, 64, 2), NAN, device=DEV)
+    abi.attn_rope_table(context(), turn()[0], pos, n, R)
+    abi.attn_sync_status(context())
+    assert out[n].isnan().all() and not out[:n].isnan().any() and R[n].isnan().all() and not R[:n].isnan().any()
+    rows = np.r_[0:5, n // 2:n // 2 + 5, n - 5:n]
+    ref, size = po.rotate(gu.np64(x[rows]).reshape(-1, 2, 128), gu.np64(pos[rows]), "halves", w, gain)
+    got = gu.np64(out[rows]).reshape(-1, 2, 128)
+    assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -21 * gain * size)
+    ang = gu.np64(pos[rows])[:, None] * turn()[1]
+    assert np.all(np.abs(gu.np64(R[rows]) - np.stack([np.cos(ang), np.sin(ang)], -1)) <= 2.0 ** -21)
+    # as many new positions, of 1024 sequences, some of them left out
+    B, T, page = 1024, 256, 64
+    c = Cache(5 * B, page, 1, False, fill="nan")
+    new = torch.randint(0, T + 1, (B,), generator=gen, device=DEV, dtype=torch.int32)
+    lens = torch.randint(0, 64, (B,), generator=gen, device=DEV, dtype=torch.int32)
+    table = torch.randperm(5 * B, generator=gen, device=DEV).int().view(B, 5)
+    k = torch.randn(2, B, T, 128, generator=gen, device=DEV).to(torch.bfloat16)
+    abi.attn_paged_append(c.ctx, c.p, k[0], k[1], B, T, T * 128, 128, None, None, table, 5, lens, new)
+    assert not reported(c.ctx)
+    at = lens[:, None].long() + torch.arange(T, device=DEV)
+    live = torch.arange(T, device=DEV) < new[:, None]
+    where = torch.gather(table.long(), 1, at // page)[live], (at % page)[live]
+    for i, pool in enumerate((c.k, c.v)):
+        assert torch.equal(pool[where][:, 0], k[i][live])
+        assert int(pool.isnan().all(-1).logical_not().sum()) == int(new.sum())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_one_page_for_all_positions(e4m3):
+    """A page as long as the longest cache: a dense cache of several sequences described as pages."""
+    c = Cache(2, 1048576, 1, e4m3, seed=20)
+    lens, t = [90000, 1], np.array([[1], [0]], dtype=np.int32)
+    q = query(2, 1)
+    h = attend(c, q, t, lens)
+    assert not reported(c.ctx)
+    codes = [c.raw(i)[:, :lens[0]].contiguous().cpu() for i in range(2)]
+    x = [po.e4m3_values()[b.numpy()] * float(c.scales[i][0]) if e4m3 else b.view(torch.bfloat16).double().numpy()
+         for i, b in enumerate(codes)]
+    for b, n in enumerate(lens):
+        ref, mean, mag = po.decode(gu.np64(q[b]).reshape(1, 4, 128), x[0][t[b, 0], :n], x[1][t[b, 0], :n])
+        d = 2 * 2.0 ** -17 * 1.02 * mag / math.sqrt(128) + 2.0 ** -20
+        assert np.all(np.abs(gu.np64(h[b]).reshape(1, 4, 128) - ref)
+                      <= 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * (2.0 ** -8 + d) * mean)
+
+
+@pytest.mark.parametrize("given", [(False, False), (True, False), (False, True)])
+def test_scales_that_are_left_out_are_one(given):
+    c = Cache(6, 16, 2, True, seed=21)
+    abi.attn_paged_destroy(c.p)
+    held = tuple(s if g else None for s, g in zip(c.scales, given))
+    c.p = abi.attn_paged_create(c.ctx, c.k, c.v, 6, 16, "e4m3", *c.strides, *held)
+    c.scales = tuple(s if g else torch.ones(8, device=DEV) for s, g in zip(c.scales, given))
+    for pool in (c.k, c.v):
+        pool.fill_(0x7F)
+    t, n = np.array([[3, 0, 5]], dtype=np.int32), 41
+    new = torch.randn(2, 1, n, 2, 128, device=DEV).to(torch.bfloat16) * 0.25
+    abi.attn_paged_append(c.ctx, c.p, new[0], new[1], 1, n, 0, 256, None, None, ints(t), 3, ints([0]))
+    assert not reported(c.ctx)
+    at = np.arange(n)
+    for i in range(2):
+        got, ref = c.numbers(i)[t[0, at // 16], at % 16], gu.np64(new[i, 0])
+        scale = gu.np64(c.scales[i][:2])[:, None]
+        ref = np.clip(ref, -448 * scale, 448 * scale)
+        assert np.all(np.abs(got - ref) <= np.maximum((2.0 ** -4 + 2.0 ** -20) * np.abs(ref), 2.0 ** -10 * scale))
+    q = query(1, 2)
+    h = attend(c, q, t, [n])
+    assert not reported(c.ctx)
+    check(c, q, t, [n], h)
+
+
 # ------------------------------------------------------------------------------- refusals
 def test_descriptions_that_are_refused():
     ctx = context(8)

@@ -140,6 +140,50 @@ def test_decode_step_against_the_oracle():
         blk.close()
 
 
+@pytest.mark.parametrize("B", [2, 70])
+def test_captured_block_steps(B):
+    """A step of the block with its rotation table and its lengths in one graph, against the dense block step by step."""
+    T, page, steps = 21, 8, 14
+    inp = gin.make_custom(seed=970 + B, B=B, T=T)
+    blk = gu.Block(inp)
+    try:
+        ctx, S = blk.ctx, T + steps
+        dense = gu.empty_cache(B, S)
+        blk.prefill(inp.x.to(DEV), inp.R.to(DEV), *dense)
+        per = -(-S // page)
+        pools = Pools(ctx, B * per, page)
+        table, lens = ints(np.random.default_rng(B).permutation(B * per).reshape(B, per)), ints([0] * B)
+        abi.attn_paged_append(ctx, pools.p, *dense, B, T, S * 1024, 1024, None, None, table, per, lens)
+        lens += T
+        rope = abi.attn_rope_init("pairs", 128, gin.ROPE_THETA)
+        x = torch.empty(B, 1, 4096, dtype=torch.bfloat16, device=DEV)
+        R, got, want = torch.empty(B, 64, 2, device=DEV), torch.empty(B, 1, 4096, device=DEV), torch.empty(B, 1, 4096, device=DEV)
+
+        def step():
+            abi.attn_rope_table(ctx, rope, lens, B, R)
+            abi.attn_decode_paged(ctx, pools.p, x, B, R, table, per, lens, got)
+            lens.add_(1)
+
+        gen = torch.Generator(device=DEV).manual_seed(B)
+        g = torch.cuda.CUDAGraph()
+        for i in range(steps):
+            x.normal_(generator=gen)
+            if i == 0:
+                step()
+                torch.cuda.synchronize()
+                with torch.cuda.graph(g):
+                    step()
+            else:
+                g.replay()
+            abi.attn_sync_status(ctx)
+            abi.attn_decode(ctx, x, B, T + i, gin.rope_table([T + i]).to(DEV), *dense, S, want)
+            abi.attn_sync_status(ctx)
+            gu.assert_close(gu.np64(got), gu.np64(want), what=f"step {i}")
+        assert lens.tolist() == [S] * B
+    finally:
+        blk.close()
+
+
 @pytest.mark.parametrize("n_kv,first", [(2, 4), (1, 7), (3, 0)])
 def test_decode_step_of_a_head_shard(n_kv, first):
     """The shard's partial Delta over pages against its Delta over a dense cache."""
