@@ -364,6 +364,31 @@ def test_attention_of_long_and_ragged_batches(B, lens, e4m3):
         assert torch.equal(h[:B].view(torch.int16), again[:B].view(torch.int16))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n_kv,lens", [(1, [2000]), (1, [2200]), (1, [4100]), (1, [8200]), (1, [8400]), (1, [20000]),
+                                       (1, [39000, 900, 0, 17000]), (2, [30000]), (3, [19000, 40]), (4, [24000, 5000]),
+                                       (8, [6000]), (7, [11000, 300])])
+def test_units_of_many_pieces(n_kv, lens, e4m3):
+    """Up to a piece for every CTA: joined at once, in groups of eight and of sixteen."""
+    n_pages = sum(-(-n // 64) for n in lens) + 2
+    c = Cache(n_pages, 64, n_kv, e4m3, seed=n_kv)
+    t = tables(lens, 64, n_pages, seed=n_kv)
+    scrub(c, t, lens)
+    q = query(len(lens), n_kv, lens[0])
+    h = attend(c, q, t, lens)
+    assert not reported(c.ctx)
+    check(c, q, t, lens, h)
+    bits = h[:len(lens)].view(torch.int16).clone()
+    for _ in range(20):
+        assert torch.equal(attend(c, q, t, lens)[:len(lens)].view(torch.int16), bits)
+    if lens[0] > 5000:  # a page that is out of range, in the middle
+        bad = t.copy()
+        bad[0, 40] = -1
+        h = attend(c, q, bad, lens)
+        assert reported(c.ctx)
+        check(c, q, t, lens, h, left_out=(0,))
+
+
 def test_attention_of_the_most_sequences():
     lens = [(b * 37) % 90 for b in range(1024)]
     n_pages = sum(-(-n // 16) for n in lens) + 2

@@ -48,7 +48,7 @@ struct gqa_ctx {
   int* status = nullptr;           // device status word (kDevErr* bits)
   int* old_len = nullptr;          // [kDecodeMaxBatch] lengths before an eviction (behind the status word)
   int* zeros = nullptr;            // [kDecodeMaxBatch] zeros (behind old_len)
-  int* counters = nullptr;         // arrival counters of the decode split merge (kCounterInts)
+  int* counters = nullptr;         // arrival counters (kCounterInts, then kGroupCounterInts)
   gqa::DeviceBuffer ws;            // workspace of the block forms
   gqa::DeviceBuffer cache_ws;      // scratch of the attention over caches of per-sequence length
   std::vector<void*> retired;      // outgrown buffers that a captured graph may still use
@@ -81,6 +81,10 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 constexpr long long kMaxTokens = 262144;
 constexpr long long kMaxSMax = 1048576;
 constexpr int kDecodeMaxBatch = 1024;
+// Arrival counters: one per (sequence, kv group, position group), and behind them those of groups of pieces of the
+// attention over pages, two per CTA.
+constexpr int kCounterInts = kDecodeMaxBatch * 8;
+constexpr int kGroupCounterInts = 2048;
 
 // ------------------------------------------------------------------ tensor maps
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

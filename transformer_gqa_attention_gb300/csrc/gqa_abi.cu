@@ -27,8 +27,6 @@ void gqa::set_last_cuda_error(cudaError_t e) { g_last_cuda_error = static_cast<i
 namespace {
 
 constexpr int kSkinnyMaxTokens = 64;     // at or below: swap-AB split-K projections
-// Arrival counters of the decode split merge, one per (sequence, kv group, position group).
-constexpr int kCounterInts = kDecodeMaxBatch * 8;
 // Prefills of at most this many tokens per sequence run the decode attention kernel with
 // kShortPos positions per CTA instead of the flash kernel (whose 128-row query tiles they
 // would fill to an eighth at most) — unless the cache is long and the flash grid fills the
@@ -298,7 +296,7 @@ gqa_status create_impl(const void* wq, const void* wk, const void* wv, const voi
   const size_t rows = c->qkv_rows(), qc = c->q_cols(), kvc = c->kv_cols();
   if (cudaMalloc(&c->w_qkv, rows * 4096 * 2) != cudaSuccess || cudaMalloc(&c->w_o, 4096 * qc * 2) != cudaSuccess ||
       cudaMalloc(&c->status, (64 + 2 * kDecodeMaxBatch) * sizeof(int)) != cudaSuccess ||
-      cudaMalloc(&c->counters, kCounterInts * sizeof(int)) != cudaSuccess) {
+      cudaMalloc(&c->counters, (kCounterInts + kGroupCounterInts) * sizeof(int)) != cudaSuccess) {
     cudaGetLastError();
     return fail(GQA_ERR_OOM);
   }
@@ -306,7 +304,7 @@ gqa_status create_impl(const void* wq, const void* wk, const void* wv, const voi
   c->zeros = c->old_len + kDecodeMaxBatch;
   cudaError_t e = cudaMemsetAsync(c->status, 0, sizeof(int), s);
   if (e == cudaSuccess) e = cudaMemsetAsync(c->zeros, 0, kDecodeMaxBatch * sizeof(int), s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(c->counters, 0, kCounterInts * sizeof(int), s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(c->counters, 0, (kCounterInts + kGroupCounterInts) * sizeof(int), s);
   // k-block-major copies: W_Q rows 0..qc-1, W_K qc..qc+kvc-1, W_V qc+kvc.. of W_QKV; W_O
   if (e == cudaSuccess) e = copy_weight_tiled(c->w_qkv, wq, qc, 0, rows, 64, s);
   if (e == cudaSuccess) e = copy_weight_tiled(c->w_qkv, wk, kvc, qc, rows, 64, s);
@@ -726,7 +724,7 @@ gqa_status attn_sync_status(gqa_ctx* c, gqa_stream_t stream) {
   GQA_CUDA(cudaMemcpy(&v, c->status, sizeof(int), cudaMemcpyDeviceToHost));
   if (v != 0) {
     // an aborted kernel may have left arrival counters mid-count
-    GQA_CUDA(cudaMemset(c->counters, 0, kCounterInts * sizeof(int)));
+    GQA_CUDA(cudaMemset(c->counters, 0, (kCounterInts + kGroupCounterInts) * sizeof(int)));
     GQA_CUDA(cudaMemset(c->status, 0, sizeof(int)));
     if (v & kDevErrTimeout) return GQA_ERR_TIMEOUT;
     if (v & kDevErrRange) return GQA_ERR_SHAPE;

@@ -90,7 +90,7 @@ cudaError_t launch_evict_move(const EvictParams& p, cudaStream_t s);
 // Paged caches (dtype: GQA_CACHE_*) and rotation.
 cudaError_t configure_paged_attn();
 cudaError_t launch_paged_attn(const CUtensorMap& k, const CUtensorMap& v, const PagedAttnParams& p, int dtype, int n_ctas,
-                              cudaStream_t s);
+                              bool groups, cudaStream_t s);
 cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_rope_apply(const RopeParams& p, cudaStream_t s);
 cudaError_t launch_rope_table(const RopeParams& p, cudaStream_t s);

@@ -24,8 +24,8 @@
 //               come with a piece's first stage.
 //
 // A piece of a unit (sequence, kv head) that a CTA does not have to itself leaves an unnormalised partial
-// (O, maximum m, sum l) behind; the last CTA of the unit to arrive joins the pieces in their order, so
-// results do not depend on which one is last.
+// (O, maximum m, sum l) behind; the last CTA of the unit (where they are many: of each group of them, then of the groups) to arrive
+// joins the pieces in their order, so results do not depend on which one is last.
 //
 // Chunks of tiles taken from a counter instead of equal ranges, because the slowest CTA takes 3 to 8 % longer than the mean, cost
 // more at their ends than they gained (up to 2.5 % on the largest call, 10 to 40 % lost on the others).
@@ -254,7 +254,8 @@ __device__ __forceinline__ int piece_keys(const KvWalk& w, int end) {
   return max(0, min(end, (w.first + w.n) * kKvTile) - w.first * kKvTile);
 }
 
-template <typename E>
+// kGroups: units are expected to have more than 16 pieces, which are joined in groups.
+template <typename E, bool kGroups>
 __global__ void __launch_bounds__(kPagedThreads, 2)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ PagedAttnParams p) {
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
       acc = make_float4(acc.x + f * x.x, acc.y + f * x.y, acc.z + f * x.z, acc.w + f * x.w);
     }
     bool write = whole;
-    if (!whole) {
+    if (!kGroups && !whole) {
       const int slot = partial_slot(blockIdx.x / p.n_kv, w.first > 0) * p.n_kv + g;
       reinterpret_cast<float4*>(p.part_o)[(static_cast<size_t>(slot) * 4 + warp) * 32 + lane] = acc;
       if (lane == 0) p.part_ml[slot * 4 + warp] = make_float2(M, Ls);
@@ -616,6 +617,77 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
           join(std::integral_constant<int, 8>{}, from);
         else
           for (int v0 = from; v0 <= to; v0 += 16) join(std::integral_constant<int, 16>{}, v0);
+      }
+    }
+    if (kGroups && !whole) {
+      // piece i of the unit's n: where its partial result is
+      const int n = to - from + 1, range_no = blockIdx.x / p.n_kv;
+      auto slot = [&](int i) { return static_cast<size_t>(partial_slot(from + i, i > 0) * p.n_kv + g); };
+      auto leave = [&](int i) {
+        const size_t row = slot(i) * 4 + warp;
+        reinterpret_cast<float4*>(p.part_o)[row * 32 + lane] = acc;
+        if (lane == 0) p.part_ml[row] = make_float2(M, Ls);
+      };
+      leave(range_no - from);
+      // More than 16 pieces are joined in groups of 8 (of more than 64: of 16), whose results take the place of their first
+      // piece's, and then those.
+      const int log_group = n > 64 ? 4 : n > 16 ? 3 : 0;
+      int first = 0, count = n, log_step = 0;
+      if (log_group) {
+        first = (range_no - from) >> log_group << log_group;
+        count = min(1 << log_group, n - first);
+      }
+      while (true) {
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        // (releases what the barrier has gathered, and acquires what those before have released)
+        int* counter = log_group != log_step ? p.group_counters + slot(first) : p.counters + w.b * p.n_kv + g;
+        if (threadIdx.x == 0) *last_flag = atomic_add_acq_rel(counter, 1) == count - 1;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (!*last_flag) break;
+        // the last one to be done joins all, eight or sixteen pieces' loads in flight together
+        if (threadIdx.x == 0) *counter = 0;  // ready for the next call
+        M = -INFINITY;
+        Ls = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto join = [&](auto at_once, int i0) {
+          constexpr int kAtOnce = decltype(at_once)::value;
+          float2 ml[kAtOnce];
+          float4 x[kAtOnce];
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {  // (past the last one: that one again)
+            const size_t row = slot(first + (min(i0 + i, count - 1) << log_step)) * 4 + warp;
+            ml[i] = __ldcg(p.part_ml + row);
+            x[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + row * 32 + lane);
+          }
+          float top = M;
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, ml[i].x);
+          const float base = top == -INFINITY ? 0.f : top;
+          const float f0 = fast_exp2(M - base);
+          M = top;
+          Ls *= f0;
+          acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i)
+            if (i0 + i < count) {
+              const float f = fast_exp2(ml[i].x - base);
+              Ls += f * ml[i].y;
+              acc = make_float4(acc.x + f * x[i].x, acc.y + f * x[i].y, acc.z + f * x[i].z, acc.w + f * x[i].w);
+            }
+        };
+        if (count <= 8)
+          join(std::integral_constant<int, 8>{}, 0);
+        else
+          for (int i0 = 0; i0 < count; i0 += 16) join(std::integral_constant<int, 16>{}, i0);
+        if (log_group == log_step) {
+          write = true;
+          break;
+        }
+        __syncwarp();  // every lane has read what this overwrites
+        leave(first);
+        first = 0;
+        count = (n + (1 << log_group) - 1) >> log_group;
+        log_step = log_group;
       }
     }
     if (write) {

@@ -216,6 +216,7 @@ struct PagedAttnParams {
   float* part_o;           // partial results of cut units: [2 CTAs][4 heads][128]
   float2* part_ml;         // their (maximum, sum): [2 CTAs][4]
   int* counters;           // [B n_kv] pieces of a unit that have arrived (zero between calls)
+  int* group_counters;     // [2 CTAs] the same of a group of a unit's pieces
   int* status;
   int fault;               // test hook: the last worker issues no loads (its waits run out)
   float scale_log2;        // log2(e) / sqrt(128)
