@@ -467,8 +467,8 @@ void attn_paged_destroy(gqa_paged *paged);
  *
  * k, v    bf16: head g of token t of sequence b at b stride_b + t stride_t + 128 g (elements): rows of
  *         a fused projection, or a dense cache [B,S_max,n_kv,128] that attn_prefill has filled.
- *         Strides multiples of 8, stride_t at least 128 n_kv, both below 2^31; stride_b is not read for
- *         B = 1, nor stride_t for T = 1.  No row may overlap the pools.
+ *         Strides multiples of 8, at least 128 n_kv and below 2^31; stride_b is not read for B = 1, nor
+ *         stride_t for T = 1.  No row may overlap the pools.
  * rope    the rotation; NULL: keys are written as they are (already rotated).
  * rope_pos [B] int32: position of each sequence's first new token in its text; NULL: kv_len[b].
  * page_table [B,max_pages] int32; entries of pages that hold no new position are not read.
@@ -495,7 +495,8 @@ gqa_status attn_paged_append(gqa_ctx *ctx, const gqa_paged *paged, const void *k
  *         0 .. n_pages - 1 among those it reads: the sequence's h is NaN and attn_sync_status reports
  *         GQA_ERR_SHAPE.
  * h       [B,512 n_kv] bf16 output; must not overlap the inputs.
- * Limits as attn_paged_append; the scratch (at most 2 MB) is the context's and grows with the first call.
+ * Limits as attn_paged_append.  The scratch (at most 2 MB) is the context's: the first call on it may allocate, and then
+ * cannot be captured.
  */
 gqa_status attn_paged_decode_attention(gqa_ctx *ctx, const gqa_paged *paged, const void *q_r, int B,
                                        const int *page_table, int max_pages, const int *kv_len, void *h,
