@@ -191,7 +191,7 @@ def tables(lens, page, n_pages, seed=0, room=1):
 
 
 # ------------------------------------------------------------------------------- append
-@pytest.mark.parametrize("n_kv", [1, 2, 3, 8])
+@pytest.mark.parametrize("n_kv", [1, 2, 3, 5, 8])
 @pytest.mark.parametrize("page,heads_first,beside", [(8, False, False), (24, True, False), (64, False, True),
                                                      (256, True, True)])
 @pytest.mark.parametrize("e4m3,layout,rot,scaling", [(False, "pairs", 128, "plain"), (True, "halves", 128, "bands"),
