@@ -1,0 +1,81 @@
+"""GPU checks of the paged-cache operators at the ends of their ranges: scores of any size, scales at
+both ends of fp32, maxima that rise or stand alone, sums of very small weights, descriptions and
+outputs that overlap."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as po
+from tests import gpu_util as gu
+from tests.test_gpu_paged import Cache, attend, context, ints, query, reported, scrub, tables
+from transformer_gqa_attention_gb300 import abi
+
+pytestmark = pytest.mark.gpu
+DEV = gu.DEV
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from transformer_gqa_attention_gb300 import _build
+    _build.build()
+
+
+def code_of(x):
+    """e4m3 codes of numbers that e4m3 holds exactly."""
+    v = po.e4m3_values()
+    x = np.asarray(x, dtype=np.float64)
+    at = np.argsort(np.where(np.isnan(v), np.inf, v), kind="stable")[:254]
+    i = at[np.searchsorted(v[at], x)]
+    assert np.array_equal(v[i], x)
+    return i.astype(np.uint8)
+
+
+def put(c, i, pages, x):
+    """Positions 0 .. n - 1 of a sequence: x [n, n_kv, 128], exact in the pool's type."""
+    at = np.arange(len(x))
+    idx = torch.from_numpy(np.asarray(pages)[at // c.page].astype(np.int64)), torch.from_numpy(at % c.page)
+    rows = torch.from_numpy(code_of(x)) if c.e4m3 else torch.from_numpy(x).to(torch.bfloat16).view(torch.int16)
+    c.raw(i)[idx] = rows.to(DEV)
+
+
+# Queries 2^power times whole numbers up to 3 against keys of such numbers: products and sums of them are
+# whole numbers below 2^11 times 2^power, exact in fp32, and two scores that differ do so by 2^power / sqrt(128)
+# at least, so that from 2^13 on the weights are equal shares of the keys with the largest score and nothing
+# (e^-700) of the others.  Shares add up exactly; the sum of values rounds with 2^-24 of it for each term that is not
+# zero (at most 200 in these draws: 2^-16 together), the quotient and the scale with 2^-22, and h once with 2^-8.
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("power", [13, 22, 25, 30, 36, 60, 100])
+@pytest.mark.parametrize("lens", [[1, 17, 300], [20000]])
+def test_scores_of_any_size(lens, power, e4m3):
+    n_kv = 2
+    n_pages = sum(-(-n // 32) for n in lens)
+    c = Cache(n_pages, 32, n_kv, e4m3, seed=power)
+    for s in c.scales if e4m3 else ():
+        s.fill_(0.5)
+    t = tables(lens, 32, n_pages, seed=power)
+    rng = np.random.default_rng(power + len(lens))
+    keys = [rng.integers(-3, 4, (n, n_kv, 128)).astype(np.float64) for n in lens]
+    qs = rng.integers(-3, 4, (len(lens), n_kv, 4, 128)).astype(np.float64)
+    keys[-1][:, 0] = np.where(qs[-1, 0, 0] >= 0, -np.abs(keys[-1][:, 0]) - (keys[-1][:, 0] == 0),
+                              np.abs(keys[-1][:, 0]))  # one head whose scores are all negative
+    for b, k in enumerate(keys):
+        put(c, 0, t[b], k)
+    scrub(c, t, lens)
+    q = torch.from_numpy(qs * 2.0 ** power).reshape(len(lens), -1).to(torch.bfloat16).to(DEV)
+    h = attend(c, q, t, lens)
+    assert not reported(c.ctx)
+    vn = c.numbers(1)
+    for b, n in enumerate(lens):
+        got = gu.np64(h[b]).reshape(n_kv, 4, 128)
+        v = po.gather(vn, t[b], n)
+        e = np.einsum("ghd,sgd->ghs", qs[b], keys[b])
+        a = (e == e.max(-1, keepdims=True)).astype(np.float64)
+        assert a.sum(-1).max() <= 200
+        a /= a.sum(-1, keepdims=True)
+        ref, mean = np.einsum("ghs,sgd->ghd", a, v), np.einsum("ghs,sgd->ghd", a, np.abs(v))
+        assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -15 * mean), (b, n)

@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     float o[16][4];  // [set of eight columns]: rows r0 (0, 1) and r0 + 8 (2, 3: nothing)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m = -INFINITY, l = 0.f;  // l: of this lane's columns
+    float m = -INFINITY, l = 0.f;  // m: largest product q k, without the scale; l: of this lane's columns
 
     // One stage, whose first key is k0 of the piece; kTail: keys past the last one are left out.
     auto stage = [&](auto tail, uint32_t k_addr, uint32_t v_addr, int last) {
@@ -472,9 +472,11 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         for (int n = 0; n < 2; ++n) mx = max3f(mx, sc[blk][n][0], sc[blk][n][1]);
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float m_new = fmaxf(m, mx * scale);
+      // The difference to the maximum first, then its scale: the largest weight is 2^kShift exactly, and no other is above
+      // it, however large the products (scaled one by one, two of 2^24 and more differ by what their rounding leaves).
+      const float m_new = fmaxf(m, mx);
       const float mu = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = fast_exp2(m - mu);
+      const float alpha = fast_exp2((m - mu) * scale);
       m = m_new;
       l *= alpha;
       uint32_t pa[kBlocks][2];
@@ -482,8 +484,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
       for (int blk = 0; blk < kBlocks; ++blk)
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float x = fast_exp2(fmaf(sc[blk][n][0], scale, PagedTile<E>::kShift - mu));
-          const float y = fast_exp2(fmaf(sc[blk][n][1], scale, PagedTile<E>::kShift - mu));
+          const float x = fast_exp2(fmaf(sc[blk][n][0] - mu, scale, PagedTile<E>::kShift));
+          const float y = fast_exp2(fmaf(sc[blk][n][1] - mu, scale, PagedTile<E>::kShift));
           l += x + y;
           if constexpr (k8) {
             const __half2 v = __floats2half2_rn(x, y);
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     if (live) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) PagedReader<E>::put(red_o + (warp * 4 + r0) * L::kRedRow, i, c2, o[2 * i], o[2 * i + 1]);
-      if ((lane & 3) == 0) red_ml[warp * 4 + r0] = make_float2(m, l);
+      if ((lane & 3) == 0) red_ml[warp * 4 + r0] = make_float2(m * scale, l);
     }
     // one decision for all 128 consumer threads
     if (!bar1_and_128(ok && !*abort_flag)) break;
