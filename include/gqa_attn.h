@@ -444,6 +444,7 @@ typedef struct gqa_paged gqa_paged; /* opaque */
  *         an extent of 1 is not read.
  * k_scale, v_scale  GQA_CACHE_E4M3: [n_kv] fp32 on the device, positive and normal: a key or value is the
  *         stored number times its head's scale (NULL: 1).  Read by every call that uses the pools.
+ *         A key scale that is negative, infinite or NaN makes its heads' results NaN.
  *         NULL for bf16.
  * Requires n_pages >= 1, page_size a multiple of 8 in 8 .. 1048576, strides below 2^39 bytes
  * and pools that span at most 2^46 elements.

@@ -79,3 +79,15 @@ def test_scores_of_any_size(lens, power, e4m3):
         a /= a.sum(-1, keepdims=True)
         ref, mean = np.einsum("ghs,sgd->ghd", a, v), np.einsum("ghs,sgd->ghd", a, np.abs(v))
         assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -15 * mean), (b, n)
+
+
+@pytest.mark.parametrize("broken", [NAN, math.inf, -0.01])
+def test_a_broken_key_scale_shows(broken):
+    c = Cache(8, 32, 4, True, seed=30)
+    t, lens = np.arange(8, dtype=np.int32).reshape(2, 4), [100, 128]
+    scrub(c, t, lens)
+    c.scales[0][1] = broken
+    h = attend(c, query(2, 4), t, lens)
+    assert not reported(c.ctx)
+    odd = torch.isnan(h[:2]).cpu().view(2, 4, 512)
+    assert odd[:, 1].all() and not odd[:, [0, 2, 3]].any()
