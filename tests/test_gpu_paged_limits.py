@@ -9,7 +9,7 @@ import torch
 
 from oracle import paged_oracle as po
 from tests import gpu_util as gu
-from tests.test_gpu_paged import Cache, attend, context, ints, query, reported, scrub, tables
+from tests.test_gpu_paged import Cache, attend, check, context, ints, query, reported, scrub, tables
 from transformer_gqa_attention_gb300 import abi
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +91,15 @@ def test_a_broken_key_scale_shows(broken):
     assert not reported(c.ctx)
     odd = torch.isnan(h[:2]).cpu().view(2, 4, 512)
     assert odd[:, 1].all() and not odd[:, [0, 2, 3]].any()
+
+
+def test_keys_of_zeros_under_scales_that_overflow():
+    """Scores of exactly 0 where query times scale passes fp32: the mean of the values."""
+    c = Cache(8, 32, 2, True, seed=31)
+    t, lens = np.arange(8, dtype=np.int32).reshape(2, 4), [100, 37]
+    c.raw(0).zero_()
+    scrub(c, t, lens)
+    c.scales[0].fill_(1e30)
+    h = attend(c, query(2, 2, size=1e30), t, lens)
+    assert not reported(c.ctx)
+    check(c, query(2, 2, size=0.0), t, lens, h)

@@ -408,9 +408,10 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         top = min(max(top, 1u << 23), 253u << 23);             // exponent field e
         const float down = __uint_as_float((254u << 23) - top);  // 2^(127 - e)
-        // (a row of zeros or tiny numbers: not a scale of 0, which a key that is left out, -inf, would make NaN)
-        // A k_scale that is no number from 0 on, or infinite, shows in the result.
-        scale = scale >= 0.f && scale < INFINITY ? fmaxf(scale * __uint_as_float(top), 0x1p-126f) : __int_as_float(0x7fc00000);
+        // Kept from 0, which a key that is left out, -inf, would make NaN (a row of zeros or tiny numbers), and from infinity,
+        // which would make NaN of products that are 0.  A k_scale that is no number from 0 on, or infinite, shows in the result.
+        scale = scale >= 0.f && scale < INFINITY ? fminf(fmaxf(scale * __uint_as_float(top), 0x1p-126f), 0x1.fffffep127f)
+                                                 : __int_as_float(0x7fc00000);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
