@@ -103,3 +103,22 @@ def test_keys_of_zeros_under_scales_that_overflow():
     h = attend(c, query(2, 2, size=1e30), t, lens)
     assert not reported(c.ctx)
     check(c, query(2, 2, size=0.0), t, lens, h)
+
+
+def test_values_of_tiny_scales():
+    c = Cache(80, 64, 2, True, seed=32)
+    lens = [5000, 37]
+    t = tables(lens, 64, 80)
+    scrub(c, t, lens)
+    q = query(2, 2)
+    for scale in (1e-30, 1e-34, 1e-36, 2.0 ** -126):
+        c.scales[1].fill_(scale)
+        h = attend(c, q, t, lens)
+        assert not reported(c.ctx)
+        vn = c.numbers(1)
+        for b, n in enumerate(lens):
+            ref, mean, mag = po.decode(gu.np64(q[b]).reshape(2, 4, 128), po.gather(c.numbers(0), t[b], n), po.gather(vn, t[b], n))
+            d = 2 * 2.0 ** -17 * 1.02 * mag / math.sqrt(128) + 2.0 ** -20
+            # 2^-134: half of bf16's smallest step
+            tol = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * (2.0 ** -11 + d) * mean + 2.0 ** -133
+            assert np.all(np.abs(gu.np64(h[b]).reshape(2, 4, 128) - ref) <= tol), (scale, b)

@@ -695,15 +695,15 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
       }
     }
     if (write) {
-      float inv = v_scale / Ls;
-      if (end == 0) inv = 0.f;
+      float inv = 1.f / Ls, out = v_scale;  // (one after the other: v_scale / Ls may be too small for fp32)
+      if (end == 0) inv = out = 0.f;
       if (end < 0) {
         inv = __int_as_float(0x7fc00000);
         if (threadIdx.x == 0) atomicOr(p.status, kDevErrRange);
       }
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.h) +
                                 (static_cast<size_t>(w.b) * p.n_kv * 4 + g * 4 + warp) * 128 + d0) =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          make_uint2(pack_bf16x2(acc.x * inv * out, acc.y * inv * out), pack_bf16x2(acc.z * inv * out, acc.w * inv * out));
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");  // the results' room is free for the next piece
   }
