@@ -440,8 +440,9 @@ typedef struct gqa_paged gqa_paged; /* opaque */
  *
  * k_pages, v_pages  the pools, owned by the caller; they must outlive the description.
  * dtype   GQA_CACHE_BF16 or GQA_CACHE_E4M3.
- * strides multiples of 16 bytes, and such that no two rows of 128 elements overlap; the stride of
- *         an extent of 1 is not read.
+ * strides multiples of 16 bytes, and each at least what all smaller ones reach together with the row of 128
+ *         elements, so that no two rows overlap; the stride of an extent of 1 is not read.  No key's row may
+ *         overlap a value's (the pools may lie in one another's gaps).
  * k_scale, v_scale  GQA_CACHE_E4M3: [n_kv] fp32 on the device, positive and normal: a key or value is the
  *         stored number times its head's scale (NULL: 1).  Read by every call that uses the pools.
  *         A key scale that is negative, infinite or NaN makes its heads' results NaN.

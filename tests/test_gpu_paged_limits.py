@@ -122,3 +122,34 @@ def test_values_of_tiny_scales():
             # 2^-134: half of bf16's smallest step
             tol = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * (2.0 ** -11 + d) * mean + 2.0 ** -133
             assert np.all(np.abs(gu.np64(h[b]).reshape(2, 4, 128) - ref) <= tol), (scale, b)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n_pages,page,n_kv,order,gaps", [
+    (3, 8, 2, (2, 0, 1), (0, 0, 0)), (3, 8, 2, (0, 2, 1), (0, 128, 0)), (3, 8, 2, (1, 0, 2), (64, 0, 256)),
+    (1, 8, 2, (0, 1, 2), (0, 256, 0)), (2, 16, 1, (1, 2, 0), (128, 0, 16)), (4, 8, 3, (0, 1, 2), (128, 0, 384))])
+def test_keys_and_values_that_overlap_are_refused(n_pages, page, n_kv, order, gaps, e4m3):
+    """Every distance of the two pools against their rows' elements one by one (host only).  order: extents (pages, slots,
+    heads) from the narrowest stride on, with `gaps` elements left behind each of them."""
+    extent, stride, at = (n_pages, page, n_kv), [0, 0, 0], 128
+    for i, gap in zip(order, gaps):
+        stride[i] = at + gap
+        at = stride[i] * extent[i]
+    grid = [np.arange(n) * s for n, s in zip(extent, stride)]
+    rows = (grid[0][:, None, None] + grid[1][:, None] + grid[2]).reshape(-1)
+    held = np.zeros(3 * at + 1024, dtype=bool)
+    held[(rows[:, None] + np.arange(128)).reshape(-1) + at + 512] = True
+    size = 1 if e4m3 else 2
+    memory = torch.zeros((3 * at + 1024) * size, dtype=torch.uint8, device=DEV)
+    base = memory.data_ptr() + (at + 512) * size
+    ctx, answers = context(n_kv), set()
+    for d in range(-at - 256, at + 256, 16):
+        meets = bool(held[rows + at + 512 + d].any() or held[rows + at + 512 + d + 127].any())
+        try:
+            abi.attn_paged_destroy(abi.attn_paged_create(ctx, base, base + d * size, n_pages, page, "e4m3" if e4m3 else "bf16", *stride))
+            got = 0
+        except abi.GQAError as e:
+            got = e.status
+        assert got == (1 if meets else 0), d
+        answers.add(got)
+    assert answers == {0, 1}

@@ -59,6 +59,25 @@ double frequency(int rot_dim, int j, double theta, const gqa_rope_scaling& s) {
 // Elements from a row's start that rows 0 .. n - 1 of `stride` reach.
 size_t reach(long long n, long long stride) { return static_cast<size_t>(n - 1) * static_cast<size_t>(stride); }
 
+// An extent of a pool with more than one entry, in bytes; below: what the narrower extents reach, at most `stride`.
+struct Extent {
+  long long n, stride, below;
+};
+
+long long floor_div(long long x, long long y) { return x / y - (x % y < 0); }
+
+// Whether rows of `row` bytes of two pools with these extents (the narrowest first) meet, the second one's `d` bytes
+// behind the first one's: of each extent no more than two steps bring them within reach of one another.
+bool rows_meet(const Extent* e, int dims, long long row, long long d) {
+  if (dims == 0) return d > -row && d < row;
+  const Extent& w = e[dims - 1];
+  const long long first = std::max(floor_div(-w.below - d, w.stride) + 1, 1 - w.n);
+  const long long last = std::min(-floor_div(d - w.below, w.stride) - 1, w.n - 1);
+  for (long long k = first; k <= last; ++k)
+    if (rows_meet(e, dims - 1, row, d + k * w.stride)) return true;
+  return false;
+}
+
 // A pool as the attention copies it: boxes of 2^log_box slots of one head and page, bf16 rows as two halves of
 // 64 elements.
 bool map_pool(CUtensorMap* m, const void* base, const gqa_paged* g) {
@@ -257,23 +276,24 @@ gqa_status attn_paged_create(gqa_ctx* c, void* k_pages, void* v_pages, int n_pag
   if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_scale) || !aligned16(v_scale)) return GQA_ERR_ALIGN;
   const int size = dtype == GQA_CACHE_BF16 ? 2 : 1;
   // dimensions with more than one entry, the narrowest stride first: each has to step over all of those before
-  struct Dim {
-    long long n, stride;
-  } dims[3];
+  Extent dims[3];
   int used = 0;
-  const Dim all[3] = {{n_pages, stride_page}, {page_size, stride_pos}, {c->n_kv, stride_head}};
-  for (const Dim& d : all)
+  const Extent all[3] = {{n_pages, stride_page, 0}, {page_size, stride_pos, 0}, {c->n_kv, stride_head, 0}};
+  for (const Extent& d : all)
     if (d.n > 1) {
       if (d.stride < 1 || d.stride >= (1LL << 39) / size || d.stride > (1LL << 46) / d.n) return GQA_ERR_SHAPE;
       if (d.stride * size % 16) return GQA_ERR_ALIGN;
-      dims[used++] = d;
+      dims[used++] = {d.n, d.stride * size, 0};
     }
-  std::sort(dims, dims + used, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
-  long long row = 128;
+  std::sort(dims, dims + used, [](const Extent& a, const Extent& b) { return a.stride < b.stride; });
+  long long reached = 128 * size;
   for (int i = 0; i < used; ++i) {
-    if (dims[i].stride < row) return GQA_ERR_INVALID_ARG;
-    row = dims[i].stride * (dims[i].n - 1) + row;
+    if (dims[i].stride < reached) return GQA_ERR_INVALID_ARG;
+    dims[i].below = reached;
+    reached += dims[i].stride * (dims[i].n - 1);
   }
+  if (rows_meet(dims, used, 128 * size, static_cast<long long>(reinterpret_cast<intptr_t>(v_pages) - reinterpret_cast<intptr_t>(k_pages))))
+    return GQA_ERR_INVALID_ARG;
   gqa_paged* g = new (std::nothrow) gqa_paged();
   if (!g) return GQA_ERR_OOM;
   g->device = c->device;
