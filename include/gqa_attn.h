@@ -496,7 +496,7 @@ gqa_status attn_paged_append(gqa_ctx *ctx, const gqa_paged *paged, const void *k
  * kv_len  [B] int32: 0 .. max_pages page_size (0: h is zero).  Out of range, or with a page outside
  *         0 .. n_pages - 1 among those it reads: the sequence's h is NaN and attn_sync_status reports
  *         GQA_ERR_SHAPE.
- * h       [B,512 n_kv] bf16 output; must not overlap the inputs.
+ * h       [B,512 n_kv] bf16 output; must not overlap the inputs, the pools' rows and scales among them.
  * Limits as attn_paged_append.  The scratch (at most 2 MB) is the context's: the first call on it may allocate, and then
  * cannot be captured.
  */

@@ -153,3 +153,43 @@ def test_keys_and_values_that_overlap_are_refused(n_pages, page, n_kv, order, ga
         assert got == (1 if meets else 0), d
         answers.add(got)
     assert answers == {0, 1}
+
+
+@pytest.mark.parametrize("e4m3,beside", [(False, True), (True, True), (False, False)])
+def test_heads_over_the_pools_are_refused(e4m3, beside):
+    """The output between pages of a pool with room between them, and on each row and scale of it."""
+    n_pages, page, n_kv, B = 3, 8, 2, 1
+    size, row, bytes_h = (1, 128, 2048) if e4m3 else (2, 256, 2048)
+    rows = page * n_kv * row                               # of a page's keys
+    room = 2 * rows + 3 * bytes_h                          # from page to page, where keys and values lie side by side
+    memory = torch.zeros(bytes_h + n_pages * room, dtype=torch.uint8, device=DEV)
+    k = memory.data_ptr() + bytes_h
+    v = k + (rows if beside else n_pages * rows)
+    strides = ((room if beside else rows) // size, n_kv * 128, 128)
+    scales = [torch.ones(512, device=DEV) for _ in range(2)] if e4m3 else [None, None]
+    ctx = context(n_kv)
+    p = abi.attn_paged_create(ctx, k, v, n_pages, page, "e4m3" if e4m3 else "bf16", *strides, *scales)
+    q = torch.zeros(B, n_kv * 512, dtype=torch.bfloat16, device=DEV)
+    t, lens = ints([[0, 1, 2]]), ints([20])
+
+    def status(h):
+        try:
+            abi.attn_paged_decode_attention(ctx, p, q, B, t, 3, lens, h)
+            return 0
+        except abi.GQAError as e:
+            return e.status
+    held = np.zeros(len(memory), dtype=bool)
+    for first in (k, v):
+        for n in range(n_pages):
+            at = first - memory.data_ptr() + n * strides[0] * size
+            held[at:at + rows] = True
+    free = 0
+    for at in range(0, len(memory) - bytes_h + 1, 16 if beside else 256):
+        want = 1 if held[at:at + bytes_h].any() else 0
+        assert status(memory.data_ptr() + at) == want, at
+        free += want == 0
+    assert free
+    for s in scales if e4m3 else ():
+        assert status(s) == 1 and status(s.data_ptr() - 2032) == 1
+    abi.attn_paged_destroy(p)
+    abi.attn_sync_status(ctx)

@@ -59,22 +59,41 @@ double frequency(int rot_dim, int j, double theta, const gqa_rope_scaling& s) {
 // Elements from a row's start that rows 0 .. n - 1 of `stride` reach.
 size_t reach(long long n, long long stride) { return static_cast<size_t>(n - 1) * static_cast<size_t>(stride); }
 
-// An extent of a pool with more than one entry, in bytes; below: what the narrower extents reach, at most `stride`.
-struct Extent {
-  long long n, stride, below;
-};
-
 long long floor_div(long long x, long long y) { return x / y - (x % y < 0); }
 
 // Whether rows of `row` bytes of two pools with these extents (the narrowest first) meet, the second one's `d` bytes
 // behind the first one's: of each extent no more than two steps bring them within reach of one another.
-bool rows_meet(const Extent* e, int dims, long long row, long long d) {
+bool rows_meet(const PagedExtent* e, int dims, long long row, long long d) {
   if (dims == 0) return d > -row && d < row;
-  const Extent& w = e[dims - 1];
+  const PagedExtent& w = e[dims - 1];
   const long long first = std::max(floor_div(-w.below - d, w.stride) + 1, 1 - w.n);
   const long long last = std::min(-floor_div(d - w.below, w.stride) - 1, w.n - 1);
   for (long long k = first; k <= last; ++k)
     if (rows_meet(e, dims - 1, row, d + k * w.stride)) return true;
+  return false;
+}
+
+// Whether bytes lo .. hi - 1 from a pool's start on hold some of a row: of three steps of an extent that they touch, the
+// middle one lies whole within them.
+bool rows_touch(const PagedExtent* e, int dims, long long row, long long lo, long long hi) {
+  if (dims == 0) return lo < row && hi > 0;
+  const PagedExtent& w = e[dims - 1];
+  const long long first = std::max(floor_div(lo - w.below, w.stride) + 1, 0LL);
+  const long long last = std::min(-floor_div(-hi, w.stride) - 1, w.n - 1);
+  if (last - first >= 2) return true;
+  for (long long i = first; i <= last; ++i)
+    if (rows_touch(e, dims - 1, row, lo - i * w.stride, hi - i * w.stride)) return true;
+  return false;
+}
+// Whether `bytes` at p hold some of what a description's calls read: rows of either pool, or scales.
+bool holds_some(const gqa_paged* g, const void* p, size_t bytes) {
+  const long long row = g->dtype == GQA_CACHE_BF16 ? 256 : 128;
+  for (const void* pool : {g->pool.k, g->pool.v}) {
+    const long long lo = static_cast<long long>(reinterpret_cast<intptr_t>(p) - reinterpret_cast<intptr_t>(pool));
+    if (rows_touch(g->extents, g->n_extents, row, lo, lo + static_cast<long long>(bytes))) return true;
+  }
+  for (const float* scales : {g->pool.k_scale, g->pool.v_scale})
+    if (scales && overlap(p, bytes, scales, 4 * static_cast<size_t>(g->n_kv))) return true;
   return false;
 }
 
@@ -276,16 +295,16 @@ gqa_status attn_paged_create(gqa_ctx* c, void* k_pages, void* v_pages, int n_pag
   if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_scale) || !aligned16(v_scale)) return GQA_ERR_ALIGN;
   const int size = dtype == GQA_CACHE_BF16 ? 2 : 1;
   // dimensions with more than one entry, the narrowest stride first: each has to step over all of those before
-  Extent dims[3];
+  PagedExtent dims[3]{};
   int used = 0;
-  const Extent all[3] = {{n_pages, stride_page, 0}, {page_size, stride_pos, 0}, {c->n_kv, stride_head, 0}};
-  for (const Extent& d : all)
+  const PagedExtent all[3] = {{n_pages, stride_page, 0}, {page_size, stride_pos, 0}, {c->n_kv, stride_head, 0}};
+  for (const PagedExtent& d : all)
     if (d.n > 1) {
       if (d.stride < 1 || d.stride >= (1LL << 39) / size || d.stride > (1LL << 46) / d.n) return GQA_ERR_SHAPE;
       if (d.stride * size % 16) return GQA_ERR_ALIGN;
       dims[used++] = {d.n, d.stride * size, 0};
     }
-  std::sort(dims, dims + used, [](const Extent& a, const Extent& b) { return a.stride < b.stride; });
+  std::sort(dims, dims + used, [](const PagedExtent& a, const PagedExtent& b) { return a.stride < b.stride; });
   long long reached = 128 * size;
   for (int i = 0; i < used; ++i) {
     if (dims[i].stride < reached) return GQA_ERR_INVALID_ARG;
@@ -308,6 +327,8 @@ gqa_status attn_paged_create(gqa_ctx* c, void* k_pages, void* v_pages, int n_pag
              v_pages,
              k_scale,
              v_scale};
+  g->n_extents = used;
+  std::copy(dims, dims + 3, g->extents);
   for (g->log_box = 3; g->log_box < 6 && page_size % (2 << g->log_box) == 0;) ++g->log_box;
   if (!map_pool(&g->map_k, k_pages, g) || !map_pool(&g->map_v, v_pages, g)) {
     delete g;
@@ -368,7 +389,7 @@ gqa_status attn_paged_decode_attention(gqa_ctx* c, const gqa_paged* g, const voi
   if ((st = check_paged(c, g, max_pages)) != GQA_OK) return st;
   const size_t heads = static_cast<size_t>(B) * c->n_kv * 1024;
   if (overlap(h, heads, q_r, heads) || overlap(h, heads, kv_len, 4 * static_cast<size_t>(B)) ||
-      overlap(h, heads, page_table, 4 * static_cast<size_t>(B) * max_pages))
+      overlap(h, heads, page_table, 4 * static_cast<size_t>(B) * max_pages) || holds_some(g, h, heads))
     return GQA_ERR_INVALID_ARG;
   CallRange range("gqa.attn_paged_decode_attention");
   return run_paged_attn(c, g, q_r, B, page_table, max_pages, kv_len, 0, h, reinterpret_cast<cudaStream_t>(stream));

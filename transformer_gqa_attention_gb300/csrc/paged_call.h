@@ -9,9 +9,20 @@
 #include "gqa_attn.h"
 #include "params.h"
 
+namespace gqa {
+
+// An extent of a pool with more than one entry, in bytes; below: what the narrower extents reach, at most `stride`.
+struct PagedExtent {
+  long long n, stride, below;
+};
+
+}  // namespace gqa
+
 struct gqa_paged {
   int device, n_kv, dtype;
   gqa::PagedPool pool;
+  int n_extents;
+  gqa::PagedExtent extents[3];  // the narrowest first
   int log_box;             // slots of the maps' boxes: a power of two, at most 64, that divides the page
   CUtensorMap map_k, map_v;
 };
