@@ -193,3 +193,105 @@ def test_heads_over_the_pools_are_refused(e4m3, beside):
         assert status(s) == 1 and status(s.data_ptr() - 2032) == 1
     abi.attn_paged_destroy(p)
     abi.attn_sync_status(ctx)
+
+
+# ------------------------------------------------------------------------------- weights of every size
+def held(c, t, b, n):
+    return [po.gather(c.numbers(i), t[b], n) for i in range(2)]
+
+
+def check_weights(c, q, k, v, h):
+    """One sequence.  As `check` of the paged operators, but with e4m3 pages the weights enter the product as fp16
+    of 2^15 times them: 2^-11 of the value at most, and 2^-40 of the largest weight for those below 2^-29 of it."""
+    ref, mean, mag = po.decode(gu.np64(q).reshape(c.n_kv, 4, 128), k, v)
+    w = 2.0 ** -11 if c.e4m3 else 2.0 ** -8
+    d = 2 * 2.0 ** -17 * 1.02 * mag / math.sqrt(128) + 2.0 ** -20
+    small = len(k) * 2.0 ** -40 * np.abs(v).max() if c.e4m3 else 0.0
+    got = gu.np64(h).reshape(c.n_kv, 4, 128)
+    assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * (w + d) * mean + small)
+    return ref
+
+
+@pytest.mark.parametrize("lens", [[1, 90, 700], [9000], [(b * 977) % 3000 for b in range(24)]])
+def test_e4m3_weights_keep_eleven_bits(lens):
+    n_pages = sum(-(-n // 32) for n in lens) + 2
+    c = Cache(n_pages, 32, 4, True, seed=40)
+    t = tables(lens, 32, n_pages, seed=40)
+    scrub(c, t, lens)
+    q = query(len(lens), 4)
+    h = attend(c, q, t, lens)
+    assert not reported(c.ctx)
+    for b, n in enumerate(lens):
+        if n:
+            check_weights(c, q[b], *held(c, t, b, n), h[b])
+
+
+@pytest.mark.parametrize("n", [640, 5120])
+@pytest.mark.parametrize("falling", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_scores_that_rise_or_fall_with_the_position(e4m3, falling, n):
+    """Key s a multiple of the queries that grows (shrinks) with s up to a score near 40: a new maximum in every stage."""
+    c = Cache(n // 64, 64, 1, e4m3, seed=41)
+    if e4m3:
+        c.scales[0].fill_(0.2)
+    t = np.random.default_rng(n).permutation(n // 64).astype(np.int32)[None]
+    q = query(1, 1)
+    q[0] = q[0, :128].repeat(4)
+    ramp = np.linspace(1.0, 0.0, n) if falling else np.linspace(0.0, 1.0, n)
+    k = torch.from_numpy(ramp[:, None] * gu.np64(q[0, :128]) * (8.0 if e4m3 else 1.6))
+    rows = k.to(torch.float8_e4m3fn).view(torch.uint8) if e4m3 else k.to(torch.bfloat16).view(torch.int16)
+    at = np.arange(n)
+    c.raw(0)[torch.from_numpy(t[0, at // 64].astype(np.int64)), torch.from_numpy(at % 64)] = rows[:, None].to(DEV)
+    h = attend(c, q, t, [n])
+    assert not reported(c.ctx)
+    check_weights(c, q[0], *held(c, t, 0, n), h[0])
+
+
+@pytest.mark.parametrize("at", [2, 3000, -1])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_one_key_far_above_the_others(e4m3, at):
+    """In the first tile, in the middle and as the last key: nearly all of the weight of one head."""
+    n, n_kv = 5000, 2
+    c = Cache(80, 64, n_kv, e4m3, seed=42)
+    if e4m3:
+        c.scales[0].fill_(0.1)
+    t = np.random.default_rng(42).permutation(80).astype(np.int32)[None]
+    rng = np.random.default_rng(43)
+    q = query(1, n_kv)
+    k = rng.integers(-3, 4, (n, n_kv, 128)).astype(np.float64)
+    q0 = gu.np64(q[0]).reshape(n_kv, 4, 128)[:, 0]
+    k[at] = np.clip(np.round(q0), -6, 6) * 8
+    if not e4m3:
+        k = k / 8
+    put(c, 0, t[0], k)
+    scrub(c, t, [n])
+    h = attend(c, q, t, [n])
+    assert not reported(c.ctx)
+    kn, vn = held(c, t, 0, n)
+    ref = check_weights(c, q[0], kn, vn, h[0])
+    assert np.abs(ref[:, 0] - vn[at]).max() < 0.05 * np.abs(vn).max()
+
+
+def test_many_small_weights_beside_a_large_one():
+    """400000 e4m3 keys of 2^-26 of the largest weight, whose values alone make the result."""
+    n, page = 400001, 64
+    n_pages = -(-n // page)
+    c = Cache(n_pages, page, 1, True, seed=44)
+    t = np.random.default_rng(44).permutation(n_pages).astype(np.int32)[None]
+    c.raw(0).zero_()
+    c.raw(1).fill_(int(code_of([1.0])[0]))
+    c.scales[0].fill_(1.0)
+    c.scales[1].fill_(1.0)
+    q = torch.zeros(1, 512, dtype=torch.bfloat16, device=DEV)
+    q[0, ::128] = 26 * math.log(2.0) * math.sqrt(128.0) / 448
+    first = int(t[0, 0])
+    c.raw(0)[first, 0, 0, 0] = int(code_of([448.0])[0])
+    c.raw(1)[first, 0] = 0
+    h = attend(c, q, t, [n])
+    assert not reported(c.ctx)
+    e = float(q[0, 0]) * 448 / math.sqrt(128.0)
+    ref = (n - 1) / (n - 1 + math.exp(e))
+    assert 0.004 < ref < 0.008
+    # sums of n equal terms in fp32 in at most 32 parts a CTA: 2^-24 of them for each of the 100 terms of a lane in a row
+    # of tiles, under 2^-12 in all; the score 26 to 2^-20; the weights 2^-11; h 2^-8
+    assert np.all(np.abs(gu.np64(h[0]) - ref) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12 + 2.0 ** -15) * ref)
