@@ -3,8 +3,9 @@
 //
 // A pair turns by position x turns / 2^64 revolutions (gqa_rope).  The product is taken modulo 2^64, that is,
 // modulo one revolution, exactly, so the angle that is left has the frequency's own error times the
-// position (2^-53 relative: 1e-10 of a radian at a million) and no error of its size; sine and cosine then
-// take the nearest fp32 to it in half revolutions (2^-25 of half a revolution at most).
+// position and no error of its size.  A frequency is a power and a few products in 64 bits, at most 1 radian per position:
+// off by 2^-51 of a radian at most (4e-10 of one at a million positions).  Sine and cosine then take the nearest fp32 to
+// the angle in half revolutions (2^-25 of half a revolution at most).
 #pragma once
 
 #include <cuda_bf16.h>
