@@ -408,7 +408,7 @@ gqa_status attn_rope_init(gqa_rope *rope, int layout, int rot_dim, double theta,
  *         may be given as they are.
  * positions [n_tok] int32, any value (a negative one turns backwards).
  * out     bf16, the same form with its own stride; x itself with the same stride rotates in
- *         place, otherwise it must not overlap x.
+ *         place, otherwise its memory from the first to the last row must not overlap x's.
  * Requires 1 <= n_tok <= 262144, 1 <= n_heads <= 1024, both strides multiples of 8 and at least
  * 128 n_heads (and below 2^31).
  */
@@ -470,7 +470,8 @@ void attn_paged_destroy(gqa_paged *paged);
  * k, v    bf16: head g of token t of sequence b at b stride_b + t stride_t + 128 g (elements): rows of
  *         a fused projection, or a dense cache [B,S_max,n_kv,128] that attn_prefill has filled.
  *         Strides multiples of 8, at least 128 n_kv and below 2^31; stride_b is not read for B = 1, nor
- *         stride_t for T = 1.  No row may overlap the pools.
+ *         stride_t for T = 1.  From their first to their last row they must not overlap the memory from a
+ *         pool's first to its last row.
  * rope    the rotation; NULL: keys are written as they are (already rotated).
  * rope_pos [B] int32: position of each sequence's first new token in its text; NULL: kv_len[b].
  * page_table [B,max_pages] int32; entries of pages that hold no new position are not read.

@@ -4,7 +4,8 @@
 // All of it reads and writes every element once, and that bounds it: 8192 tokens of 32 heads (134 MB) are rotated in 22.1 us,
 // 6.1 TB/s; 4 x 8192 tokens (268 MB) appended in 41.4 us, 6.5 TB/s (the copy rate).  What else costs is the chain of round
 // trips of a warp that lives for one token (lengths; page, keys and values; stores) and its some 800 instructions: with
-// e4m3 pages, half the bytes to write, 8 prompts of up to 2048 tokens (53 MB) take 12.5 us of which 2.2 are a launch.
+// e4m3 pages, half the bytes to write, 8 prompts of up to 2048 tokens (53 MB) take 12.5 us of which 2.2 are a launch.  There
+// are warps for all B T rows: 47 % of those prompts' have no new token, read two lengths and leave.
 // CTAs of 128 threads: those of 256 take 13.1, of 512 15.8.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -26,7 +27,9 @@ __device__ __forceinline__ uint4 ld16(const void* p) { return ld_behind_wait(sta
 // ------------------------------------------------------------------------------ rotation
 // grid (ceil(n_tok / kWarps), groups of heads_each heads); a warp per token and group: eight threads
 // per head, kAhead times four heads at a time, whose angles are the same.  The first heads are loaded
-// while sine and cosine are computed (kAhead 1, 2, 4: 8192 tokens of 32 heads 27.1, 22.2, 22.7 us).
+// while sine and cosine are computed (kAhead 1, 2, 4: 8192 tokens of 32 heads 27.1, 22.2, 22.7 us).  kAhead 1 is for
+// warps of at most four heads: a few tokens, and any number of tokens that have no more (of one head 8 lanes
+// of a warp's 32 have work, and each computes its eight sines and cosines itself).
 template <int kAhead>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) rope_apply_kernel(const __grid_constant__ RopeParams p) {
   griddep_launch_dependents();
@@ -67,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) rope_apply_kernel(c
   }
 }
 
-// Heads of a warp: all of a token's where that gives the GPU 16 warps an SM, else a share of them, 4 at least (the
+// Heads of a warp: all of a token's where that gives the GPU's 152 SMs 16 warps each, else a share of them, 4 at least (the
 // queries of 64 tokens, 2.2 us; all 32 heads in one warp: 4.6, eight round trips one after the other).
 cudaError_t launch_rope_apply(const RopeParams& q, cudaStream_t s) {
   constexpr int kEnough = 2432;
