@@ -31,7 +31,8 @@
 // more at their ends than they gained (up to 2.5 % on the largest call, 10 to 40 % lost on the others).
 //
 // bf16: weights enter the product with V as bf16, as in the dense cache's attention (2^-8 of each; their sum is
-// taken before that): h is off by 0.0016 to 0.0020 in the 2-norm, where rounding it alone gives 0.0016 to 0.0017.
+// taken before that): h is off by 0.0016 to 0.0020 in the 2-norm, where rounding it alone gives 0.0016 to 0.0017
+// (a million keys of like weight: 0.0023).
 // e4m3: numbers become fp16, which holds all of them, NaN included (bf16 would as well, but there is no
 // instruction to it).  The queries are brought to fp16 with the exponent of their row's largest element taken
 // out (exact down to 2^-14 of it, to 2^-25 of it below), which goes into the scale of the scores with k_scale;
