@@ -93,6 +93,20 @@ def test_a_broken_key_scale_shows(broken):
     assert odd[:, 1].all() and not odd[:, [0, 2, 3]].any()
 
 
+@pytest.mark.parametrize("scale", [NAN, math.inf, -0.01, 0.0])
+def test_an_empty_sequence_is_zero_whatever_the_scales(scale):
+    c = Cache(8, 32, 4, True, seed=33)
+    t, lens = np.arange(8, dtype=np.int32).reshape(2, 4), [0, 60]
+    scrub(c, t, lens)
+    for s in c.scales:
+        s[2] = scale
+    q = query(2, 4)
+    h = attend(c, q, t, lens)
+    assert not reported(c.ctx)
+    assert (h[0] == 0).all()
+    assert torch.isfinite(h[1].view(4, 512)[[0, 1, 3]]).all()
+
+
 def test_keys_of_zeros_under_scales_that_overflow():
     """Scores of exactly 0 where query times scale passes fp32: the mean of the values."""
     c = Cache(8, 32, 2, True, seed=31)

@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     if (live) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) PagedReader<E>::put(red_o + (warp * 4 + r0) * L::kRedRow, i, c2, o[2 * i], o[2 * i + 1]);
-      if ((lane & 3) == 0) red_ml[warp * 4 + r0] = make_float2(m * scale, l);
+      if ((lane & 3) == 0) red_ml[warp * 4 + r0] = make_float2(m == -INFINITY ? m : m * scale, l);  // (no key, no scale)
     }
     // one decision for all 128 consumer threads
     if (!bar1_and_128(ok && !*abort_flag)) break;
